@@ -11,6 +11,7 @@ the HIP runtime torch already loaded (one runtime per process).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -35,11 +36,18 @@ SV_DTYPE_BF16 = 1
 SV_FLAG_BAD_BUDGET = 0x1
 SV_FLAG_BAD_TOKEN = 0x2
 SV_FLAG_SYNC_TIMEOUT = 0x4
+SV_FLAG_BAD_LENGTH = 0x8
+SV_FLAG_BAD_PAGE = 0x10
 
 SV_MAX_BATCH = 16384
 SV_MAX_K = 32
 SV_MAX_VOCAB = 1 << 20
 SV_NOALLOC_SCRATCH_BYTES = 16 << 20
+SV_MAX_HEADS = 256
+SV_MAX_PAGE = 4096
+SV_MAX_CONTEXT = 1 << 24
+SV_MAX_HIDDEN = 65536
+SV_MAX_STRIDE = 2147483647
 
 EXPORTED = (
     "spec_verify_init",
@@ -58,6 +66,13 @@ EXPORTED = (
     "spec_verify_hidden_workspace_bytes",
     "spec_markov_draft",
     "spec_markov_draft_workspace_bytes",
+    "spec_verify_cache_bytes",
+    "spec_verify_cache_write",
+    "spec_verify_cache_read",
+    "spec_verify_attention",
+    "spec_verify_attention_workspace_bytes",
+    "spec_head_quantize",
+    "spec_head_logits",
     "spec_verify_free",
     "spec_verify_strerror",
     "spec_verify_chunks",
@@ -113,6 +128,24 @@ def _declare(lib):
     lib.spec_markov_draft_workspace_bytes.restype = ctypes.c_size_t
     lib.spec_budget_schedule.argtypes = [_vp, _i, _i, _i, ctypes.c_float, _vp, _vp]
     lib.spec_budget_schedule.restype = _i
+    lib.spec_verify_cache_bytes.argtypes = [_i, _i, _i, _i]
+    lib.spec_verify_cache_bytes.restype = ctypes.c_size_t
+    lib.spec_verify_cache_write.argtypes = [_vp, _vp, _i, ctypes.c_int64, ctypes.c_int64, _vp,
+                                            _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]
+    lib.spec_verify_cache_write.restype = _i
+    lib.spec_verify_cache_read.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
+                                           _vp, _vp, _vp, _vp]
+    lib.spec_verify_cache_read.restype = _i
+    lib.spec_verify_attention.argtypes = [_vp, ctypes.c_int64, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
+                                          _i, _i, _i, _i, ctypes.c_float, _i, _vp, _vp, _vp,
+                                          ctypes.c_size_t, _vp]
+    lib.spec_verify_attention.restype = _i
+    lib.spec_verify_attention_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i, _i]
+    lib.spec_verify_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.spec_head_quantize.argtypes = [_vp, _i, _i, _i, _i, _vp, _vp, _vp]
+    lib.spec_head_quantize.restype = _i
+    lib.spec_head_logits.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp]
+    lib.spec_head_logits.restype = _i
     lib.spec_verify_timing.argtypes = [_vp, _i]
     lib.spec_verify_timing.restype = _i
     lib.spec_verify_timing_read.argtypes = [_vp, ctypes.POINTER(_i), ctypes.POINTER(ctypes.c_double)]
@@ -576,3 +609,275 @@ class MarkovDraft:
                                self.workspace.data_ptr(), self.workspace.numel(), s)
         _check(rc, "spec_markov_draft")
         return out_logits, out_tokens, status
+
+
+# ---- the paged 4-bit cache and the 8-bit head --------------------------------------
+
+def spec_verify_cache_bytes(num_pages: int, kv_heads: int, head_dim: int, page_size: int) -> int:
+    return int(load().spec_verify_cache_bytes(int(num_pages), int(kv_heads), int(head_dim),
+                                              int(page_size)))
+
+
+def spec_verify_cache_write(keys, values, dtype, key_stride, value_stride, page_table, ctx_lens,
+                            budgets, B, T, kv_heads, head_dim, page_size, max_pages, num_pages,
+                            cache, out_status, stream) -> int:
+    return load().spec_verify_cache_write(keys, values, dtype, key_stride, value_stride,
+                                          page_table, ctx_lens, budgets, B, T, kv_heads, head_dim,
+                                          page_size, max_pages, num_pages, cache, out_status,
+                                          stream)
+
+
+def spec_verify_cache_read(cache, page_table, starts, lens, B, T, kv_heads, head_dim, page_size,
+                           max_pages, num_pages, dtype, out_keys, out_values, out_status,
+                           stream) -> int:
+    return load().spec_verify_cache_read(cache, page_table, starts, lens, B, T, kv_heads,
+                                         head_dim, page_size, max_pages, num_pages, dtype,
+                                         out_keys, out_values, out_status, stream)
+
+
+def spec_verify_attention(queries, query_stride, cache, page_table, ctx_lens, budgets, B, K,
+                          q_heads, kv_heads, head_dim, page_size, max_pages, num_pages, scale,
+                          window, out, out_status, workspace, workspace_bytes, stream) -> int:
+    return load().spec_verify_attention(queries, query_stride, cache, page_table, ctx_lens,
+                                        budgets, B, K, q_heads, kv_heads, head_dim, page_size,
+                                        max_pages, num_pages, scale, window, out, out_status,
+                                        workspace, workspace_bytes, stream)
+
+
+def spec_verify_attention_workspace_bytes(B: int, K: int, q_heads: int, kv_heads: int,
+                                          head_dim: int, page_size: int, max_pages: int,
+                                          window: int = 0) -> int:
+    return int(load().spec_verify_attention_workspace_bytes(
+        int(B), int(K), int(q_heads), int(kv_heads), int(head_dim), int(page_size),
+        int(max_pages), int(window)))
+
+
+def spec_head_quantize(src, dtype, rows, H, block_rows, out_codes, out_scales, stream) -> int:
+    return load().spec_head_quantize(src, dtype, rows, H, block_rows, out_codes, out_scales, stream)
+
+
+def spec_head_logits(h_codes, h_scales, w_codes, w_scales, R, H, V, dtype, out, stream) -> int:
+    return load().spec_head_logits(h_codes, h_scales, w_codes, w_scales, R, H, V, dtype, out,
+                                   stream)
+
+
+@contextlib.contextmanager
+def _enqueue(device, stream):
+    """Makes ``device`` current and yields the stream's handle. Tensors that
+    torch allocates inside belong to ``stream``, so that one freed when the
+    call returns is not handed out again before the stream is done with it."""
+    if stream is None:
+        if device.index is None or device.index == torch.cuda.current_device():
+            yield _stream_handle(device)
+        else:
+            with torch.cuda.device(device):
+                yield _stream_handle(device)
+    else:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def _need(t, name, dtype, shape, device):
+    """A contiguous tensor of exactly this type, shape and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _token_stride(t, name, device):
+    """Elements between tokens of a [B, T, heads, head_dim] tensor whose heads
+    are contiguous and whose requests follow each other."""
+    B, T, heads, dim = t.shape
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    sb, st, sh, sd = t.stride()
+    stride = st if T > 1 else sb if B > 1 else heads * dim
+    if ((dim > 1 and sd != 1) or (heads > 1 and sh != dim)
+            or (B > 1 and T > 1 and sb != T * stride) or stride < heads * dim):
+        raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens, got "
+                         f"strides {t.stride()}")
+    return stride
+
+
+class BlockCache:
+    """A target layer's paged 4-bit key/value cache on one device: writing
+    blocks (or prompts), reading tokens back, and the attention of drafted
+    blocks over it. Holds the pool (torch-allocated unless given: uint8
+    [num_pages, kv_heads, page_size / 32, 34 head_dim]); the page table and
+    the lengths are the caller's.
+
+    ``status`` (int32 [1] on the device, or None) collects SV_FLAG_* bits;
+    nothing clears it. Calls are enqueued on ``stream`` (default: the current
+    torch stream) and not waited for."""
+
+    def __init__(self, device, num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64,
+                 pool: torch.Tensor | None = None):
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("BlockCache needs a GPU device")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.device = device
+        self.num_pages, self.kv_heads = int(num_pages), int(kv_heads)
+        self.head_dim, self.page_size = int(head_dim), int(page_size)
+        if spec_verify_cache_bytes(num_pages, kv_heads, head_dim, page_size) == 0:
+            raise ValueError(f"bad cache geometry: {num_pages} pages of {page_size} tokens, "
+                             f"{kv_heads} heads of {head_dim}")
+        shape = (self.num_pages, self.kv_heads, self.page_size // 32, 34 * self.head_dim)
+        if pool is None:
+            pool = torch.zeros(shape, dtype=torch.uint8, device=device)
+        self._pool_ptr = _need(pool, "pool", torch.uint8, shape, device)
+        self.pool = pool
+
+    def _table(self, page_table, B):
+        if page_table.dim() != 2 or page_table.shape[0] != B or page_table.shape[1] < 1:
+            raise ValueError(f"page_table must be [{B}, max_pages], got {tuple(page_table.shape)}")
+        return (_need(page_table, "page_table", torch.int32, page_table.shape, self.device),
+                int(page_table.shape[1]))
+
+    def _ints(self, t, name, n):
+        return None if t is None else _need(t, name, torch.int32, (n,), self.device)
+
+    def write(self, keys, values, page_table, ctx_lens, budgets=None, status=None, stream=None):
+        """Quantise [B, T, kv_heads, head_dim] keys and values (float32 or
+        bfloat16; slices of a fused projection's rows are fine) into positions
+        ctx_lens[b] .. ctx_lens[b] + budgets[b] of every request."""
+        if keys.dim() != 4 or keys.shape[2:] != (self.kv_heads, self.head_dim):
+            raise ValueError(f"keys must be [B, T, {self.kv_heads}, {self.head_dim}]")
+        if values.shape != keys.shape or values.dtype != keys.dtype or keys.dtype not in _DTYPES:
+            raise ValueError("keys and values must share their shape and be float32 or bfloat16")
+        B, T = keys.shape[:2]
+        ks = _token_stride(keys, "keys", self.device)
+        vs = _token_stride(values, "values", self.device)
+        table, width = self._table(page_table, B)
+        ctx = _need(ctx_lens, "ctx_lens", torch.int32, (B,), self.device)
+        bud = self._ints(budgets, "budgets", B)
+        st = self._ints(status, "status", 1)
+        with _enqueue(self.device, stream) as s:
+            rc = spec_verify_cache_write(keys.data_ptr(), values.data_ptr(), _DTYPES[keys.dtype],
+                                         ks, vs, table, ctx, bud, B, T, self.kv_heads,
+                                         self.head_dim, self.page_size, width, self.num_pages,
+                                         self._pool_ptr, st, s)
+        _check(rc, "spec_verify_cache_write")
+
+    def read(self, page_table, starts, lens, length: int, dtype=torch.bfloat16, out=None,
+             status=None, stream=None):
+        """The keys and values [B, length, kv_heads, head_dim] of positions
+        starts[b] .. starts[b] + lens[b] - 1 (starts None: 0). Rows behind
+        lens[b] are left as ``out`` (a pair of tensors) holds them; fresh
+        outputs are zero there."""
+        B, T = int(lens.shape[0]), int(length)
+        shape = (B, T, self.kv_heads, self.head_dim)
+        table, width = self._table(page_table, B)
+        first = self._ints(starts, "starts", B)
+        n = _need(lens, "lens", torch.int32, (B,), self.device)
+        st = self._ints(status, "status", 1)
+        if out is not None:
+            dtype = out[0].dtype
+        if dtype not in _DTYPES:
+            raise ValueError(f"values are read as float32 or bfloat16, not {dtype}")
+        with _enqueue(self.device, stream) as s:
+            if out is None:
+                out = tuple(torch.zeros(shape, dtype=dtype, device=self.device) for _ in range(2))
+            ok = _need(out[0], "out keys", dtype, shape, self.device)
+            ov = _need(out[1], "out values", dtype, shape, self.device)
+            rc = spec_verify_cache_read(self._pool_ptr, table, first, n, B, T, self.kv_heads,
+                                        self.head_dim, self.page_size, width, self.num_pages,
+                                        _DTYPES[dtype], ok, ov, st, s)
+        _check(rc, "spec_verify_cache_read")
+        return out[0], out[1]
+
+    def attend(self, queries, page_table, ctx_lens, budgets=None, scale: float | None = None,
+               window: int = 0, out=None, status=None, stream=None):
+        """Attention of the blocks' rows, bfloat16 [B, K+1, q_heads, head_dim]
+        (a slice of a fused projection's rows is fine), over the cache, which
+        already holds the blocks' own tokens. ``scale`` None: head_dim ** -0.5.
+        Rows behind budgets[b] and empty slots are left as ``out`` holds them;
+        a fresh output is zero there."""
+        if queries.dim() != 4 or queries.dtype != torch.bfloat16 \
+                or queries.shape[3] != self.head_dim or queries.shape[1] < 1:
+            raise ValueError(f"queries must be bfloat16 [B, K+1, q_heads, {self.head_dim}]")
+        B, T, heads, dim = queries.shape
+        stride = _token_stride(queries, "queries", self.device)
+        table, width = self._table(page_table, B)
+        ctx = _need(ctx_lens, "ctx_lens", torch.int32, (B,), self.device)
+        bud = self._ints(budgets, "budgets", B)
+        st = self._ints(status, "status", 1)
+        window = int(window)
+        nbytes = spec_verify_attention_workspace_bytes(max(B, 1), T - 1, heads, self.kv_heads, dim,
+                                                       self.page_size, width, window)
+        if nbytes == 0:
+            raise ValueError(f"bad attention shape: B={B} K={T - 1} q_heads={heads} kv_heads="
+                             f"{self.kv_heads} window={window} max_pages={width}")
+        with _enqueue(self.device, stream) as s:
+            if out is None:
+                out = torch.zeros((B, T, heads, dim), dtype=torch.bfloat16, device=self.device)
+            o = _need(out, "out", torch.bfloat16, (B, T, heads, dim), self.device)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            rc = spec_verify_attention(queries.data_ptr(), stride, self._pool_ptr, table, ctx, bud,
+                                       B, T - 1, heads, self.kv_heads, dim, self.page_size, width,
+                                       self.num_pages,
+                                       dim ** -0.5 if scale is None else float(scale), window, o,
+                                       st, ws.data_ptr(), nbytes, s)
+        _check(rc, "spec_verify_attention")
+        return out
+
+
+def head_quantize(x: torch.Tensor, block_rows: int = 1, out=None, stream=None):
+    """Quantise float32 or bfloat16 [rows, H] (contiguous, on the GPU) to
+    8 bits: (codes float8_e4m3fn [rows, Hp], scales float8_e8m0fnu
+    [ceil(rows / block_rows), Hp / 128]), Hp = H rounded up to 128, zeros
+    behind H. block_rows 1 for hidden states, 128 for a head."""
+    if x.dim() != 2 or x.dtype not in _DTYPES or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous float32 or bfloat16 [rows, H] GPU tensor")
+    block_rows = int(block_rows)
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    rows, H = x.shape
+    blocks = -(-H // 128)
+    shapes = (rows, blocks * 128), (-(-rows // block_rows), blocks)
+    types = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    with _enqueue(x.device, stream) as s:
+        if out is None:
+            out = tuple(torch.empty(n, dtype=t, device=x.device) for n, t in zip(shapes, types))
+        c = _need(out[0], "out codes", types[0], shapes[0], x.device)
+        sc = _need(out[1], "out scales", types[1], shapes[1], x.device)
+        rc = spec_head_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, H, block_rows, c, sc, s)
+    _check(rc, "spec_head_quantize")
+    return out[0], out[1]
+
+
+def head_logits(h_codes: torch.Tensor, h_scales: torch.Tensor, w_codes: torch.Tensor,
+                w_scales: torch.Tensor, dtype=torch.float32, out=None, stream=None):
+    """Logits [R, V] (float32 or bfloat16) of quantised states (block_rows 1)
+    under a quantised head (block_rows 128)."""
+    if h_codes.dim() != 2 or w_codes.dim() != 2 or h_codes.shape[1] != w_codes.shape[1] \
+            or h_codes.shape[1] % 128 != 0 or h_codes.shape[1] == 0:
+        raise ValueError("h_codes [R, Hp] and w_codes [V, Hp] must share Hp, a multiple of 128")
+    if not h_codes.is_cuda:
+        raise ValueError("h_codes must be a GPU tensor")
+    dev = h_codes.device
+    R, H = h_codes.shape
+    V = w_codes.shape[0]
+    e4m3, e8m0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    hc = _need(h_codes, "h_codes", e4m3, (R, H), dev)
+    hs = _need(h_scales, "h_scales", e8m0, (R, H // 128), dev)
+    wc = _need(w_codes, "w_codes", e4m3, (V, H), dev)
+    ws = _need(w_scales, "w_scales", e8m0, (-(-V // 128), H // 128), dev)
+    if out is not None:
+        dtype = out.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"logits are float32 or bfloat16, not {dtype}")
+    with _enqueue(dev, stream) as s:
+        if out is None:
+            out = torch.empty((R, V), dtype=dtype, device=dev)
+        o = _need(out, "out", dtype, (R, V), dev)
+        rc = spec_head_logits(hc, hs, wc, ws, R, H, V, _DTYPES[dtype], o, s)
+    _check(rc, "spec_head_logits")
+    return out

@@ -3,8 +3,11 @@
 ``python -m draft_verify_sampling_spec_amd.build`` (or ``build_library()``)
 compiles ``csrc/spec_verify.hip`` (verification), ``csrc/budget_schedule.hip``
 (the verify-budget scheduler), ``csrc/head_stats.hip`` (output-head row
-statistics), ``csrc/verify_hidden.hip`` (verification from hidden states) and
-``csrc/markov_draft.hip`` (the drafter's low-rank Markov head) into
+statistics), ``csrc/verify_hidden.hip`` (verification from hidden states),
+``csrc/markov_draft.hip`` (the drafter's low-rank Markov head),
+``csrc/block_cache.hip`` (the paged 4-bit key/value cache),
+``csrc/block_attention.hip`` (attention of drafted blocks over it) and
+``csrc/head_fp8.hip`` (the output head in 8-bit floating point) into
 ``libspec_verify.so`` next to this file.
 """
 from __future__ import annotations
@@ -20,7 +23,10 @@ SRC = os.path.join(PKG_DIR, "csrc", "spec_verify.hip")
 SOURCES = [SRC, os.path.join(PKG_DIR, "csrc", "budget_schedule.hip"),
            os.path.join(PKG_DIR, "csrc", "head_stats.hip"),
            os.path.join(PKG_DIR, "csrc", "verify_hidden.hip"),
-           os.path.join(PKG_DIR, "csrc", "markov_draft.hip")]
+           os.path.join(PKG_DIR, "csrc", "markov_draft.hip"),
+           os.path.join(PKG_DIR, "csrc", "block_cache.hip"),
+           os.path.join(PKG_DIR, "csrc", "block_attention.hip"),
+           os.path.join(PKG_DIR, "csrc", "head_fp8.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libspec_verify.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)

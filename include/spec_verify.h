@@ -89,10 +89,20 @@ enum sv_status {
                                    that call are not valid. No wait depends on
                                    other workgroups being resident. */
 
+#define SV_FLAG_BAD_LENGTH 0x8u /* a request's tokens do not fit its page table
+                                   row (or an output); it was skipped */
+#define SV_FLAG_BAD_PAGE 0x10u  /* a page number that a call needed was outside
+                                   the pool; its tokens were skipped */
+
 /* Library limits. */
 #define SV_MAX_BATCH 16384
 #define SV_MAX_K 32
 #define SV_MAX_VOCAB (1 << 20)
+#define SV_MAX_HEADS 256
+#define SV_MAX_PAGE 4096
+#define SV_MAX_CONTEXT (1 << 24)
+#define SV_MAX_HIDDEN 65536
+#define SV_MAX_STRIDE 2147483647
 
 /* Size of the static device scratch of spec_verify_run_noalloc (per GPU). */
 #define SV_NOALLOC_SCRATCH_BYTES (16u << 20)
@@ -429,6 +439,195 @@ int spec_markov_draft(const void* base_logits, const void* markov_a, const void*
 /* spec_markov_draft_workspace_bytes -- scratch spec_markov_draft needs for
  * (B, V); 0 on bad arguments. Host only. */
 size_t spec_markov_draft_workspace_bytes(int B, int V);
+
+/*
+ * The paged 4-bit key/value cache of the target model.
+ *
+ * A verify step scores a block in one pass of the target ("Speculative
+ * decoding becomes standard: DSpark and multi-token drafters", section "Why
+ * draft-and-verify does not change the output"): per layer, the k_b + 1 new
+ * tokens' keys and values enter the cache and every row of the block attends
+ * over it. The cache is one caller-owned buffer of
+ * spec_verify_cache_bytes() bytes (device, 16-byte aligned):
+ *   uint8 [num_pages][kv_heads][page_size / 32][34 * head_dim],
+ * tiles of 32 consecutive tokens of one head. Keys and values are e2m1 codes
+ * (a sign bit, then 0, 0.5, 1, 1.5, 2, 3, 4, 6), one scale byte per token,
+ * head and 32 channels: 2^(byte - 127), 255 = not a number. The scale is the
+ * smallest power of two, at least 2^-64, under which the group's largest
+ * magnitude is at most 6 (at most 2^125: larger magnitudes saturate); codes
+ * are rounded to nearest, ties to even. A group that holds a NaN or an
+ * infinity reads as NaN. Tokens never share a scale, so rejected drafted
+ * tokens are undone by the lengths alone.
+ * Inside a tile, for token tok (0..31) with half = tok / 16, low = tok % 16,
+ * quad = low / 4, and D = head_dim, U = min(16, D / 8), C = min(4, D / 32):
+ *   key bytes    y = 0 .. D/2 - 1  at half 8 D + (y / U) 16 U + low U + y % U
+ *   value bytes  y = 0 .. D/2 - 1, piece = y / C, at 16 D +
+ *       (((piece / 16) 2 + half) 4 + quad) 64 C + (piece % 16) 4 C +
+ *       (low % 4) C + y % C
+ *   key scale of group g = channel / 32    at 32 D + 32 g + 2 low + half
+ *   value scale of group g                 at 33 D + 32 g + 8 quad + 4 half + low % 4
+ * Byte y holds channel 2 y in its low half and 2 y + 1 in its high half.
+ * Shared arguments:
+ *   kv_heads, head_dim   1..SV_MAX_HEADS; 64, 128 or 256.
+ *   page_size    tokens of a page: a power of two, 32..SV_MAX_PAGE.
+ *   page_table   int32 [B, max_pages] (device): the page of positions
+ *                [i page_size, (i + 1) page_size) of request b. Entries that a
+ *                call does not need are never read as pages; a needed entry
+ *                outside [0, num_pages) sets SV_FLAG_BAD_PAGE and its tokens
+ *                are skipped (never accessed out of bounds). max_pages *
+ *                page_size is at most SV_MAX_CONTEXT.
+ *   ctx_lens     int32 [B] (device): tokens of request b in the cache before
+ *                this block; negative marks an empty slot, which is skipped
+ *                (nothing read, nothing written).
+ *   budgets      int32 [B] (device) or NULL: the block has budgets[b] + 1
+ *                tokens, at positions ctx_lens[b] onwards (clamped into the
+ *                block's width, with SV_FLAG_BAD_BUDGET); NULL: all of them.
+ *   out_status   int32 [1] (device) or NULL: SV_FLAG_* bits are OR-ed into it
+ *                (the caller clears it; one word can collect a whole step).
+ *                Outputs of a flagged request are undefined, apart from what
+ *                is said to be skipped.
+ * A block that does not fit its page table row sets SV_FLAG_BAD_LENGTH and is
+ * skipped. Requests may share pages that are only read; two tokens written to
+ * the same place in one call leave either of them.
+ */
+
+/* spec_verify_cache_bytes -- bytes of a cache of num_pages pages; 0 on bad
+ * arguments. Host only. */
+size_t spec_verify_cache_bytes(int num_pages, int kv_heads, int head_dim, int page_size);
+
+/*
+ * spec_verify_cache_write -- quantise the keys and values of every request's
+ * block (or prompt) into the cache. Stream-ordered, one launch.
+ *   keys, values   [B, T, kv_heads, head_dim] of type dtype (device, 16-byte
+ *                  aligned): token t of request b starts at element (b T + t)
+ *                  stride, its heads contiguous. Tokens at t > budgets[b] are
+ *                  never read.
+ *   key_stride, value_stride  elements between tokens: at least kv_heads *
+ *                  head_dim, a multiple of 16 bytes (a slice of a fused
+ *                  projection's rows is taken as it is).
+ *   B, T           requests (0..SV_MAX_BATCH; 0 is a no-op), tokens per
+ *                  request (0..SV_MAX_CONTEXT; 0 is a no-op); T * kv_heads *
+ *                  head_dim at most 2^33.
+ * Other bytes of the cache keep their values.
+ * Errors (nothing enqueued): SV_ERR_ARG, SV_ERR_DTYPE, SV_ERR_NULL,
+ * SV_ERR_ALIGN; SV_ERR_HIP if the launch fails.
+ */
+int spec_verify_cache_write(const void* keys, const void* values, int dtype, int64_t key_stride,
+                            int64_t value_stride, const int32_t* page_table,
+                            const int32_t* ctx_lens, const int32_t* budgets, int B, int T,
+                            int kv_heads, int head_dim, int page_size, int max_pages,
+                            int num_pages, void* cache, int32_t* out_status, void* stream);
+
+/*
+ * spec_verify_cache_read -- read tokens back as the values their codes stand
+ * for (exact in both types). Stream-ordered, one launch.
+ *   starts       int32 [B] (device) or NULL (all 0): first position; negative
+ *                marks an empty slot.
+ *   lens         int32 [B] (device): tokens to read, at most T (more, or past
+ *                the page table row: SV_FLAG_BAD_LENGTH, request skipped);
+ *                0 or less: none.
+ *   B, T, dtype  as above; out_keys, out_values [B, T, kv_heads, head_dim] of
+ *                type dtype (device, 16-byte aligned). Tokens at t >= lens[b]
+ *                keep their values.
+ * Errors as spec_verify_cache_write.
+ */
+int spec_verify_cache_read(const void* cache, const int32_t* page_table, const int32_t* starts,
+                           const int32_t* lens, int B, int T, int kv_heads, int head_dim,
+                           int page_size, int max_pages, int num_pages, int dtype, void* out_keys,
+                           void* out_values, int32_t* out_status, void* stream);
+
+/*
+ * spec_verify_attention -- attention of every row of the drafted blocks over
+ * the cache, which already holds the blocks' own tokens
+ * (spec_verify_cache_write on the same stream). Row t of request b, t <=
+ * budgets[b], stands at position p = ctx_lens[b] + t and sees the positions
+ * [max(0, p - window + 1), p] (window 0: [0, p]); query head i reads kv head
+ * i / (q_heads / kv_heads):
+ *   out = sum_j softmax_j(scale q . k_j) v_j.
+ * Products accumulate in fp32, the softmax's statistics are fp32. A NaN group
+ * of a key or value reaches exactly the rows that see its token. K = 0 is the
+ * single-token form. Stream-ordered, no host sync, one launch, or two when the
+ * contexts are split over workgroups (a choice by the shapes alone).
+ *   queries      bf16 [B, K+1, q_heads, head_dim] (device, 16-byte aligned),
+ *                query_stride elements between tokens (at least q_heads *
+ *                head_dim, a multiple of 8). Rows t > budgets[b] are never read.
+ *   B, K         requests (0..SV_MAX_BATCH; 0 is a no-op), drafted tokens
+ *                (0..SV_MAX_K).
+ *   q_heads      a multiple of kv_heads, up to SV_MAX_HEADS.
+ *   scale        finite; usually 1 / sqrt(head_dim).
+ *   window       0, or the number of positions a row sees, its own included.
+ *                Pages wholly before every row's window are not needed.
+ *   out          bf16 [B, K+1, q_heads, head_dim] (device, 16-byte aligned).
+ *                Rows t > budgets[b] and empty slots keep their values.
+ *   workspace    device scratch of at least
+ *                spec_verify_attention_workspace_bytes() bytes (256-byte
+ *                aligned), caller-owned, its contents of no account; calls
+ *                that share it must not overlap.
+ * Errors (nothing enqueued): SV_ERR_ARG, SV_ERR_NULL, SV_ERR_ALIGN;
+ * SV_ERR_HIP if a launch fails.
+ */
+int spec_verify_attention(const void* queries, int64_t query_stride, const void* cache,
+                          const int32_t* page_table, const int32_t* ctx_lens,
+                          const int32_t* budgets, int B, int K, int q_heads, int kv_heads,
+                          int head_dim, int page_size, int max_pages, int num_pages, float scale,
+                          int window, void* out, int32_t* out_status, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* spec_verify_attention_workspace_bytes -- scratch spec_verify_attention
+ * needs; 0 on bad arguments. Host only. */
+size_t spec_verify_attention_workspace_bytes(int B, int K, int q_heads, int kv_heads,
+                                             int head_dim, int page_size, int max_pages,
+                                             int window);
+
+/*
+ * The output head in 8-bit floating point (the shared projection of "What
+ * DSpark adds", paragraph 1, held in half of bf16's bytes).
+ *
+ * Codes are e4m3 (largest 448), rows padded with zeros to Hp = H rounded up
+ * to a multiple of 128; scales are bytes 2^(byte - 127), 255 = not a number,
+ * one per block: a row's 128 channels, or 128 x 128 of a head. The scale is
+ * the smallest power of two, at least 2^-64, under which the block's largest
+ * magnitude is at most 448 (at most 2^119: larger magnitudes saturate); codes
+ * are rounded to nearest, ties to even. A block that holds a NaN or an
+ * infinity has NaN codes and scale.
+ */
+
+/*
+ * spec_head_quantize -- quantise hidden states or a head. Stream-ordered, one
+ * launch.
+ *   src         [rows, H] of type dtype (sv_dtype), row-major (device,
+ *               16-byte aligned); rows 0..SV_MAX_VOCAB (0 is a no-op), H a
+ *               multiple of 8, 8..SV_MAX_HIDDEN.
+ *   block_rows  1 (states) or 128 (a head).
+ *   out_codes   uint8 [rows, Hp] (device, 16-byte aligned).
+ *   out_scales  uint8 [ceil(rows / block_rows), Hp / 128] (device).
+ * Errors (nothing enqueued): SV_ERR_ARG, SV_ERR_DTYPE, SV_ERR_NULL,
+ * SV_ERR_ALIGN; SV_ERR_HIP if the launch fails.
+ */
+int spec_head_quantize(const void* src, int dtype, int rows, int H, int block_rows,
+                       void* out_codes, void* out_scales, void* stream);
+
+/*
+ * spec_head_logits -- logits of quantised states under a quantised head,
+ *   out[r, v] = sum_i (h[r, i] s_h) (w[v, i] s_w),
+ * the rows that spec_verify_run reads. Stream-ordered, one launch.
+ *   h_codes, h_scales  R states quantised with block_rows = 1.
+ *   w_codes, w_scales  the head, V rows quantised with block_rows = 128.
+ *   R, H, V    rows (0..SV_MAX_VOCAB; 0 is a no-op), hidden size
+ *              (1..SV_MAX_HIDDEN; codes have Hp channels), vocabulary
+ *              (1..SV_MAX_VOCAB).
+ *   dtype      type of out (sv_dtype). fp32 logits are fp32 accumulations of
+ *              exact products. bf16 logits may come from the 8-bit matrix
+ *              instructions, whose sums keep about 16 bits (1e-5 relative to
+ *              the row, measured), before they are rounded to 8.
+ *   out        [R, V] row-major (device, aligned to its element size).
+ * Codes are 16-byte aligned.
+ * Errors (nothing enqueued): SV_ERR_ARG, SV_ERR_DTYPE, SV_ERR_NULL,
+ * SV_ERR_ALIGN; SV_ERR_HIP if the launch fails.
+ */
+int spec_head_logits(const void* h_codes, const void* h_scales, const void* w_codes,
+                     const void* w_scales, int R, int H, int V, int dtype, void* out,
+                     void* stream);
 
 /* spec_verify_free -- release the context (NULL-safe, idempotent on NULL).
  * Waits for the device before freeing the workspace. */

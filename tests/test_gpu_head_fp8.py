@@ -1,0 +1,229 @@
+"""The output head in 8 bits on the GPU against the fp64 oracle. Quantisation
+is compared for equality (a code is a function of the input alone).
+
+Logits, with S = sum_i |h_i w_i| over the dequantised values: an fp32 logit is
+an fp32 sum of exact products, off by at most 4 sqrt(Hp) 2^-24 S (the head's
+usual bound, a margin of 4 over the random walk). A bf16 logit is rounded
+(half a step, 2^-8 of itself) from sums of at least 16 bits: the 8-bit matrix
+instructions keep each 4-product partial sum to about 2^-16 of its largest
+term, so 2^-15 S covers them."""
+import math
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from draft_verify_sampling_spec_amd import SpecVerify, BlockCache, head_logits, head_quantize
+from draft_verify_sampling_spec_amd import schedule_budgets
+from oracle import lowbit as lb
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+def _log(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+def _scales(t):
+    b = t.view(torch.uint8).cpu().numpy().astype(np.float64)
+    return np.where(b == 255, np.nan, np.exp2(b - 127.0))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("rows,H", [(1, 8), (3, 128), (129, 136), (300, 520), (128, 2560), (37, 1000)])
+def test_quantize_matches_the_oracle(rows, H, block_rows, dtype):
+    _log(f"[quantize] rows={rows} H={H} block_rows={block_rows} {dtype}")
+    rng = np.random.default_rng(rows + H)
+    x = rng.normal(size=(rows, H)) * np.exp2(rng.integers(-12, 12, (rows, 1)).astype(float))
+    x = torch.tensor(x).to(dtype)
+    codes, scales = head_quantize(x.to(DEV), block_rows)
+    rc, rs = lb.quantise_head(x.double().numpy(), block_rows)
+    assert codes.shape == rc.shape and scales.shape == rs.shape
+    assert np.array_equal(_scales(scales), rs)
+    assert np.array_equal(codes.double().cpu().numpy(), rc)
+    assert np.all(codes.view(torch.uint8)[:, H:].cpu().numpy() == 0)
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_borders_and_specials(block_rows):
+    """All e4m3 values and the midpoints between them with their neighbours at
+    several scales; zeros, denormals, the largest magnitudes, NaN, infinities."""
+    v = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    mid = (v[1:] + v[:-1]) / 2
+    base = np.concatenate([v, mid, np.nextafter(mid.astype(np.float32), np.float32(1e9)),
+                           np.nextafter(mid.astype(np.float32), np.float32(0))])
+    base = np.concatenate([base, np.zeros(-base.size % 127)]).reshape(-1, 127)
+    base = np.concatenate([np.full((base.shape[0], 1), 448.0), base], 1)   # fixes the scale
+    rows = [s * base * np.exp2(float(e)) for e in (-64, -3, 0, 60, 119) for s in (1, -1)]
+    rows += [np.zeros((1, 128)), np.full((1, 128), 1e-42), np.full((1, 128), -3.4e38)]
+    for bad in (np.nan, np.inf, -np.inf):
+        r = np.linspace(-1, 1, 128)[None]
+        r[0, 5] = bad
+        rows.append(r)
+    x = np.concatenate(rows).astype(np.float32)
+    for part in ([x] if block_rows == 1 else [x[i:i + 7] for i in range(0, len(x), 7)]):
+        codes, scales = head_quantize(torch.tensor(part).to(DEV), block_rows)
+        rc, rs = lb.quantise_head(part.astype(np.float64), block_rows)
+        assert np.array_equal(_scales(scales), rs, equal_nan=True)
+        assert np.array_equal(codes.double().cpu().numpy(), rc, equal_nan=True)
+
+
+def _check_logits(R, H, V, dtype, seed=0, rows=None, hot=False):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    h = torch.randn(R, H, generator=g, device=DEV)
+    if hot:
+        h = h * torch.exp2(torch.randint(-9, 9, (R, 1), generator=g, device=DEV).float())
+    w = torch.randn(V, H, generator=g, device=DEV) * (3.0 / H ** 0.5)
+    hc, hs = head_quantize(h, 1)
+    wc, ws = head_quantize(w, 128)
+    got = head_logits(hc, hs, wc, ws, dtype=dtype)
+    assert got.shape == (R, V) and got.dtype == dtype
+    pick = torch.arange(R) if rows is None else torch.as_tensor(rows)
+    a = lb.head_values(hc[pick].double().cpu().numpy(), _scales(hs[pick]), 1)
+    b = lb.head_values(wc.double().cpu().numpy(), _scales(ws), 128)
+    ref, S = a @ b.T, np.abs(a) @ np.abs(b).T
+    tol = 4 * math.sqrt(a.shape[1]) * 2.0 ** -24 * S + 1e-30
+    if dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -15 * S + 2.0 ** -8 * (1 + 2.0 ** -7) * np.abs(ref)
+    err = np.abs(got[pick].double().cpu().numpy() - ref)
+    assert np.all(err <= tol), float((err / tol).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,H,V", [(1, 8, 1), (5, 128, 17), (16, 136, 100), (17, 2560, 333),
+                                   (48, 384, 1001), (64, 640, 129), (65, 256, 2050), (128, 128, 512),
+                                   (200, 1000, 777), (300, 512, 1029), (513, 256, 515),
+                                   (1024, 384, 256), (700, 2560, 1500)])
+def test_logits_match_the_oracle(R, H, V, dtype):
+    _log(f"[logits] R={R} H={H} V={V} {dtype}")
+    _check_logits(R, H, V, dtype, seed=R + V, hot=R % 2 == 1)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R", [48, 600])
+def test_logits_of_a_whole_vocabulary(R, dtype):
+    """Outputs past 2^26 values and codes past 2^28 bytes; some rows by the oracle."""
+    _check_logits(R, 2560, 151936, dtype, seed=R, rows=[0, 17, R - 1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R", [4, 300])
+def test_a_nan_block_reaches_its_row_or_columns_only(R, dtype):
+    g = torch.Generator(device=DEV).manual_seed(3)
+    h = torch.randn(R, 256, generator=g, device=DEV)
+    w = torch.randn(400, 256, generator=g, device=DEV)
+    h[1, 200] = float("inf")
+    w[130, 3] = float("nan")
+    got = head_logits(*head_quantize(h, 1), *head_quantize(w, 128), dtype=dtype)
+    want = torch.zeros(R, 400, dtype=torch.bool)
+    want[1] = True
+    want[:, 128:256] = True
+    assert torch.equal(torch.isnan(got).cpu(), want)
+
+
+def test_streams_outputs_and_replays():
+    g = torch.Generator(device=DEV).manual_seed(5)
+    h = torch.randn(40, 512, generator=g, device=DEV).bfloat16()
+    w = torch.randn(1000, 512, generator=g, device=DEV).bfloat16()
+    wq = head_quantize(w, 128)
+    hq = head_quantize(h)
+    want = head_logits(*hq, *wq)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = head_logits(*head_quantize(h, stream=side), *wq, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    out = torch.zeros_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        head_quantize(h, out=hq)
+        head_logits(*hq, *wq, out=out)
+    for i in range(4):
+        h.mul_(1.25)
+        eager = head_logits(*head_quantize(h), *wq)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
+    assert head_logits(hq[0][:0], hq[1][:0], *wq).shape == (0, 1000)
+
+
+def test_python_refusals():
+    x = torch.zeros(4, 64, device=DEV)
+    for bad in (x.half(), x.t(), x[0], x.cpu()):
+        with pytest.raises(ValueError):
+            head_quantize(bad)
+    with pytest.raises(ValueError):
+        head_quantize(x, 64)
+    with pytest.raises(RuntimeError):
+        head_quantize(torch.zeros(4, 12, device=DEV))
+    hc, hs = head_quantize(x)
+    wc, ws = head_quantize(x, 128)
+    with pytest.raises(ValueError):
+        head_logits(hc, hs, wc, ws, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        head_logits(hc, hs[:2], wc, ws)
+    with pytest.raises(ValueError):
+        head_logits(hc, hs, wc, hs)                        # scales of another block shape
+
+
+def test_a_verify_step_from_few_bits():
+    """The operators as a serving step uses them: budgets from confidences,
+    the block's keys and values into the cache, its attention, an 8-bit output
+    projection (here the head itself), and the verify of the logits; three steps
+    whose contexts grow by what was kept. Greedy verification against the
+    oracle's logits: the kept prefix is the target's own argmax wherever its
+    margin exceeds the logits' tolerance."""
+    B, K, Hq, Hkv, D, page, V = 6, 4, 8, 2, 64, 32, 1000
+    H = Hq * D
+    g = torch.Generator(device=DEV).manual_seed(21)
+    head = torch.randn(V, H, generator=g, device=DEV).bfloat16() * 3
+    wq = head_quantize(head, 128)
+    cache = BlockCache(DEV, 40, Hkv, D, page)
+    table = torch.randperm(40, generator=g, device=DEV)[:36].to(torch.int32).view(B, 6).contiguous()
+    ctx = torch.tensor([0, 31, 64, 5, 90, 33], dtype=torch.int32, device=DEV)
+    prompt = torch.randn(2, B, 96, Hkv, D, generator=g, device=DEV).bfloat16()
+    zero = torch.zeros_like(ctx)
+    cache.write(prompt[0], prompt[1], table, zero, ctx - 1 + (ctx == 0).int())
+    sv = SpecVerify(DEV, B, K, V, torch.float32)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for step in range(3):
+        conf = torch.rand(B, K, generator=g, device=DEV)
+        budgets = schedule_budgets(conf, 2 * B)
+        qkv = torch.randn(B, K + 1, (Hq + 2 * Hkv) * D, generator=g, device=DEV).bfloat16()
+        q, k, v = (x.unflatten(-1, (-1, D)) for x in qkv.split([Hq * D, Hkv * D, Hkv * D], -1))
+        cache.write(k, v, table, ctx, budgets, status=status)
+        o = cache.attend(q, table, ctx, budgets, status=status)
+        hq = head_quantize(o.view(B * (K + 1), H))
+        logits = head_logits(*hq, *wq).view(B, K + 1, V)
+        tokens = logits[:, :K].argmax(-1).to(torch.int32)
+        tokens[::2, 1] = 7                                  # a wrong draft in every other request
+        out, n, _, _ = sv.run(logits, None, tokens, budgets, 0.0, 1, want_probs=False)
+        torch.cuda.synchronize()
+        # The oracle's step on the same inputs.
+        pool, tab, c = cache.pool.cpu().numpy(), table.cpu().numpy(), ctx.cpu().numpy()
+        kb = budgets.cpu().numpy()
+        wv = lb.head_values(wq[0].double().cpu().numpy(), _scales(wq[1]), 128)
+        for b in range(B):
+            m = int(c[b] + kb[b] + 1)
+            kk, vv = lb.read(pool, tab[b], 0, m, D, page)
+            ref, mag, _ = lb.attend(q[b, :kb[b] + 1].double().cpu().numpy(), kk, vv, 0, int(c[b]), D ** -0.5)
+            got = o[b, :kb[b] + 1].double().cpu().numpy()
+            assert np.all(np.abs(got - ref) <= 2.0 ** -7 * (mag + np.abs(ref)))
+            hv = lb.head_values(*lb.quantise_head(got.reshape(kb[b] + 1, H), 1), 1)
+            z = hv @ wv.T
+            S = (np.abs(hv) @ np.abs(wv).T).max(-1)
+            kept = 0
+            for i in range(kb[b] + 1):
+                top = np.sort(z[i])[-2:]
+                assert top[1] - top[0] > 8 * math.sqrt(H) * 2.0 ** -24 * S[i]
+                if i == kb[b] or int(tokens[b, i]) != int(z[i].argmax()):
+                    assert int(out[b, i]) == int(z[i].argmax())
+                    break
+                kept += 1
+            assert int(n[b]) == kept
+        ctx = ctx + n + 1                                   # rejected tokens are simply overwritten
+    assert int(status) == 0 and sv.status() == 0
+    sv.close()
