@@ -11,6 +11,7 @@
 #include <cmath>
 
 #include "cache_tile.h"
+#include "lds_dma.h"
 
 namespace {
 
@@ -144,70 +145,255 @@ struct LogitArgs {
     int R, V, blocks;
 };
 
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(uint16_t* p, float v) {
-    *p = __builtin_bit_cast(uint16_t, (__bf16)v);
+// The product: workgroups hold tiles of TV vocabulary columns x TR rows, the
+// operands' codes streamed through an LDS ring of kStages blocks of 128
+// channels by buffer-to-LDS loads. A row's 128 bytes are eight chunks of 16;
+// chunk c of row i lies at position c ^ (i & 7), so that the eight lanes that
+// read one chunk column at a time touch all banks (the loads choose their
+// global chunk accordingly; LDS itself is filled linearly).
+//
+// kF8: 8-bit matrix instructions with both scales as their operands, for bf16
+// logits. Otherwise the codes are decoded to bf16 (exact, scales included) in
+// registers and multiplied in bf16, for fp32 logits: the 8-bit instructions
+// keep a sum of products only to about 2^-17 of its terms (relative error
+// 1.4e-5 of a row's norm, measured at 128, 2,560 and 10,240 channels), an
+// eighth of a hundredth of a bf16 rounding but two hundred fp32 ones.
+template <int TV_, int TR_, int WV_, int WR_, int kStages_, bool kF8_, typename O_>
+struct Cfg {
+    static constexpr int TV = TV_, TR = TR_, WV = WV_, WR = WR_, kStages = kStages_;
+    static constexpr bool kF8 = kF8_;
+    using O = O_;
+    static constexpr int kWaves = WV * WR, kThreads = 64 * kWaves;
+    static constexpr int MV = TV / WV / 32, MR = TR / WR / 32;    // 32 x 32 tiles of a wave
+    static constexpr int kLoads = (TV + TR) / 8 / kWaves;         // buffer loads per wave and stage
+    static constexpr int kStageBytes = (TV + TR) * kBlock;
+    static constexpr int kRing = kStages * kStageBytes;
+    static constexpr int kRowBytes = TV * (int)sizeof(O);
+    // Rows that the ring holds of the finished tile.
+    static constexpr int kPass = kRing / kRowBytes < TR ? kRing / kRowBytes / 64 * 64 : TR;
+    static_assert(TV % (32 * WV) == 0 && TR % (32 * WR) == 0, "whole 32 x 32 tiles");
+    static_assert((TV + TR) % (8 * kWaves) == 0 && TV % (8 * kWaves) == 0, "even loads");
+    static_assert(128 % (TV / WV) == 0, "one head scale per wave and block");
+    static_assert(kPass >= 32 && TR % kPass == 0 && kPass % (TR / WR) == 0, "whole waves per pass");
+};
+
+typedef __attribute__((ext_vector_type(8))) int i32x8;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+
+__device__ __forceinline__ uint2 pack4(const float (&v)[4], uint16_t) {
+    bf16x2 a, b;
+    a[0] = (__bf16)v[0]; a[1] = (__bf16)v[1];
+    b[0] = (__bf16)v[2]; b[1] = (__bf16)v[3];
+    return make_uint2(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b));
+}
+__device__ __forceinline__ f32x4 pack4(const float (&v)[4], float) {
+    return f32x4{v[0], v[1], v[2], v[3]};
 }
 
-// A wavefront: 16 vocabulary columns x 16 kMT rows, the head's codes straight
-// from memory.
-template <int kMT, typename O>
-__global__ __launch_bounds__(256) void logits_stream_kernel(LogitArgs a) {
-    const int lane = threadIdx.x & 63, x = lane & 15, quad = lane >> 4;
-    const int v0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 16;
-    if (v0 >= a.V) return;
-    const int r0 = blockIdx.y * 16 * kMT;
-    const long long pitch = (long long)a.blocks * kBlock;
-    const int wrow = min(v0 + x, a.V - 1);
-    const uint8_t* wp = a.w + wrow * pitch + quad * 16;
-    const uint8_t* wsp = a.ws + (long long)(wrow / kBlock) * a.blocks;
-    const uint8_t* hp[kMT];
-    const uint8_t* hsp[kMT];
-    #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
-        const int r = min(r0 + mt * 16 + x, a.R - 1);
-        hp[mt] = a.h + r * pitch + quad * 16;
-        hsp[mt] = a.hs + (long long)r * a.blocks;
-    }
-    f32x4 acc[kMT] = {};
-    for (int k = 0; k < a.blocks; ++k) {
-        const u32x4 w0 = *reinterpret_cast<const u32x4*>(wp + (long long)k * kBlock);
-        const u32x4 w1 = *reinterpret_cast<const u32x4*>(wp + (long long)k * kBlock + 64);
-        const float s = scale_of(wsp[k]);
-        const bf16x8 wf[4] = {decode8(w0[0], w0[1], s), decode8(w0[2], w0[3], s),
-                              decode8(w1[0], w1[1], s), decode8(w1[2], w1[3], s)};
+template <typename C>
+__global__ __launch_bounds__(C::kThreads) void logits_kernel(LogitArgs a, int v_tiles, int band) {
+    using O = typename C::O;
+    __shared__ __attribute__((aligned(128))) unsigned char ring[C::kRing];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    // Tile order: workgroups go round-robin over the 8 XCDs; each XCD takes
+    // every eighth column tile and walks a band of row tiles under it, so
+    // that a tile of the head is read from HBM once per band and the band's
+    // states stay in that XCD's L2.
+    const int r_tiles = (a.R + C::TR - 1) / C::TR;
+    const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
+    const int v_per = (v_tiles + 7) / 8;
+    const int b0 = at / (v_per * band) * band;
+    const int in_band = min(band, r_tiles - b0);
+    const int rest = at - b0 * v_per;
+    const int vt = rest / in_band * 8 + xcd, rt = b0 + rest % in_band;
+    if (vt >= v_tiles) return;
+    const int v0 = vt * C::TV, r0 = rt * C::TR;
+
+    const unsigned pitch = (unsigned)a.blocks * kBlock;
+    const __amdgpu_buffer_rsrc_t wsrc =
+        svdma::rsrc(a.w + (long long)v0 * pitch, (unsigned)min(C::TV, a.V - v0) * pitch);
+    const __amdgpu_buffer_rsrc_t hsrc =
+        svdma::rsrc(a.h + (long long)r0 * pitch, (unsigned)min(C::TR, a.R - r0) * pitch);
+    // Load i of a wave covers rows 8 (i kWaves + wave) .. + 7 of the stage, the
+    // head's rows first. Rows past the operand read as zeros.
+    const unsigned lane_off = (lane >> 3) * pitch + (((lane & 7) ^ (lane >> 3)) * 16);
+    auto fetch = [&](int k) {
+        unsigned char* base = ring + (k % C::kStages) * C::kStageBytes;
         #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-            const u32x4 h0 = *reinterpret_cast<const u32x4*>(hp[mt] + (long long)k * kBlock);
-            const u32x4 h1 = *reinterpret_cast<const u32x4*>(hp[mt] + (long long)k * kBlock + 64);
-            const float t = scale_of(hsp[mt][k]);
-            acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[0], decode8(h0[0], h0[1], t), acc[mt], 0, 0, 0);
-            acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[1], decode8(h0[2], h0[3], t), acc[mt], 0, 0, 0);
-            acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[2], decode8(h1[0], h1[1], t), acc[mt], 0, 0, 0);
-            acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[3], decode8(h1[2], h1[3], t), acc[mt], 0, 0, 0);
+        for (int i = 0; i < C::kLoads; ++i) {
+            const int row = 8 * (i * C::kWaves + wave);
+            const bool head = i * C::kWaves * 8 < C::TV;
+            const unsigned off = lane_off + (unsigned)(head ? row : row - C::TV) * pitch + k * kBlock;
+            svdma::load16(head ? wsrc : hsrc, off, base + row * kBlock);
+        }
+    };
+
+    const int wv = wave % C::WV, wr = wave / C::WV;
+    const int vrow = wv * 32 * C::MV, rrow = wr * 32 * C::MR;
+    const uint8_t* wsp = a.ws + (long long)(min(v0 + vrow, a.V - 1) / kBlock) * a.blocks;
+    const uint8_t* hsp[C::MR];
+    #pragma unroll
+    for (int j = 0; j < C::MR; ++j) {
+        hsp[j] = a.hs + (long long)min(r0 + rrow + 32 * j + (lane & 31), a.R - 1) * a.blocks;
+    }
+
+    f32x16 acc[C::MV][C::MR] = {};
+    unsigned sw = wsp[0], sh[C::MR];
+    #pragma unroll
+    for (int j = 0; j < C::MR; ++j) sh[j] = hsp[j][0];
+    #pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) {
+        if (s < a.blocks) fetch(s);
+    }
+    const unsigned lds_row = (lane & 31) * kBlock;
+    for (int k = 0; k < a.blocks; ++k) {
+        // Stage k has arrived when at most the loads of the stages after it
+        // are outstanding (the scales' loads only make this stricter).
+        if (k + C::kStages - 2 < a.blocks) {
+            svdma::wait_vm<(C::kStages - 2) * C::kLoads>();
+        } else {
+            svdma::wait_vm<0>();
+        }
+        svdma::ring_barrier();
+        // Everyone has read stage k - 1: its place is free.
+        if (k + C::kStages - 1 < a.blocks) fetch(k + C::kStages - 1);
+        const unsigned sw_now = sw;
+        unsigned sh_now[C::MR];
+        #pragma unroll
+        for (int j = 0; j < C::MR; ++j) sh_now[j] = sh[j];
+        if (k + 1 < a.blocks) {
+            sw = wsp[k + 1];
+            #pragma unroll
+            for (int j = 0; j < C::MR; ++j) sh[j] = hsp[j][k + 1];
+        }
+        const unsigned char* wbase = ring + (k % C::kStages) * C::kStageBytes + vrow * kBlock + lds_row;
+        const unsigned char* hbase =
+            ring + (k % C::kStages) * C::kStageBytes + (C::TV + rrow) * kBlock + lds_row;
+        #pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int c0 = 4 * half + 2 * (lane >> 5);
+            const int p0 = (c0 ^ (lane & 7)) * 16, p1 = ((c0 + 1) ^ (lane & 7)) * 16;
+            u32x4 wc[C::MV][2], hc[C::MR][2];
+            #pragma unroll
+            for (int i = 0; i < C::MV; ++i) {
+                wc[i][0] = *reinterpret_cast<const u32x4*>(wbase + i * 32 * kBlock + p0);
+                wc[i][1] = *reinterpret_cast<const u32x4*>(wbase + i * 32 * kBlock + p1);
+            }
+            #pragma unroll
+            for (int j = 0; j < C::MR; ++j) {
+                hc[j][0] = *reinterpret_cast<const u32x4*>(hbase + j * 32 * kBlock + p0);
+                hc[j][1] = *reinterpret_cast<const u32x4*>(hbase + j * 32 * kBlock + p1);
+            }
+            if constexpr (C::kF8) {
+                i32x8 hf[C::MR];
+                #pragma unroll
+                for (int j = 0; j < C::MR; ++j) {
+                    hf[j] = __builtin_bit_cast(i32x8, __builtin_shufflevector(hc[j][0], hc[j][1], 0, 1, 2, 3, 4, 5, 6, 7));
+                }
+                #pragma unroll
+                for (int i = 0; i < C::MV; ++i) {
+                    const i32x8 wf = __builtin_bit_cast(i32x8, __builtin_shufflevector(wc[i][0], wc[i][1], 0, 1, 2, 3, 4, 5, 6, 7));
+                    #pragma unroll
+                    for (int j = 0; j < C::MR; ++j) {
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            wf, hf[j], acc[i][j], 0, 0, 0, (int)sw_now, 0, (int)sh_now[j]);
+                    }
+                }
+            } else {
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    bf16x8 hf[C::MR];
+                    #pragma unroll
+                    for (int j = 0; j < C::MR; ++j) {
+                        hf[j] = decode8(hc[j][q >> 1][2 * (q & 1)], hc[j][q >> 1][2 * (q & 1) + 1],
+                                        scale_of(sh_now[j]));
+                    }
+                    #pragma unroll
+                    for (int i = 0; i < C::MV; ++i) {
+                        const bf16x8 wf = decode8(wc[i][q >> 1][2 * (q & 1)],
+                                                  wc[i][q >> 1][2 * (q & 1) + 1], scale_of(sw_now));
+                        #pragma unroll
+                        for (int j = 0; j < C::MR; ++j) {
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf, hf[j], acc[i][j], 0, 0, 0);
+                        }
+                    }
+                }
+            }
         }
     }
+
+    // The tile goes out through LDS, row by row: 16-byte chunk c of row i at
+    // c ^ (i & mask).
+    constexpr int kChunks = C::kRowBytes / 16;
+    constexpr int kMask = (kChunks < 32 ? kChunks : 32) - 1;
+    constexpr int kPer = 16 / (int)sizeof(O);                      // values of a chunk
+    const bool wide = (a.V * (int)sizeof(O)) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
     O* out = static_cast<O*>(a.out);
     #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
-        const int r = r0 + mt * 16 + x;
-        if (r >= a.R) continue;
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int v = v0 + 4 * quad + i;
-            if (v < a.V) put(out + (long long)r * a.V + v, acc[mt][i]);
+    for (int pass = 0; pass < C::TR / C::kPass; ++pass) {
+        __syncthreads();
+        if (rrow / C::kPass == pass) {
+            #pragma unroll
+            for (int j = 0; j < C::MR; ++j) {
+                const int row = rrow % C::kPass + 32 * j + (lane & 31);
+                #pragma unroll
+                for (int i = 0; i < C::MV; ++i) {
+                    #pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1],
+                                            acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+                        const int col = vrow + 32 * i + 8 * g + 4 * (lane >> 5);
+                        unsigned char* dst = ring + row * C::kRowBytes +
+                                             ((col / kPer) ^ (row & kMask)) * 16 + col % kPer * sizeof(O);
+                        const auto w = pack4(v, O{});
+                        __builtin_memcpy(__builtin_assume_aligned(dst, sizeof(w)), &w, sizeof(w));
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const int rows = min(C::kPass, a.R - r0 - pass * C::kPass), cols = min(C::TV, a.V - v0);
+        O* dst = out + (long long)(r0 + pass * C::kPass) * a.V + v0;
+        if (wide) {
+            for (int i = threadIdx.x; i < C::kPass * kChunks; i += C::kThreads) {
+                const int row = i / kChunks, c = i % kChunks;
+                if (row < rows && c * kPer < cols) {
+                    *reinterpret_cast<u32x4*>(dst + (long long)row * a.V + c * kPer) =
+                        *reinterpret_cast<const u32x4*>(ring + row * C::kRowBytes + (c ^ (row & kMask)) * 16);
+                }
+            }
+        } else {
+            for (int i = threadIdx.x; i < C::kPass * C::TV; i += C::kThreads) {
+                const int row = i / C::TV, col = i % C::TV;
+                if (row < rows && col < cols) {
+                    dst[(long long)row * a.V + col] = *reinterpret_cast<const O*>(
+                        ring + row * C::kRowBytes + ((col / kPer) ^ (row & kMask)) * 16 + col % kPer * sizeof(O));
+                }
+            }
         }
     }
 }
 
-template <int kMT>
-void launch_stream(const LogitArgs& a, int dtype, hipStream_t s) {
-    const dim3 grid((unsigned)((a.V + 63) / 64), (unsigned)((a.R + 16 * kMT - 1) / (16 * kMT)));
-    if (dtype == SV_DTYPE_F32) {
-        hipLaunchKernelGGL((logits_stream_kernel<kMT, float>), grid, dim3(256), 0, s, a);
-    } else {
-        hipLaunchKernelGGL((logits_stream_kernel<kMT, uint16_t>), grid, dim3(256), 0, s, a);
-    }
+template <typename C>
+void launch_logits(const LogitArgs& a, hipStream_t s) {
+    const int v_tiles = (a.V + C::TV - 1) / C::TV, r_tiles = (a.R + C::TR - 1) / C::TR;
+    const int bands = (r_tiles + 7) / 8;
+    const int band = (r_tiles + bands - 1) / bands;
+    const long long grid = (long long)(v_tiles + 7) / 8 * 8 * r_tiles;
+    hipLaunchKernelGGL((logits_kernel<C>), dim3((unsigned)grid), dim3(C::kThreads), 0, s, a, v_tiles,
+                       band);
+}
+
+// Tiles by the number of rows: up to 64 rows the head's bytes decide and the
+// tile is as narrow as its rows; above, the largest tile that they fill.
+template <bool kF8, typename O>
+void launch_rows(const LogitArgs& a, hipStream_t s) {
+    if (a.R <= 32) launch_logits<Cfg<64, 32, 2, 1, 3, kF8, O>>(a, s);
+    else if (a.R <= 64) launch_logits<Cfg<64, 64, 2, 2, 3, kF8, O>>(a, s);
+    else if (a.R <= 128) launch_logits<Cfg<256, 128, 4, 2, 3, kF8, O>>(a, s);
+    else launch_logits<Cfg<256, 256, 2, 4, 2, kF8, O>>(a, s);
 }
 
 }  // namespace
@@ -268,10 +454,7 @@ extern "C" int spec_head_logits(const void* h_codes, const void* h_scales, const
                 static_cast<const uint8_t*>(w_codes), static_cast<const uint8_t*>(w_scales),
                 out, R, V, (H + kBlock - 1) / kBlock};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const int tiles = (R + 15) / 16;
-    if (tiles == 1) launch_stream<1>(a, dtype, s);
-    else if (tiles == 2) launch_stream<2>(a, dtype, s);
-    else if (tiles == 3) launch_stream<3>(a, dtype, s);
-    else launch_stream<4>(a, dtype, s);
+    if (dtype == SV_DTYPE_F32) launch_rows<false, float>(a, s);
+    else launch_rows<true, uint16_t>(a, s);
     return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
