@@ -18,6 +18,8 @@
 // operand of V^T P^T (whose contraction runs over tokens in that same order),
 // and the accumulators' rescale is a per-lane factor. The cache's tile layout
 // gives every lane its codes in 16-byte loads in these orders.
+#include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "cache_tile.h"
@@ -33,6 +35,22 @@ typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
 constexpr int kWaves = 4;
 constexpr float kNegInf = -INFINITY;
 
+// How the work is cut. A unit is a request's kv head and block of 16 kMT
+// rows; its tiles are cut into splits of `chunk` tiles, a workgroup each. The
+// lengths are on the device, so the cut is made there: every workgroup adds
+// up the tiles of all requests, takes
+//   chunk = max(total / kManySplits, min(total / kFewSplits, kChunk))
+// (rounded up, at least kLeastChunk), and finds its own split by a prefix sum
+// over the requests. kFewSplits workgroups are resident at once; chunks are
+// cut below kChunk tiles only to fill them, and above kChunk only when more
+// than kManySplits splits would come of it. With kDirectUnits units or more
+// every unit is one workgroup and nothing is cut.
+constexpr int kFewSplits = 512;
+constexpr int kManySplits = 2048;
+constexpr int kChunk = 64;
+constexpr int kLeastChunk = 8;
+constexpr int kDirectUnits = 4096;
+
 struct AttendArgs {
     const uint16_t* q;
     long long q_stride;
@@ -41,25 +59,34 @@ struct AttendArgs {
     const int32_t* budgets;
     uint16_t* out;
     int32_t* status;
-    float* part_o;      // [unit][split][16 kMT rows][D], not normalised
-    float2* part_ml;    // [unit][split][16 kMT rows]: maximum, sum
+    float* part_o;      // [slot][16 kMT rows][D], not normalised
+    float2* part_ml;    // [slot][16 kMT rows]: reference exponent, sum
+    int2* cut;          // [B]: the request's first slot, and chunk
     Pages pages;
-    int K, Hq, group;
-    int row_blocks;     // blocks of 16 kMT rows of a request's (K + 1) group rows
-    int chunk;          // tiles of one split
-    int splits;         // splits launched per unit
+    int B, K, Hq, group;
+    int row_blocks;     // blocks of 16 kMT rows of a full block's (K + 1) group rows
     int window;
-    float c;            // scale * log2(e)
+    bool direct;        // a workgroup per unit
+    bool negate;        // scale < 0: queries are negated and |scale| is used
+    float c;            // |scale| * log2(e)
 };
 
 // The tiles a request's block reads: [first, end).
 struct Span {
     int first, end;
+    __device__ __forceinline__ int size() const { return end - first; }
 };
 __device__ __forceinline__ Span span_of(const Block& blk, int window) {
     const int lo = window > 0 ? max(0, blk.ctx - window + 1) : 0;
     return Span{lo / kTile, (blk.ctx + blk.len + kTile - 1) / kTile};
 }
+
+// What a workgroup works on: tiles [t0, t1) of (b, h, row block rb), and
+// whether they are all of the unit's.
+struct Work {
+    int b, h, rb, t0, t1;
+    bool whole;
+};
 
 __device__ __forceinline__ unsigned pack_bf16(float a, float b) {
     bf16x2 v;
@@ -68,273 +95,435 @@ __device__ __forceinline__ unsigned pack_bf16(float a, float b) {
     return __builtin_bit_cast(unsigned, v);
 }
 
-// Maximum / sum over the four lanes that hold the same row.
+// Maximum / sum over the four lanes that hold the same row (lane ^ 16, ^ 32).
 __device__ __forceinline__ float quad_max(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+    auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float quad_sum(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
+__device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// A tile's bytes as one lane holds them.
+template <int D>
+struct Frag {
+    using L = Tile<D>;
+    static constexpr int kWords = L::U / 4;             // words of a key unit
+    unsigned k[2][L::kPlanes][kWords];                  // half, plane: a token's unit of channels
+    unsigned v[2][L::kPlanes][L::C];                    // half, plane: 4 tokens' pieces
+    unsigned ks[L::kPlanes];                            // key scales of both halves
+    unsigned vs[L::kPlanes][2];                         // value scales of 4 + 4 tokens
+
+    __device__ __forceinline__ void load(const uint8_t* tile, int lane) {
+        const int x = lane & 15, quad = lane >> 4;
+        #pragma unroll
+        for (int p = 0; p < L::kPlanes; ++p) {
+            #pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                __builtin_memcpy(k[half][p], __builtin_assume_aligned(
+                    tile + half * (8 * D) + (p * 64 + lane) * L::U, L::U), L::U);
+                __builtin_memcpy(v[half][p], __builtin_assume_aligned(
+                    tile + L::kVCodes + ((p * 2 + half) * 64 + lane) * (4 * L::C), 4 * L::C), 4 * L::C);
+            }
+            const int kg = D == 64 ? quad >> 1 : p * 4 + quad;
+            ks[p] = *reinterpret_cast<const uint16_t*>(tile + L::kKScales + kg * 32 + x * 2);
+            const int vg = D == 64 ? x >> 3 : p * 4 + (x >> 2);
+            __builtin_memcpy(vs[p], __builtin_assume_aligned(
+                tile + L::kVScales + (vg * 4 + quad) * 8, 8), 8);
+        }
+    }
+};
+
+// Registers of one wavefront over its tiles.
+template <int D, int kMT>
+struct State {
+    using L = Tile<D>;
+    static constexpr int kPlanes = L::kPlanes;
+    static constexpr int kUnitSteps = D == 64 ? 2 : 4;  // products of 32 channels in a key unit
+    static constexpr int kSteps = D / 32;
+    static constexpr int kChans = D == 64 ? 4 : 8;      // channels of a value piece
+    f32x4 o[kMT][kPlanes][kChans];
+    float ref[kMT];     // reference of the exponents, in scores (before c); -inf: nothing seen
+    float sum[kMT];     // this lane's share of the row's sum
+    int pos[kMT];       // the row's position; -1 past the block
+};
 
 template <int D, int kMT>
 struct Lds {
     static constexpr int kPieces = kMT * Tile<D>::kPlanes * (D == 64 ? 4 : 8) / 4;  // float4 per lane and round
+    u32x4 q[kMT][D / 32][64];           // right operands of K Q^T
     f32x4 o[kWaves][kPieces][64];
-    float m[kWaves][kMT][16];
-    float l[kWaves][kMT][16];
+    float ref[kWaves][kMT][16];
+    float sum[kWaves][kMT][16];
+    unsigned scan[kWaves];
+    int found[4];
 };
 
-template <int D, int kMT>
-__global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
+// One tile. kAct: row tiles that hold rows of the block. kMasked: some row
+// does not see some token of the tile.
+template <int D, int kMT, int kAct, bool kMasked>
+__device__ __forceinline__ void tile_step(State<D, kMT>& st, const Frag<D>& f,
+                                          const Lds<D, kMT>& sh, const AttendArgs& a, int lane,
+                                          int tok0, int last, const uint8_t* tile) {
     using L = Tile<D>;
-    constexpr int kPlanes = L::kPlanes;
-    constexpr int kKeySteps = D / 32;                  // products of 32 channels
-    constexpr int kUnitSteps = D == 64 ? 2 : 4;        // of which in one key unit
-    constexpr int kChans = D == 64 ? 4 : 8;            // channels of a value piece
+    using S = State<D, kMT>;
+    const int quad = lane >> 4;
+    // Scores of 2 x 16 tokens (lane: tokens 16 half + 4 quad + r).
+    f32x4 z[kAct][2] = {};
+    #pragma unroll
+    for (int p = 0; p < S::kPlanes; ++p) {
+        const float s[2] = {scale_of(f.ks[p] & 255u), scale_of(f.ks[p] >> 8)};
+        #pragma unroll
+        for (int j = 0; j < S::kUnitSteps; ++j) {
+            bf16x8 kf[2];
+            #pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const unsigned w = f.k[half][p][j];
+                const u32x4 kw = {decode2<0>(w, s[half]), decode2<1>(w, s[half]),
+                                  decode2<2>(w, s[half]), decode2<3>(w, s[half])};
+                kf[half] = __builtin_bit_cast(bf16x8, kw);
+            }
+            #pragma unroll
+            for (int mt = 0; mt < kAct; ++mt) {
+                const bf16x8 qf = __builtin_bit_cast(bf16x8, sh.q[mt][p * S::kUnitSteps + j][lane]);
+                #pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    z[mt][half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[half], qf, z[mt][half], 0, 0, 0);
+                }
+            }
+        }
+    }
+
+    // Probabilities 2^((z - ref) c). The reference follows the running
+    // maximum only when a score exceeds it by 8 / c: until then terms stay
+    // below 2^8 and nothing has to be rescaled.
+    bf16x8 pf[kAct];
+    #pragma unroll
+    for (int mt = 0; mt < kAct; ++mt) {
+        float s[8];
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = z[mt][i >> 2][i & 3];
+        if (kMasked) {
+            const int lo = a.window > 0 ? st.pos[mt] - a.window : -1;
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = tok0 + 16 * (i >> 2) + 4 * quad + (i & 3);
+                if (j > st.pos[mt] || j <= lo) s[i] = kNegInf;
+            }
+        }
+        float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])),
+                          fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
+        // Also true while ref is -inf and anything is seen.
+        const bool grow = (top - st.ref[mt]) * a.c > 8.0f || (st.ref[mt] == kNegInf && top > kNegInf);
+        if (__ballot(grow) != 0) {
+            top = fmaxf(quad_max(top), st.ref[mt]);
+            const float keep = st.ref[mt] == kNegInf ? 0.0f : exp2_fast((st.ref[mt] - top) * a.c);
+            st.ref[mt] = top;
+            st.sum[mt] *= keep;
+            #pragma unroll
+            for (int p = 0; p < S::kPlanes; ++p) {
+                #pragma unroll
+                for (int j = 0; j < S::kChans; ++j) st.o[mt][p][j] *= keep;
+            }
+        }
+        // A row that has seen nothing yet: its terms are 2^(-inf) = 0.
+        const float off = st.ref[mt] == kNegInf ? 0.0f : -st.ref[mt] * a.c;
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = exp2_fast(__builtin_fmaf(s[i], a.c, off));
+        st.sum[mt] += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+        const u32x4 pw = {pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]), pack_bf16(s[4], s[5]),
+                          pack_bf16(s[6], s[7])};
+        pf[mt] = __builtin_bit_cast(bf16x8, pw);
+    }
+
+    // Values: 8 tokens (4 quad + r of both halves) x kChans channels a plane.
+    #pragma unroll
+    for (int p = 0; p < S::kPlanes; ++p) {
+        unsigned w[8];
+        float vs[8];
+        bool poison = false;
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int half = i >> 2, r = i & 3;
+            if constexpr (D == 64) {
+                w[i] = r & 1 ? f.v[half][p][r >> 1] >> 16 : f.v[half][p][r >> 1];
+            } else {
+                w[i] = f.v[half][p][r];
+            }
+            const unsigned sc = f.vs[p][half];
+            unsigned bits = (r == 3 ? sc >> 1 : sc << (23 - 8 * r)) & 0x7f800000u;
+            if (kMasked) {
+                // What some row does not see must not reach it as 0 * NaN:
+                // tokens past the block hold anything and are cleared; NaN
+                // groups of tokens that other rows see are cleared here and
+                // put into those rows below.
+                const int j = tok0 + 16 * half + 4 * quad + r;
+                const bool nan = bits == 0x7f800000u;
+                poison |= nan && j <= last;
+                if (nan || j > last) {
+                    bits = 0x3f800000u;
+                    w[i] = 0;
+                }
+            }
+            vs[i] = __uint_as_float(bits);
+        }
+        #pragma unroll
+        for (int cb = 0; cb < S::kChans / 2; ++cb) {
+            unsigned e[8];
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                e[i] = cb == 0   ? decode2<0>(w[i], vs[i])
+                       : cb == 1 ? decode2<1>(w[i], vs[i])
+                       : cb == 2 ? decode2<2>(w[i], vs[i])
+                                 : decode2<3>(w[i], vs[i]);
+            }
+            u32x4 even, odd;
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                even[i] = __builtin_amdgcn_perm(e[2 * i + 1], e[2 * i], 0x05040100u);
+                odd[i] = __builtin_amdgcn_perm(e[2 * i + 1], e[2 * i], 0x07060302u);
+            }
+            #pragma unroll
+            for (int mt = 0; mt < kAct; ++mt) {
+                st.o[mt][p][2 * cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, even), pf[mt], st.o[mt][p][2 * cb], 0, 0, 0);
+                st.o[mt][p][2 * cb + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, odd), pf[mt], st.o[mt][p][2 * cb + 1], 0, 0, 0);
+            }
+        }
+        if (kMasked && __ballot(poison) != 0) {
+            // The accumulators of this lane hold channels of one group of each
+            // plane (pieces 4 quad + r): NaN for the rows that see a NaN token
+            // of that group.
+            const int og = D == 64 ? quad >> 1 : p * 4 + quad;
+            for (int tok = 0; tok < kTile; ++tok) {
+                const int j = tok0 + tok;
+                if (j > last || tile[L::v_scale(tok, og)] != 255u) continue;
+                #pragma unroll
+                for (int mt = 0; mt < kAct; ++mt) {
+                    if (j > st.pos[mt] || (a.window > 0 && j <= st.pos[mt] - a.window)) continue;
+                    #pragma unroll
+                    for (int c = 0; c < S::kChans; ++c) st.o[mt][p][c] *= NAN;
+                }
+            }
+        }
+    }
+}
+
+// This wavefront's tiles t0 + wave, t0 + wave + kWaves, ...; the next tile's
+// bytes are in flight while one is worked on.
+template <int D, int kMT, int kAct>
+__device__ __forceinline__ void tile_loop(State<D, kMT>& st, const Lds<D, kMT>& sh,
+                                          const AttendArgs& a, const Work& wk, const Block& blk,
+                                          int lane, int wave) {
+    using L = Tile<D>;
+    // Tokens that every row of the block sees: [all_lo, all_hi).
+    const int last = blk.ctx + blk.len - 1, all_hi = blk.ctx + 1;
+    const int all_lo = a.window > 0 ? max(0, last - a.window + 1) : 0;
+    auto locate = [&](int t) {
+        if (t >= wk.t1) return -1ll;
+        const long long at = a.pages.tile(wk.b, wk.h, t * kTile, L::kBytes);
+        if (at < 0 && lane == 0) flag(a.status, SV_FLAG_BAD_PAGE);
+        return at;
+    };
+    auto work = [&](const Frag<D>& f, long long at, int t) {
+        if (at < 0) return;
+        const int tok0 = t * kTile;
+        if (tok0 < all_lo || tok0 + kTile > all_hi) {
+            tile_step<D, kMT, kAct, true>(st, f, sh, a, lane, tok0, last, a.cache + at);
+        } else {
+            tile_step<D, kMT, kAct, false>(st, f, sh, a, lane, tok0, last, a.cache + at);
+        }
+    };
+    Frag<D> f[2];
+    int t = wk.t0 + wave;
+    long long at[2] = {locate(t), -1};
+    if (at[0] >= 0) f[0].load(a.cache + at[0], lane);
+    while (t < wk.t1) {
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            at[1 - i] = locate(t + kWaves);
+            if (at[1 - i] >= 0) f[1 - i].load(a.cache + at[1 - i], lane);
+            work(f[i], at[i], t);
+            t += kWaves;
+        }
+    }
+}
+
+// Finds the split of workgroup `slot`; false when there is none.
+template <int D, int kMT>
+__device__ bool find_work(const AttendArgs& a, Lds<D, kMT>& sh, Work& wk) {
+    const int slot = blockIdx.x;
+    if (a.direct) {
+        wk.rb = slot % a.row_blocks;
+        wk.h = slot / a.row_blocks % a.pages.heads;
+        wk.b = slot / a.row_blocks / a.pages.heads;
+        const Block blk = block_of(a.ctx_lens, a.budgets, wk.b, a.K + 1, a.pages, nullptr, false);
+        if (wk.rb * 16 * kMT >= blk.len * a.group) return false;
+        const Span s = span_of(blk, a.window);
+        wk.t0 = s.first;
+        wk.t1 = s.end;
+        wk.whole = true;
+        return true;
+    }
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int per = (a.B + 255) / 256;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    // Tiles of a request (0: nothing to do) and its units.
+    auto tiles_of = [&](int b, int& units, int& first) {
+        const Block blk = block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, nullptr, false);
+        units = (blk.len * a.group + 16 * kMT - 1) / (16 * kMT) * a.pages.heads;
+        if (blk.len == 0) return 0;
+        const Span s = span_of(blk, a.window);
+        first = s.first;
+        return s.size();
+    };
+    auto block_total = [&](unsigned v, unsigned& before) {      // inclusive scan over threads
+        unsigned incl = v;
+        #pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const unsigned u = __shfl_up(incl, o, 64);
+            if (lane >= o) incl += u;
+        }
+        __syncthreads();
+        if (lane == 63) sh.scan[wave] = incl;
+        __syncthreads();
+        before = incl - v;
+        unsigned total = 0;
+        #pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) before += sh.scan[w];
+            total += sh.scan[w];
+        }
+        return total;
+    };
+    if (tid == 0) sh.found[0] = -1;
+    int units, first = 0;
+    unsigned mine = 0, before;
+    for (int b = b0; b < b1; ++b) mine += tiles_of(b, units, first) * units;
+    const unsigned total = block_total(mine, before);
+    unsigned chunk = max((total + kManySplits - 1) / kManySplits,
+                         min((total + kFewSplits - 1) / kFewSplits, (unsigned)kChunk));
+    chunk = max(chunk, (unsigned)kLeastChunk);
+    mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int n = tiles_of(b, units, first);
+        mine += (n + chunk - 1) / chunk * units;
+    }
+    block_total(mine, before);
+    for (int b = b0; b < b1; ++b) {
+        const int n = tiles_of(b, units, first);
+        const unsigned count = (n + chunk - 1) / chunk * units;
+        if ((unsigned)slot >= before && (unsigned)slot < before + count) {
+            const int in = slot - before, split = in / units;
+            sh.found[0] = b;
+            sh.found[1] = in % units;
+            sh.found[2] = first + split * chunk;
+            sh.found[3] = min(first + (split + 1) * (int)chunk, first + n) | (n <= (int)chunk ? 1 << 30 : 0);
+            if (in == 0) a.cut[b] = make_int2(before, chunk);
+        }
+        before += count;
+    }
+    __syncthreads();
+    if (sh.found[0] < 0) return false;
+    wk.b = __builtin_amdgcn_readfirstlane(sh.found[0]);
+    const int unit = __builtin_amdgcn_readfirstlane(sh.found[1]);
+    wk.h = unit % a.pages.heads;
+    wk.rb = unit / a.pages.heads;
+    wk.t0 = __builtin_amdgcn_readfirstlane(sh.found[2]);
+    const int end = __builtin_amdgcn_readfirstlane(sh.found[3]);
+    wk.t1 = end & ((1 << 30) - 1);
+    wk.whole = end >> 30;
+    return true;
+}
+
+// Accumulators of more than 96 registers a lane leave one wave per SIMD.
+template <int D, int kMT>
+__global__ __launch_bounds__(256, (D * kMT <= 384 ? 2 : 1)) void attend_kernel(AttendArgs a) {
+    using S = State<D, kMT>;
+    constexpr int kPlanes = S::kPlanes, kChans = S::kChans;
     __shared__ Lds<D, kMT> sh;
     const int lane = threadIdx.x & 63, x = lane & 15, quad = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int id = blockIdx.x;
-    const int split = id % a.splits;
-    id /= a.splits;
-    const int unit = id;
-    const int rb = id % a.row_blocks;
-    id /= a.row_blocks;
-    const int h = id % a.pages.heads, b = id / a.pages.heads;
 
-    const Block blk = block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, a.status,
-                               split == 0 && rb == 0 && h == 0 && threadIdx.x == 0);
+    if (blockIdx.x == 0) {            // report bad budgets and lengths, once per call
+        for (int b = threadIdx.x; b < a.B; b += 256) {
+            block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, a.status, true);
+        }
+    }
+    Work wk;
+    if (!find_work<D, kMT>(a, sh, wk)) return;
+    const Block blk = block_of(a.ctx_lens, a.budgets, wk.b, a.K + 1, a.pages, nullptr, false);
     const int rows = blk.len * a.group;
-    if (rb * 16 * kMT >= rows) return;
-    const Span span = span_of(blk, a.window);
-    const int t0 = span.first + split * a.chunk, t1 = min(t0 + a.chunk, span.end);
-    if (t0 >= t1) return;
 
-    // This lane's rows and their queries.
-    int pos[kMT];                 // the row's position; rows past the block see nothing
-    bf16x8 q[kMT][kKeySteps];
-    #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
-        const int r = (rb * kMT + mt) * 16 + x;
-        const int t = r / a.group;
-        const bool live = r < rows;
-        pos[mt] = live ? blk.ctx + t : -1;
-        const uint16_t* src = a.q + ((long long)b * (a.K + 1) + t) * a.q_stride +
-                              (h * a.group + (r - t * a.group)) * D;
-        #pragma unroll
-        for (int s = 0; s < kKeySteps; ++s) {
-            // Unit of plane s / kUnitSteps and this quad, 8 channels of step s.
-            const int ch = (s / kUnitSteps * 4 + quad) * (8 * kUnitSteps) + 8 * (s % kUnitSteps);
-            u32x4 w = {0, 0, 0, 0};
-            if (live) w = *reinterpret_cast<const u32x4*>(src + ch);
-            q[mt][s] = __builtin_bit_cast(bf16x8, w);
+    // The queries as right operands: lane holds row x, 8 channels of its unit.
+    for (int i = wave; i < kMT * S::kSteps; i += kWaves) {
+        const int mt = i / S::kSteps, s = i % S::kSteps;
+        const int r = (wk.rb * kMT + mt) * 16 + x, t = r / a.group;
+        u32x4 w = {0, 0, 0, 0};
+        if (r < rows) {
+            const int ch = (s / S::kUnitSteps * 4 + quad) * (8 * S::kUnitSteps) + 8 * (s % S::kUnitSteps);
+            w = *reinterpret_cast<const u32x4*>(a.q + ((long long)wk.b * (a.K + 1) + t) * a.q_stride +
+                                                (wk.h * a.group + (r - t * a.group)) * D + ch);
+            if (a.negate) w ^= u32x4{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
         }
+        sh.q[mt][s][lane] = w;
     }
-
-    f32x4 o[kMT][kPlanes][kChans];
-    float m[kMT], l[kMT];
+    S st;
     #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
-        m[mt] = kNegInf;
-        l[mt] = 0.0f;
+        const int r = (wk.rb * kMT + mt) * 16 + x;
+        st.pos[mt] = r < rows ? blk.ctx + r / a.group : -1;
+        st.ref[mt] = kNegInf;
+        st.sum[mt] = 0.0f;
         #pragma unroll
         for (int p = 0; p < kPlanes; ++p) {
             #pragma unroll
-            for (int j = 0; j < kChans; ++j) o[mt][p][j] = f32x4{0, 0, 0, 0};
+            for (int j = 0; j < kChans; ++j) st.o[mt][p][j] = f32x4{0, 0, 0, 0};
         }
     }
+    __syncthreads();
 
-    // Tokens that every row of the block sees: [all_lo, all_hi).
-    const int last = blk.ctx + blk.len - 1;
-    const int all_hi = blk.ctx + 1;
-    const int all_lo = a.window > 0 ? max(0, last - a.window + 1) : 0;
-
-    for (int tile_at = t0 + wave; tile_at < t1; tile_at += kWaves) {
-        const int tok0 = tile_at * kTile;
-        const long long at = a.pages.tile(b, h, tok0, L::kBytes);
-        if (at < 0) {
-            if (lane == 0) flag(a.status, SV_FLAG_BAD_PAGE);
-            continue;
-        }
-        const uint8_t* tile = a.cache + at;
-        const bool masked = tok0 < all_lo || tok0 + kTile > all_hi;
-
-        // Scores of 2 x 16 tokens (lane: tokens 16 half + 4 quad + r).
-        f32x4 z[kMT][2];
-        #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) z[mt][half] = f32x4{0, 0, 0, 0};
-            #pragma unroll
-            for (int p = 0; p < kPlanes; ++p) {
-                const int g = D == 64 ? quad >> 1 : p * 4 + quad;
-                const float s = scale_of(tile[L::kKScales + g * 32 + x * 2 + half]);
-                unsigned w[kUnitSteps];
-                __builtin_memcpy(w, tile + half * (8 * D) + ((p * 4 + quad) * 16 + x) * L::U, L::U);
-                #pragma unroll
-                for (int j = 0; j < kUnitSteps; ++j) {
-                    const u32x4 kw = {decode2<0>(w[j], s), decode2<1>(w[j], s),
-                                      decode2<2>(w[j], s), decode2<3>(w[j], s)};
-                    const bf16x8 kf = __builtin_bit_cast(bf16x8, kw);
-                    #pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt) {
-                        z[mt][half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            kf, q[mt][p * kUnitSteps + j], z[mt][half], 0, 0, 0);
-                    }
-                }
-            }
-        }
-
-        // Probabilities and running statistics.
-        bf16x8 pf[kMT];
-        #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-            float s[8];
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] = z[mt][i >> 2][i & 3] * a.c;
-            if (masked) {
-                const int lo = a.window > 0 ? pos[mt] - a.window : -1;
-                #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = tok0 + 16 * (i >> 2) + 4 * quad + (i & 3);
-                    if (j > pos[mt] || j <= lo) s[i] = kNegInf;
-                }
-            }
-            float top = s[0];
-            #pragma unroll
-            for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i]);
-            top = fmaxf(quad_max(top), m[mt]);
-            // A row that has seen nothing yet keeps -inf; its terms are 0.
-            const float ref = top == kNegInf ? 0.0f : top;
-            const float keep = exp2f(m[mt] - ref);
-            m[mt] = top;
-            float sum = 0.0f;
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                s[i] = exp2f(s[i] - ref);
-                sum += s[i];
-            }
-            l[mt] = l[mt] * keep + sum;
-            #pragma unroll
-            for (int p = 0; p < kPlanes; ++p) {
-                #pragma unroll
-                for (int j = 0; j < kChans; ++j) o[mt][p][j] *= keep;
-            }
-            const u32x4 pw = {pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]), pack_bf16(s[4], s[5]),
-                              pack_bf16(s[6], s[7])};
-            pf[mt] = __builtin_bit_cast(bf16x8, pw);
-        }
-
-        // Values: 8 tokens (4 quad + r of both halves) x kChans channels.
-        #pragma unroll
-        for (int p = 0; p < kPlanes; ++p) {
-            const int g = D == 64 ? x >> 3 : p * 4 + (x >> 2);
-            unsigned sc[2];
-            __builtin_memcpy(sc, tile + L::kVScales + (g * 4 + quad) * 8, 8);
-            unsigned w[8];
-            #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint8_t* src =
-                    tile + L::kVCodes + (((p * 2 + half) * 4 + quad) * 16 + x) * (4 * L::C);
-                if constexpr (D == 64) {
-                    unsigned u[2];
-                    __builtin_memcpy(u, src, 8);
-                    w[4 * half] = u[0] & 0xffffu;
-                    w[4 * half + 1] = u[0] >> 16;
-                    w[4 * half + 2] = u[1] & 0xffffu;
-                    w[4 * half + 3] = u[1] >> 16;
-                } else {
-                    __builtin_memcpy(&w[4 * half], src, 16);
-                }
-            }
-            float vs[8];
-            bool poison = false;
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                unsigned byte = (sc[i >> 2] >> (8 * (i & 3))) & 255u;
-                if (masked) {
-                    // What some row does not see must not reach it as 0 * NaN:
-                    // tokens past the block hold anything and are cleared;
-                    // NaN groups of tokens that other rows see are cleared
-                    // here and put into those rows below.
-                    const int j = tok0 + 16 * (i >> 2) + 4 * quad + (i & 3);
-                    const bool nan = byte == 255u;
-                    poison |= nan && j <= last;
-                    if (nan || j > last) {
-                        byte = 127u;
-                        w[i] = 0;
-                    }
-                }
-                vs[i] = scale_of(byte);
-            }
-            #pragma unroll
-            for (int cb = 0; cb < kChans / 2; ++cb) {
-                unsigned e[8];
-                #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    e[i] = cb == 0   ? decode2<0>(w[i], vs[i])
-                           : cb == 1 ? decode2<1>(w[i], vs[i])
-                           : cb == 2 ? decode2<2>(w[i], vs[i])
-                                     : decode2<3>(w[i], vs[i]);
-                }
-                u32x4 even, odd;
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    even[i] = __builtin_amdgcn_perm(e[2 * i + 1], e[2 * i], 0x05040100u);
-                    odd[i] = __builtin_amdgcn_perm(e[2 * i + 1], e[2 * i], 0x07060302u);
-                }
-                #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) {
-                    o[mt][p][2 * cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, even), pf[mt], o[mt][p][2 * cb], 0, 0, 0);
-                    o[mt][p][2 * cb + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, odd), pf[mt], o[mt][p][2 * cb + 1], 0, 0, 0);
-                }
-            }
-            if (masked && __ballot(poison) != 0) {
-                // The accumulators of this lane hold channels of one group of
-                // each plane (pieces 4 quad + r): NaN for the rows that see a
-                // NaN token of that group.
-                const int og = D == 64 ? quad >> 1 : p * 4 + quad;
-                for (int tok = 0; tok < kTile; ++tok) {
-                    const int j = tok0 + tok;
-                    if (j > last || tile[L::v_scale(tok, og)] != 255u) continue;
-                    #pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt) {
-                        if (j > pos[mt] || (a.window > 0 && j <= pos[mt] - a.window)) continue;
-                        #pragma unroll
-                        for (int c = 0; c < kChans; ++c) o[mt][p][c] *= NAN;
-                    }
-                }
-            }
-        }
-    }
+    const int act = min((rows - wk.rb * 16 * kMT + 15) / 16, kMT);
+    if (kMT >= 4 && act == 4) tile_loop<D, kMT, (kMT < 4 ? 1 : 4)>(st, sh, a, wk, blk, lane, wave);
+    else if (kMT >= 3 && act == 3) tile_loop<D, kMT, (kMT < 3 ? 1 : 3)>(st, sh, a, wk, blk, lane, wave);
+    else if (kMT >= 2 && act == 2) tile_loop<D, kMT, (kMT < 2 ? 1 : 2)>(st, sh, a, wk, blk, lane, wave);
+    else tile_loop<D, kMT, 1>(st, sh, a, wk, blk, lane, wave);
 
     // Join the waves: component r of every accumulator in round r, so that
     // wave r ends with kChans consecutive channels per (row, plane).
     #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
-        const float sum = quad_sum(l[mt]);
+        const float sum = quad_sum(st.sum[mt]);
         if (quad == 0) {
-            sh.m[wave][mt][x] = m[mt];
-            sh.l[wave][mt][x] = sum;
+            sh.ref[wave][mt][x] = st.ref[mt];
+            sh.sum[wave][mt][x] = sum;
         }
     }
     __syncthreads();
-    float factor[kMT], total[kMT], top[kMT];
+    float total[kMT], top[kMT];
     #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
         top[mt] = kNegInf;
         #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top[mt] = fmaxf(top[mt], sh.m[w][mt][x]);
+        for (int w = 0; w < kWaves; ++w) top[mt] = fmaxf(top[mt], sh.ref[w][mt][x]);
         const float ref = top[mt] == kNegInf ? 0.0f : top[mt];
-        factor[mt] = exp2f(m[mt] - ref);
+        const float mine = exp2_fast((st.ref[mt] - ref) * a.c);
         total[mt] = 0.0f;
         #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            total[mt] += sh.l[w][mt][x] * exp2f(sh.m[w][mt][x] - ref);
+            total[mt] += sh.sum[w][mt][x] * exp2_fast((sh.ref[w][mt][x] - ref) * a.c);
+        }
+        #pragma unroll
+        for (int p = 0; p < kPlanes; ++p) {
+            #pragma unroll
+            for (int j = 0; j < kChans; ++j) st.o[mt][p][j] *= mine;
         }
     }
     f32x4 mine[Lds<D, kMT>::kPieces];
@@ -346,9 +535,8 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
             for (int p = 0; p < kPlanes; ++p) {
                 #pragma unroll
                 for (int c = 0; c < kChans; c += 4) {
-                    const f32x4 v = {o[mt][p][c][r] * factor[mt], o[mt][p][c + 1][r] * factor[mt],
-                                     o[mt][p][c + 2][r] * factor[mt],
-                                     o[mt][p][c + 3][r] * factor[mt]};
+                    const f32x4 v = {st.o[mt][p][c][r], st.o[mt][p][c + 1][r],
+                                     st.o[mt][p][c + 2][r], st.o[mt][p][c + 3][r]};
                     sh.o[wave][((mt * kPlanes + p) * kChans + c) / 4][lane] = v;
                 }
             }
@@ -357,34 +545,33 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
         if (wave == r) {
             #pragma unroll
             for (int i = 0; i < Lds<D, kMT>::kPieces; ++i) {
-                mine[i] = sh.o[0][i][lane] + sh.o[1][i][lane] + sh.o[2][i][lane] + sh.o[3][i][lane];
+                mine[i] = (sh.o[0][i][lane] + sh.o[1][i][lane]) + (sh.o[2][i][lane] + sh.o[3][i][lane]);
             }
         }
         __syncthreads();
     }
 
-    const bool whole = a.splits == 1;
     #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
-        const int r = (rb * kMT + mt) * 16 + x;
+        const int r = (wk.rb * kMT + mt) * 16 + x;
         if (r >= rows) continue;
         const int t = r / a.group;
-        const long long part = ((long long)unit * a.splits + split) * (16 * kMT) + mt * 16 + x;
-        if (!whole && wave == 0 && quad == 0) a.part_ml[part] = make_float2(top[mt], total[mt]);
+        const long long part = (long long)blockIdx.x * (16 * kMT) + mt * 16 + x;
+        if (!wk.whole && wave == 0 && quad == 0) a.part_ml[part] = make_float2(top[mt], total[mt]);
         const float inv = 1.0f / total[mt];
         #pragma unroll
         for (int p = 0; p < kPlanes; ++p) {
             const int ch = p * 128 + (4 * quad + wave) * kChans;
             const f32x4* v = &mine[(mt * kPlanes + p) * kChans / 4];
-            if (whole) {
-                uint16_t* dst = a.out + (((long long)b * (a.K + 1) + t) * a.Hq + h * a.group +
+            if (wk.whole) {
+                uint16_t* dst = a.out + (((long long)wk.b * (a.K + 1) + t) * a.Hq + wk.h * a.group +
                                          (r - t * a.group)) * D + ch;
                 unsigned w[kChans / 2];
                 #pragma unroll
                 for (int c = 0; c < kChans; c += 2) {
                     w[c / 2] = pack_bf16(v[c / 4][c % 4] * inv, v[c / 4][c % 4 + 1] * inv);
                 }
-                __builtin_memcpy(dst, w, 2 * kChans);
+                __builtin_memcpy(__builtin_assume_aligned(dst, 2 * kChans), w, 2 * kChans);
             } else {
                 #pragma unroll
                 for (int c = 0; c < kChans; c += 4) {
@@ -398,46 +585,48 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
 // Joins the splits of one row: one wavefront per row, in the order of the
 // splits.
 template <int D, int kMT>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int B) {
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     const int lane = threadIdx.x & 63;
     const int T = a.K + 1;
-    const long long i = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (i >= (long long)B * T * a.Hq) return;
-    const int head = (int)(i % a.Hq);
-    const int t = (int)(i / a.Hq % T), b = (int)(i / a.Hq / T);
+    const int i = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (i >= a.B * T * a.Hq) return;
+    const int head = i % a.Hq, t = i / a.Hq % T, b = i / a.Hq / T;
     const Block blk = block_of(a.ctx_lens, a.budgets, b, T, a.pages, nullptr, false);
     if (t >= blk.len) return;
-    const Span span = span_of(blk, a.window);
-    const int n = (span.end - span.first + a.chunk - 1) / a.chunk;
+    const int2 cut = a.cut[b];
+    const int n = (span_of(blk, a.window).size() + cut.y - 1) / cut.y;
+    if (n == 1) return;
+    const int units = (blk.len * a.group + 16 * kMT - 1) / (16 * kMT) * a.pages.heads;
     const int h = head / a.group, r = t * a.group + head % a.group;
     const int rb = r / (16 * kMT), in = r % (16 * kMT);
-    const long long unit = ((long long)b * a.pages.heads + h) * a.row_blocks + rb;
-    const long long part = unit * a.splits * (16 * kMT) + in;
+    const long long part = (long long)(cut.x + rb * a.pages.heads + h) * (16 * kMT) + in;
+    const long long step = (long long)units * (16 * kMT);
     float top = kNegInf;
-    for (int s = 0; s < n; ++s) top = fmaxf(top, a.part_ml[part + (long long)s * 16 * kMT].x);
+    for (int s = 0; s < n; ++s) top = fmaxf(top, a.part_ml[part + s * step].x);
     const float ref = top == kNegInf ? 0.0f : top;
     float sum = 0.0f;
     float acc[D / 64] = {};
     for (int s = 0; s < n; ++s) {
-        const long long p = part + (long long)s * 16 * kMT;
+        const long long p = part + s * step;
         const float2 ml = a.part_ml[p];
-        const float f = exp2f(ml.x - ref);
+        const float f = exp2_fast((ml.x - ref) * a.c);
         sum += ml.y * f;
         #pragma unroll
         for (int c = 0; c < D / 64; ++c) acc[c] += a.part_o[p * D + lane * (D / 64) + c] * f;
     }
     const float inv = 1.0f / sum;
-    uint16_t* dst = a.out + i * D + lane * (D / 64);
+    uint16_t* dst = a.out + (long long)i * D + lane * (D / 64);
     #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
         dst[c] = __builtin_bit_cast(uint16_t, (__bf16)(acc[c] * inv));
     }
 }
 
-// How a call is cut: rows per wavefront, row blocks, splits.
+// What the host fixes of a call: rows per wavefront, row blocks, workgroups.
 struct Plan {
-    int mt, row_blocks, chunk, splits;
-    long long units;
+    int mt, row_blocks;
+    bool direct;
+    long long slots;
 };
 
 Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_pages, int window) {
@@ -446,22 +635,21 @@ Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_p
     const int most = D == 256 ? 2 : 4;       // accumulators: kMT D / 4 registers a lane
     p.mt = (rows + 15) / 16 < most ? (rows + 15) / 16 : most;
     p.row_blocks = (rows + 16 * p.mt - 1) / (16 * p.mt);
-    p.units = (long long)B * kv_heads * p.row_blocks;
+    const long long units = (long long)B * kv_heads * p.row_blocks;
+    p.direct = units >= kDirectUnits;
+    // Splits: every unit's last one, and no more than kManySplits full ones
+    // or than the page table row can hold.
     long long tokens = (long long)max_pages * page_size;
     if (window > 0 && tokens > (long long)window + K + kTile) tokens = (long long)window + K + kTile;
-    const int tiles = (int)((tokens + kTile - 1) / kTile) + 1;
-    // Enough workgroups for the 256 CUs, no split shorter than 16 tiles.
-    long long splits = (1024 + p.units - 1) / p.units;
-    const long long longest = (tiles + 15) / 16;
-    if (splits > longest) splits = longest;
-    p.chunk = (int)((tiles + splits - 1) / splits);
-    p.splits = (tiles + p.chunk - 1) / p.chunk;
+    const long long tiles = (tokens + kTile - 1) / kTile + 1;
+    const long long per_unit = (tiles + kLeastChunk - 1) / kLeastChunk;
+    p.slots = p.direct ? units : std::min(units + kManySplits, units * per_unit);
     return p;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-size_t parts_of(const Plan& p) { return (size_t)p.units * p.splits * 16 * p.mt; }
+size_t parts_of(const Plan& p) { return (size_t)p.slots * 16 * p.mt; }
 
 bool shape_ok(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_pages, int window) {
     return B >= 0 && B <= SV_MAX_BATCH && K >= 0 && K <= SV_MAX_K && window >= 0 &&
@@ -470,13 +658,13 @@ bool shape_ok(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_
 }
 
 template <int D, int kMT>
-void launch(const AttendArgs& a, const Plan& p, int B, hipStream_t s) {
-    hipLaunchKernelGGL((attend_kernel<D, kMT>), dim3((unsigned)(p.units * p.splits)), dim3(256), 0,
-                       s, a);
-    if (p.splits > 1) {
-        const long long rows = (long long)B * (a.K + 1) * a.Hq;
+void launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
+    hipLaunchKernelGGL((attend_kernel<D, kMT>), dim3((unsigned)p.slots), dim3(256), 0, s, a);
+    if (!p.direct) {
+        // Fewer than kDirectUnits units: the rows fit 32 bits.
+        const int rows = a.B * (a.K + 1) * a.Hq;
         hipLaunchKernelGGL((attend_join_kernel<D, kMT>), dim3((unsigned)((rows + 3) / 4)),
-                           dim3(256), 0, s, a, B);
+                           dim3(256), 0, s, a);
     }
 }
 
@@ -489,8 +677,9 @@ extern "C" size_t spec_verify_attention_workspace_bytes(int B, int K, int q_head
         return 0;
     }
     const Plan p = plan_of(B, K, q_heads, kv_heads, head_dim, page_size, max_pages, window);
-    if (p.splits == 1) return 256;
-    return round256(parts_of(p) * head_dim * sizeof(float)) + round256(parts_of(p) * sizeof(float2));
+    if (p.direct) return 256;
+    return round256((size_t)B * sizeof(int2)) + round256(parts_of(p) * sizeof(float2)) +
+           parts_of(p) * head_dim * sizeof(float);
 }
 
 extern "C" int spec_verify_attention(const void* queries, int64_t query_stride, const void* cache,
@@ -527,31 +716,35 @@ extern "C" int spec_verify_attention(const void* queries, int64_t query_stride, 
     a.budgets = budgets;
     a.out = static_cast<uint16_t*>(out);
     a.status = out_status;
-    a.part_o = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float2*>(
-        static_cast<char*>(workspace) +
-        (p.splits == 1 ? 0 : round256(parts_of(p) * head_dim * sizeof(float))));
+    char* ws = static_cast<char*>(workspace);
+    a.cut = reinterpret_cast<int2*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(ws + round256((size_t)B * sizeof(int2)));
+    a.part_o = reinterpret_cast<float*>(ws + round256((size_t)B * sizeof(int2)) +
+                                        round256(parts_of(p) * sizeof(float2)));
     a.pages = make_pages(page_table, kv_heads, page_size, max_pages, num_pages);
+    a.B = B;
     a.K = K;
     a.Hq = q_heads;
     a.group = q_heads / kv_heads;
     a.row_blocks = p.row_blocks;
-    a.chunk = p.chunk;
-    a.splits = p.splits;
     a.window = window;
-    a.c = (float)((double)scale * 1.4426950408889634);
+    a.direct = p.direct;
+    a.negate = scale < 0.0f;
+    // A scale of 0 becomes 2^-126, under which every seen score is as good as 0
+    // and an unseen one (-inf) still is -inf.
+    a.c = std::max((float)(std::fabs((double)scale) * 1.4426950408889634), FLT_MIN);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     switch (head_dim * 8 + p.mt) {
-        case 64 * 8 + 1: launch<64, 1>(a, p, B, s); break;
-        case 64 * 8 + 2: launch<64, 2>(a, p, B, s); break;
-        case 64 * 8 + 3: launch<64, 3>(a, p, B, s); break;
-        case 64 * 8 + 4: launch<64, 4>(a, p, B, s); break;
-        case 128 * 8 + 1: launch<128, 1>(a, p, B, s); break;
-        case 128 * 8 + 2: launch<128, 2>(a, p, B, s); break;
-        case 128 * 8 + 3: launch<128, 3>(a, p, B, s); break;
-        case 128 * 8 + 4: launch<128, 4>(a, p, B, s); break;
-        case 256 * 8 + 1: launch<256, 1>(a, p, B, s); break;
-        default: launch<256, 2>(a, p, B, s); break;
+        case 64 * 8 + 1: launch<64, 1>(a, p, s); break;
+        case 64 * 8 + 2: launch<64, 2>(a, p, s); break;
+        case 64 * 8 + 3: launch<64, 3>(a, p, s); break;
+        case 64 * 8 + 4: launch<64, 4>(a, p, s); break;
+        case 128 * 8 + 1: launch<128, 1>(a, p, s); break;
+        case 128 * 8 + 2: launch<128, 2>(a, p, s); break;
+        case 128 * 8 + 3: launch<128, 3>(a, p, s); break;
+        case 128 * 8 + 4: launch<128, 4>(a, p, s); break;
+        case 256 * 8 + 1: launch<256, 1>(a, p, s); break;
+        default: launch<256, 2>(a, p, s); break;
     }
     return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
