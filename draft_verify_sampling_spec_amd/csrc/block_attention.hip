@@ -181,6 +181,7 @@ __device__ __forceinline__ void tile_step(State<D, kMT>& st, const Frag<D>& f,
         const float s[2] = {scale_of(f.ks[p] & 255u), scale_of(f.ks[p] >> 8)};
         #pragma unroll
         for (int j = 0; j < S::kUnitSteps; ++j) {
+            __builtin_amdgcn_sched_barrier(0);
             bf16x8 kf[2];
             #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -203,6 +204,7 @@ __device__ __forceinline__ void tile_step(State<D, kMT>& st, const Frag<D>& f,
     // Probabilities 2^((z - ref) c). The reference follows the running
     // maximum only when a score exceeds it by 8 / c: until then terms stay
     // below 2^8 and nothing has to be rescaled.
+    __builtin_amdgcn_sched_barrier(0);
     bf16x8 pf[kAct];
     #pragma unroll
     for (int mt = 0; mt < kAct; ++mt) {
@@ -275,6 +277,7 @@ __device__ __forceinline__ void tile_step(State<D, kMT>& st, const Frag<D>& f,
         }
         #pragma unroll
         for (int cb = 0; cb < S::kChans / 2; ++cb) {
+            __builtin_amdgcn_sched_barrier(0);
             unsigned e[8];
             #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -316,41 +319,53 @@ __device__ __forceinline__ void tile_step(State<D, kMT>& st, const Frag<D>& f,
     }
 }
 
-// This wavefront's tiles t0 + wave, t0 + wave + kWaves, ...; the next tile's
-// bytes are in flight while one is worked on.
+// This wavefront's share of the tiles [t0, t1). The tiles that every row sees
+// whole come in a loop that keeps the next tile's bytes in flight; the few at
+// the ends that some row does not see whole (the block's own, and the windows'
+// edges) are worked on one by one while the loop's first bytes are on their
+// way.
 template <int D, int kMT, int kAct>
 __device__ __forceinline__ void tile_loop(State<D, kMT>& st, const Lds<D, kMT>& sh,
                                           const AttendArgs& a, const Work& wk, const Block& blk,
                                           int lane, int wave) {
     using L = Tile<D>;
-    // Tokens that every row of the block sees: [all_lo, all_hi).
-    const int last = blk.ctx + blk.len - 1, all_hi = blk.ctx + 1;
+    const int last = blk.ctx + blk.len - 1;
+    // Tiles [u0, u1) of this split lie wholly in [all_lo, ctx + 1), the tokens
+    // that every row of the block sees.
     const int all_lo = a.window > 0 ? max(0, last - a.window + 1) : 0;
+    const int u0 = min(max(wk.t0, (all_lo + kTile - 1) / kTile), wk.t1);
+    const int u1 = max(u0, min(wk.t1, (blk.ctx + 1) / kTile));
+    // A tile whose page is bad is flagged and skipped; the first tile of the
+    // cache stands in for its bytes.
     auto locate = [&](int t) {
-        if (t >= wk.t1) return -1ll;
-        const long long at = a.pages.tile(wk.b, wk.h, t * kTile, L::kBytes);
+        const long long at = a.pages.tile<true>(wk.b, wk.h, t * kTile, L::kBytes);
         if (at < 0 && lane == 0) flag(a.status, SV_FLAG_BAD_PAGE);
         return at;
     };
-    auto work = [&](const Frag<D>& f, long long at, int t) {
-        if (at < 0) return;
-        const int tok0 = t * kTile;
-        if (tok0 < all_lo || tok0 + kTile > all_hi) {
-            tile_step<D, kMT, kAct, true>(st, f, sh, a, lane, tok0, last, a.cache + at);
-        } else {
-            tile_step<D, kMT, kAct, false>(st, f, sh, a, lane, tok0, last, a.cache + at);
-        }
-    };
     Frag<D> f[2];
-    int t = wk.t0 + wave;
-    long long at[2] = {locate(t), -1};
-    if (at[0] >= 0) f[0].load(a.cache + at[0], lane);
-    while (t < wk.t1) {
+    int t = u0 + wave;
+    long long at[2] = {-1, -1};
+    if (t < u1) {
+        at[0] = locate(t);
+        f[0].load(a.cache + max(at[0], 0ll), lane);
+    }
+    const int edges = (u0 - wk.t0) + (wk.t1 - u1);
+    for (int i = kWaves - 1 - wave; i < edges; i += kWaves) {
+        const int e = wk.t0 + i < u0 ? wk.t0 + i : u1 + (i - (u0 - wk.t0));
+        const long long edge = locate(e);
+        if (edge < 0) continue;
+        Frag<D> g;
+        g.load(a.cache + edge, lane);
+        tile_step<D, kMT, kAct, true>(st, g, sh, a, lane, e * kTile, last, a.cache + edge);
+    }
+    while (t < u1) {
         #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            at[1 - i] = locate(t + kWaves);
-            if (at[1 - i] >= 0) f[1 - i].load(a.cache + at[1 - i], lane);
-            work(f[i], at[i], t);
+            // Past the end: the same tile again, from the cache and unused.
+            const bool more = t + kWaves < u1;
+            at[1 - i] = more ? locate(t + kWaves) : -1;
+            f[1 - i].load(a.cache + max(more ? at[1 - i] : at[i], 0ll), lane);
+            if (at[i] >= 0) tile_step<D, kMT, kAct, false>(st, f[i], sh, a, lane, t * kTile, last, nullptr);
             t += kWaves;
         }
     }
@@ -445,7 +460,7 @@ __device__ bool find_work(const AttendArgs& a, Lds<D, kMT>& sh, Work& wk) {
 
 // Accumulators of more than 96 registers a lane leave one wave per SIMD.
 template <int D, int kMT>
-__global__ __launch_bounds__(256, (D * kMT <= 384 ? 2 : 1)) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs a) {
     using S = State<D, kMT>;
     constexpr int kPlanes = S::kPlanes, kChans = S::kChans;
     __shared__ Lds<D, kMT> sh;
@@ -496,8 +511,8 @@ __global__ __launch_bounds__(256, (D * kMT <= 384 ? 2 : 1)) void attend_kernel(A
     else if (kMT >= 2 && act == 2) tile_loop<D, kMT, (kMT < 2 ? 1 : 2)>(st, sh, a, wk, blk, lane, wave);
     else tile_loop<D, kMT, 1>(st, sh, a, wk, blk, lane, wave);
 
-    // Join the waves: component r of every accumulator in round r, so that
-    // wave r ends with kChans consecutive channels per (row, plane).
+    // Join the waves: component r of every accumulator in round r, of which
+    // wave r writes kChans consecutive channels per (row, plane).
     #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
         const float sum = quad_sum(st.sum[mt]);
@@ -526,7 +541,6 @@ __global__ __launch_bounds__(256, (D * kMT <= 384 ? 2 : 1)) void attend_kernel(A
             for (int j = 0; j < kChans; ++j) st.o[mt][p][j] *= mine;
         }
     }
-    f32x4 mine[Lds<D, kMT>::kPieces];
     #pragma unroll
     for (int r = 0; r < 4; ++r) {
         #pragma unroll
@@ -544,41 +558,44 @@ __global__ __launch_bounds__(256, (D * kMT <= 384 ? 2 : 1)) void attend_kernel(A
         __syncthreads();
         if (wave == r) {
             #pragma unroll
-            for (int i = 0; i < Lds<D, kMT>::kPieces; ++i) {
-                mine[i] = (sh.o[0][i][lane] + sh.o[1][i][lane]) + (sh.o[2][i][lane] + sh.o[3][i][lane]);
+            for (int mt = 0; mt < kMT; ++mt) {
+                const int row = (wk.rb * kMT + mt) * 16 + x;
+                if (row >= rows) continue;
+                const int t = row / a.group;
+                const long long part = (long long)blockIdx.x * (16 * kMT) + mt * 16 + x;
+                if (!wk.whole && r == 0 && quad == 0) {
+                    a.part_ml[part] = make_float2(top[mt], total[mt]);
+                }
+                const float inv = 1.0f / total[mt];
+                uint16_t* dst = a.out + (((long long)wk.b * (a.K + 1) + t) * a.Hq + wk.h * a.group +
+                                         (row - t * a.group)) * D;
+                #pragma unroll
+                for (int p = 0; p < kPlanes; ++p) {
+                    const int ch = p * 128 + (4 * quad + r) * kChans;
+                    f32x4 v[kChans / 4];
+                    #pragma unroll
+                    for (int c = 0; c < kChans / 4; ++c) {
+                        const int i = (mt * kPlanes + p) * (kChans / 4) + c;
+                        v[c] = (sh.o[0][i][lane] + sh.o[1][i][lane]) +
+                               (sh.o[2][i][lane] + sh.o[3][i][lane]);
+                    }
+                    if (wk.whole) {
+                        unsigned w[kChans / 2];
+                        #pragma unroll
+                        for (int c = 0; c < kChans; c += 2) {
+                            w[c / 2] = pack_bf16(v[c / 4][c % 4] * inv, v[c / 4][c % 4 + 1] * inv);
+                        }
+                        __builtin_memcpy(__builtin_assume_aligned(dst + ch, 2 * kChans), w, 2 * kChans);
+                    } else {
+                        #pragma unroll
+                        for (int c = 0; c < kChans / 4; ++c) {
+                            *reinterpret_cast<f32x4*>(a.part_o + part * D + ch + 4 * c) = v[c];
+                        }
+                    }
+                }
             }
         }
         __syncthreads();
-    }
-
-    #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
-        const int r = (wk.rb * kMT + mt) * 16 + x;
-        if (r >= rows) continue;
-        const int t = r / a.group;
-        const long long part = (long long)blockIdx.x * (16 * kMT) + mt * 16 + x;
-        if (!wk.whole && wave == 0 && quad == 0) a.part_ml[part] = make_float2(top[mt], total[mt]);
-        const float inv = 1.0f / total[mt];
-        #pragma unroll
-        for (int p = 0; p < kPlanes; ++p) {
-            const int ch = p * 128 + (4 * quad + wave) * kChans;
-            const f32x4* v = &mine[(mt * kPlanes + p) * kChans / 4];
-            if (wk.whole) {
-                uint16_t* dst = a.out + (((long long)wk.b * (a.K + 1) + t) * a.Hq + wk.h * a.group +
-                                         (r - t * a.group)) * D + ch;
-                unsigned w[kChans / 2];
-                #pragma unroll
-                for (int c = 0; c < kChans; c += 2) {
-                    w[c / 2] = pack_bf16(v[c / 4][c % 4] * inv, v[c / 4][c % 4 + 1] * inv);
-                }
-                __builtin_memcpy(__builtin_assume_aligned(dst, 2 * kChans), w, 2 * kChans);
-            } else {
-                #pragma unroll
-                for (int c = 0; c < kChans; c += 4) {
-                    *reinterpret_cast<f32x4*>(a.part_o + part * D + ch + c) = v[c / 4];
-                }
-            }
-        }
     }
 }
 

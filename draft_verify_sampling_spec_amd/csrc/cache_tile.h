@@ -101,9 +101,12 @@ struct Pages {
     int heads;
 
     // Tile of token position pos (>= 0) of request b, head h: byte offset in
-    // the cache, or -1 when the page is outside the pool.
+    // the cache, or -1 when the page is outside the pool. kUniform: the
+    // arguments are the same for the whole wavefront.
+    template <bool kUniform = false>
     __device__ __forceinline__ long long tile(int b, int h, int pos, int tile_bytes) const {
-        const int page = table[(size_t)b * max_pages + (pos >> shift)];
+        int page = table[(size_t)b * max_pages + (pos >> shift)];
+        if (kUniform) page = __builtin_amdgcn_readfirstlane(page);
         if ((unsigned)page >= (unsigned)num_pages) return -1;
         const int per = 1 << (shift - 5);
         return (((long long)page * heads + h) * per + ((pos >> 5) & (per - 1))) * tile_bytes;
