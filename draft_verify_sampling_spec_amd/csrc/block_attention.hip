@@ -43,13 +43,15 @@ constexpr float kNegInf = -INFINITY;
 // (rounded up, at least kLeastChunk), and finds its own split by a prefix sum
 // over the requests. kFewSplits workgroups are resident at once; chunks are
 // cut below kChunk tiles only to fill them, and above kChunk only when more
-// than kManySplits splits would come of it. With kDirectUnits units or more
-// every unit is one workgroup and nothing is cut.
+// than kManySplits splits would come of it. With kDirectUnits units or more,
+// or page table rows of fewer than kDirectTiles tiles, every unit is one
+// workgroup and nothing is cut.
 constexpr int kFewSplits = 512;
 constexpr int kManySplits = 2048;
 constexpr int kChunk = 64;
 constexpr int kLeastChunk = 8;
 constexpr int kDirectUnits = 4096;
+constexpr int kDirectTiles = 32;
 
 struct AttendArgs {
     const uint16_t* q;
@@ -59,8 +61,8 @@ struct AttendArgs {
     const int32_t* budgets;
     uint16_t* out;
     int32_t* status;
-    float* part_o;      // [slot][16 kMT rows][D], not normalised
-    float2* part_ml;    // [slot][16 kMT rows]: reference exponent, sum
+    float* part_o;      // [unit][16 kMT rows][split][D], not normalised
+    float2* part_ml;    // [unit][16 kMT rows][split]: reference exponent, sum
     int2* cut;          // [B]: the request's first slot, and chunk
     Pages pages;
     int B, K, Hq, group;
@@ -81,11 +83,16 @@ __device__ __forceinline__ Span span_of(const Block& blk, int window) {
     return Span{lo / kTile, (blk.ctx + blk.len + kTile - 1) / kTile};
 }
 
-// What a workgroup works on: tiles [t0, t1) of (b, h, row block rb), and
-// whether they are all of the unit's.
+// What a workgroup works on: tiles [t0, t1) of (b, h, row block rb), one of
+// the unit's n splits; slot: the unit's first.
 struct Work {
     int b, h, rb, t0, t1;
-    bool whole;
+    int n, split, slot;
+    // Where the partial of the unit's row `in` lies: a row's splits follow
+    // each other, so that the join reads one run.
+    __device__ __forceinline__ long long part(int rows, int in) const {
+        return (long long)slot * rows + in * n + split;
+    }
 };
 
 __device__ __forceinline__ unsigned pack_bf16(float a, float b) {
@@ -120,22 +127,23 @@ struct Frag {
     unsigned ks[L::kPlanes];                            // key scales of both halves
     unsigned vs[L::kPlanes][2];                         // value scales of 4 + 4 tokens
 
-    __device__ __forceinline__ void load(const uint8_t* tile, int lane) {
-        const int x = lane & 15, quad = lane >> 4;
+    // The tile is the same for the whole wavefront: one scalar base, a 32-bit
+    // offset per lane.
+    __device__ __forceinline__ void load(const uint8_t* tile, unsigned lane) {
+        const unsigned x = lane & 15, quad = lane >> 4;
         #pragma unroll
         for (int p = 0; p < L::kPlanes; ++p) {
             #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 __builtin_memcpy(k[half][p], __builtin_assume_aligned(
-                    tile + half * (8 * D) + (p * 64 + lane) * L::U, L::U), L::U);
+                    tile + (half * 8 * D + p * 64 * L::U) + lane * L::U, L::U), L::U);
                 __builtin_memcpy(v[half][p], __builtin_assume_aligned(
-                    tile + L::kVCodes + ((p * 2 + half) * 64 + lane) * (4 * L::C), 4 * L::C), 4 * L::C);
+                    tile + (L::kVCodes + (p * 2 + half) * 256 * L::C) + lane * (4 * L::C), 4 * L::C), 4 * L::C);
             }
-            const int kg = D == 64 ? quad >> 1 : p * 4 + quad;
-            ks[p] = *reinterpret_cast<const uint16_t*>(tile + L::kKScales + kg * 32 + x * 2);
-            const int vg = D == 64 ? x >> 3 : p * 4 + (x >> 2);
+            const unsigned kg = D == 64 ? quad >> 1 : quad, vg = D == 64 ? x >> 3 : x >> 2;
+            ks[p] = *reinterpret_cast<const uint16_t*>(tile + (L::kKScales + p * 128) + (kg * 32 + x * 2));
             __builtin_memcpy(vs[p], __builtin_assume_aligned(
-                tile + L::kVScales + (vg * 4 + quad) * 8, 8), 8);
+                tile + (L::kVScales + p * 128) + (vg * 4 + quad) * 8, 8), 8);
         }
     }
 };
@@ -149,7 +157,7 @@ struct State {
     static constexpr int kSteps = D / 32;
     static constexpr int kChans = D == 64 ? 4 : 8;      // channels of a value piece
     f32x4 o[kMT][kPlanes][kChans];
-    float ref[kMT];     // reference of the exponents, in scores (before c); -inf: nothing seen
+    float ref[kMT];     // reference of the exponents; -inf: nothing seen
     float sum[kMT];     // this lane's share of the row's sum
     int pos[kMT];       // the row's position; -1 past the block
 };
@@ -162,7 +170,7 @@ struct Lds {
     float ref[kWaves][kMT][16];
     float sum[kWaves][kMT][16];
     unsigned scan[kWaves];
-    int found[4];
+    int found[7];
 };
 
 // One tile. kAct: row tiles that hold rows of the block. kMasked: some row
@@ -201,43 +209,47 @@ __device__ __forceinline__ void tile_step(State<D, kMT>& st, const Frag<D>& f,
         }
     }
 
-    // Probabilities 2^((z - ref) c). The reference follows the running
-    // maximum only when a score exceeds it by 8 / c: until then terms stay
-    // below 2^8 and nothing has to be rescaled.
+    // Probabilities 2^(c z - ref). The reference follows the running maximum
+    // only when a term exceeds 2^8: until then nothing has to be rescaled.
     __builtin_amdgcn_sched_barrier(0);
     bf16x8 pf[kAct];
     #pragma unroll
     for (int mt = 0; mt < kAct; ++mt) {
-        float s[8];
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = z[mt][i >> 2][i & 3];
         if (kMasked) {
             const int lo = a.window > 0 ? st.pos[mt] - a.window : -1;
             #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int j = tok0 + 16 * (i >> 2) + 4 * quad + (i & 3);
-                if (j > st.pos[mt] || j <= lo) s[i] = kNegInf;
+                if (j > st.pos[mt] || j <= lo) z[mt][i >> 2][i & 3] = kNegInf;
             }
         }
+        // A row that has seen nothing yet has reference 0 here; what it does
+        // not see is 2^(-inf) = 0.
+        const bool fresh = st.ref[mt] == kNegInf;
+        const float ref = fresh ? 0.0f : st.ref[mt];
+        float s[8];
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf(z[mt][i >> 2][i & 3], a.c, -ref);
         float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])),
                           fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
-        // Also true while ref is -inf and anything is seen.
-        const bool grow = (top - st.ref[mt]) * a.c > 8.0f || (st.ref[mt] == kNegInf && top > kNegInf);
-        if (__ballot(grow) != 0) {
-            top = fmaxf(quad_max(top), st.ref[mt]);
-            const float keep = st.ref[mt] == kNegInf ? 0.0f : exp2_fast((st.ref[mt] - top) * a.c);
-            st.ref[mt] = top;
+        if (__ballot(top > (fresh ? kNegInf : 8.0f)) != 0) {
+            // The four lanes of a row share its reference.
+            top = quad_max(top);
+            const float next = fresh ? top : fmaxf(ref, ref + top);
+            const float keep = fresh ? 0.0f : exp2_fast(ref - next);
+            const float off = next == kNegInf ? 0.0f : next;
+            st.ref[mt] = next;
             st.sum[mt] *= keep;
             #pragma unroll
             for (int p = 0; p < S::kPlanes; ++p) {
                 #pragma unroll
                 for (int j = 0; j < S::kChans; ++j) st.o[mt][p][j] *= keep;
             }
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf(z[mt][i >> 2][i & 3], a.c, -off);
         }
-        // A row that has seen nothing yet: its terms are 2^(-inf) = 0.
-        const float off = st.ref[mt] == kNegInf ? 0.0f : -st.ref[mt] * a.c;
         #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = exp2_fast(__builtin_fmaf(s[i], a.c, off));
+        for (int i = 0; i < 8; ++i) s[i] = exp2_fast(s[i]);
         st.sum[mt] += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
         const u32x4 pw = {pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]), pack_bf16(s[4], s[5]),
                           pack_bf16(s[6], s[7])};
@@ -320,56 +332,71 @@ __device__ __forceinline__ void tile_step(State<D, kMT>& st, const Frag<D>& f,
 }
 
 // This wavefront's share of the tiles [t0, t1). The tiles that every row sees
-// whole come in a loop that keeps the next tile's bytes in flight; the few at
-// the ends that some row does not see whole (the block's own, and the windows'
-// edges) are worked on one by one while the loop's first bytes are on their
-// way.
-template <int D, int kMT, int kAct>
-__device__ __forceinline__ void tile_loop(State<D, kMT>& st, const Lds<D, kMT>& sh,
-                                          const AttendArgs& a, const Work& wk, const Block& blk,
-                                          int lane, int wave) {
+// whole come in a loop that keeps the bytes of the next kAhead tiles in
+// flight; the few at the ends that some row does not see whole (the block's
+// own, and the windows' edges) are worked on one by one while the loop's first
+// bytes are on their way.
+template <int D, int kAhead>
+struct Stream {
     using L = Tile<D>;
-    const int last = blk.ctx + blk.len - 1;
-    // Tiles [u0, u1) of this split lie wholly in [all_lo, ctx + 1), the tokens
-    // that every row of the block sees.
-    const int all_lo = a.window > 0 ? max(0, last - a.window + 1) : 0;
-    const int u0 = min(max(wk.t0, (all_lo + kTile - 1) / kTile), wk.t1);
-    const int u1 = max(u0, min(wk.t1, (blk.ctx + 1) / kTile));
+    Frag<D> f[kAhead + 1];
+    long long at[kAhead + 1];
+    int t, u0, u1;
+
     // A tile whose page is bad is flagged and skipped; the first tile of the
-    // cache stands in for its bytes.
-    auto locate = [&](int t) {
-        const long long at = a.pages.tile<true>(wk.b, wk.h, t * kTile, L::kBytes);
-        if (at < 0 && lane == 0) flag(a.status, SV_FLAG_BAD_PAGE);
-        return at;
-    };
-    Frag<D> f[2];
-    int t = u0 + wave;
-    long long at[2] = {-1, -1};
-    if (t < u1) {
-        at[0] = locate(t);
-        f[0].load(a.cache + max(at[0], 0ll), lane);
+    // cache stands in for its bytes, and past the end for the bytes of no tile.
+    __device__ __forceinline__ long long locate(const AttendArgs& a, const Work& wk, int tile,
+                                                int lane) const {
+        const long long p = a.pages.tile<true>(wk.b, wk.h, tile * kTile, L::kBytes);
+        if (p < 0 && lane == 0) flag(a.status, SV_FLAG_BAD_PAGE);
+        return p;
     }
-    const int edges = (u0 - wk.t0) + (wk.t1 - u1);
-    for (int i = kWaves - 1 - wave; i < edges; i += kWaves) {
-        const int e = wk.t0 + i < u0 ? wk.t0 + i : u1 + (i - (u0 - wk.t0));
-        const long long edge = locate(e);
-        if (edge < 0) continue;
-        Frag<D> g;
-        g.load(a.cache + edge, lane);
-        tile_step<D, kMT, kAct, true>(st, g, sh, a, lane, e * kTile, last, a.cache + edge);
+    template <int i>
+    __device__ __forceinline__ void fetch(const AttendArgs& a, const Work& wk, int tile, int lane) {
+        at[i] = tile < u1 ? locate(a, wk, tile, lane) : -1;
+        f[i].load(a.cache + max(at[i], 0ll), lane);
     }
-    while (t < u1) {
-        #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            // Past the end: the same tile again, from the cache and unused.
-            const bool more = t + kWaves < u1;
-            at[1 - i] = more ? locate(t + kWaves) : -1;
-            f[1 - i].load(a.cache + max(more ? at[1 - i] : at[i], 0ll), lane);
-            if (at[i] >= 0) tile_step<D, kMT, kAct, false>(st, f[i], sh, a, lane, t * kTile, last, nullptr);
-            t += kWaves;
+    __device__ __forceinline__ void start(const AttendArgs& a, const Work& wk, const Block& blk,
+                                          int lane, int wave) {
+        // Tiles [u0, u1) of this split lie wholly in [all_lo, ctx + 1), the
+        // tokens that every row of the block sees.
+        const int all_lo = a.window > 0 ? max(0, blk.ctx + blk.len - a.window) : 0;
+        u0 = min(max(wk.t0, (all_lo + kTile - 1) / kTile), wk.t1);
+        u1 = max(u0, min(wk.t1, (blk.ctx + 1) / kTile));
+        t = u0 + wave;
+        if (t < u1) {
+            fetch<0>(a, wk, t, lane);
+            if constexpr (kAhead == 2) fetch<1>(a, wk, t + kWaves, lane);
         }
     }
-}
+    template <int kMT, int kAct>
+    __device__ __forceinline__ void run(State<D, kMT>& st, const Lds<D, kMT>& sh,
+                                        const AttendArgs& a, const Work& wk, const Block& blk,
+                                        int lane, int wave) {
+        const int last = blk.ctx + blk.len - 1;
+        const int edges = (u0 - wk.t0) + (wk.t1 - u1);
+        for (int i = kWaves - 1 - wave; i < edges; i += kWaves) {
+            const int e = wk.t0 + i < u0 ? wk.t0 + i : u1 + (i - (u0 - wk.t0));
+            const long long edge = locate(a, wk, e, lane);
+            if (edge < 0) continue;
+            Frag<D> g;
+            g.load(a.cache + edge, lane);
+            tile_step<D, kMT, kAct, true>(st, g, sh, a, lane, e * kTile, last, a.cache + edge);
+        }
+        while (t < u1) {
+            step<kMT, kAct, 0>(st, sh, a, wk, lane);
+            step<kMT, kAct, 1>(st, sh, a, wk, lane);
+            if constexpr (kAhead == 2) step<kMT, kAct, 2>(st, sh, a, wk, lane);
+        }
+    }
+    template <int kMT, int kAct, int i>
+    __device__ __forceinline__ void step(State<D, kMT>& st, const Lds<D, kMT>& sh,
+                                         const AttendArgs& a, const Work& wk, int lane) {
+        fetch<(i + kAhead) % (kAhead + 1)>(a, wk, t + kAhead * kWaves, lane);
+        if (at[i] >= 0) tile_step<D, kMT, kAct, false>(st, f[i], sh, a, lane, 0, 0, nullptr);
+        t += kWaves;
+    }
+};
 
 // Finds the split of workgroup `slot`; false when there is none.
 template <int D, int kMT>
@@ -384,7 +411,7 @@ __device__ bool find_work(const AttendArgs& a, Lds<D, kMT>& sh, Work& wk) {
         const Span s = span_of(blk, a.window);
         wk.t0 = s.first;
         wk.t1 = s.end;
-        wk.whole = true;
+        wk.n = 1;
         return true;
     }
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -419,28 +446,40 @@ __device__ bool find_work(const AttendArgs& a, Lds<D, kMT>& sh, Work& wk) {
         return total;
     };
     if (tid == 0) sh.found[0] = -1;
-    int units, first = 0;
+    // The first of this thread's requests (the only one up to 256) is kept.
+    int units0 = 0, first0 = 0, n0 = 0;
     unsigned mine = 0, before;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(b, units, first) * units;
+    if (b0 < b1) n0 = tiles_of(b0, units0, first0);
+    mine = n0 * units0;
+    for (int b = b0 + 1; b < b1; ++b) {
+        int units, first = 0;
+        const int n = tiles_of(b, units, first);
+        mine += n * units;
+    }
     const unsigned total = block_total(mine, before);
     unsigned chunk = max((total + kManySplits - 1) / kManySplits,
                          min((total + kFewSplits - 1) / kFewSplits, (unsigned)kChunk));
     chunk = max(chunk, (unsigned)kLeastChunk);
     mine = 0;
     for (int b = b0; b < b1; ++b) {
-        const int n = tiles_of(b, units, first);
+        int units = units0, first, n = n0;
+        if (b > b0) n = tiles_of(b, units, first);
         mine += (n + chunk - 1) / chunk * units;
     }
     block_total(mine, before);
     for (int b = b0; b < b1; ++b) {
-        const int n = tiles_of(b, units, first);
+        int units = units0, first = first0, n = n0;
+        if (b > b0) n = tiles_of(b, units, first);
         const unsigned count = (n + chunk - 1) / chunk * units;
         if ((unsigned)slot >= before && (unsigned)slot < before + count) {
             const int in = slot - before, split = in / units;
             sh.found[0] = b;
             sh.found[1] = in % units;
             sh.found[2] = first + split * chunk;
-            sh.found[3] = min(first + (split + 1) * (int)chunk, first + n) | (n <= (int)chunk ? 1 << 30 : 0);
+            sh.found[3] = min(first + (split + 1) * (int)chunk, first + n);
+            sh.found[4] = count / units;
+            sh.found[5] = split;
+            sh.found[6] = before + in % units * (count / units);
             if (in == 0) a.cut[b] = make_int2(before, chunk);
         }
         before += count;
@@ -452,15 +491,25 @@ __device__ bool find_work(const AttendArgs& a, Lds<D, kMT>& sh, Work& wk) {
     wk.h = unit % a.pages.heads;
     wk.rb = unit / a.pages.heads;
     wk.t0 = __builtin_amdgcn_readfirstlane(sh.found[2]);
-    const int end = __builtin_amdgcn_readfirstlane(sh.found[3]);
-    wk.t1 = end & ((1 << 30) - 1);
-    wk.whole = end >> 30;
+    wk.t1 = __builtin_amdgcn_readfirstlane(sh.found[3]);
+    wk.n = __builtin_amdgcn_readfirstlane(sh.found[4]);
+    wk.split = __builtin_amdgcn_readfirstlane(sh.found[5]);
+    wk.slot = __builtin_amdgcn_readfirstlane(sh.found[6]);
     return true;
 }
 
-// Accumulators of more than 96 registers a lane leave one wave per SIMD.
+// Waves per SIMD that the registers leave room for, and tiles in flight.
 template <int D, int kMT>
-__global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs a) {
+constexpr int occupancy() {
+    return D == 256 || kMT == 4 ? 2 : D * kMT <= 128 ? 4 : D * kMT <= 256 ? 3 : 2;
+}
+template <int D, int kMT>
+constexpr int ahead() {
+    return D * kMT == 384 || (D == 256 && kMT == 1) ? 2 : 1;
+}
+
+template <int D, int kMT>
+__global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(AttendArgs a) {
     using S = State<D, kMT>;
     constexpr int kPlanes = S::kPlanes, kChans = S::kChans;
     __shared__ Lds<D, kMT> sh;
@@ -476,6 +525,9 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs a) {
     if (!find_work<D, kMT>(a, sh, wk)) return;
     const Block blk = block_of(a.ctx_lens, a.budgets, wk.b, a.K + 1, a.pages, nullptr, false);
     const int rows = blk.len * a.group;
+
+    Stream<D, ahead<D, kMT>()> stream;
+    stream.start(a, wk, blk, lane, wave);
 
     // The queries as right operands: lane holds row x, 8 channels of its unit.
     for (int i = wave; i < kMT * S::kSteps; i += kWaves) {
@@ -506,10 +558,10 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs a) {
     __syncthreads();
 
     const int act = min((rows - wk.rb * 16 * kMT + 15) / 16, kMT);
-    if (kMT >= 4 && act == 4) tile_loop<D, kMT, (kMT < 4 ? 1 : 4)>(st, sh, a, wk, blk, lane, wave);
-    else if (kMT >= 3 && act == 3) tile_loop<D, kMT, (kMT < 3 ? 1 : 3)>(st, sh, a, wk, blk, lane, wave);
-    else if (kMT >= 2 && act == 2) tile_loop<D, kMT, (kMT < 2 ? 1 : 2)>(st, sh, a, wk, blk, lane, wave);
-    else tile_loop<D, kMT, 1>(st, sh, a, wk, blk, lane, wave);
+    if (kMT >= 4 && act == 4) stream.template run<kMT, (kMT < 4 ? 1 : 4)>(st, sh, a, wk, blk, lane, wave);
+    else if (kMT >= 3 && act == 3) stream.template run<kMT, (kMT < 3 ? 1 : 3)>(st, sh, a, wk, blk, lane, wave);
+    else if (kMT >= 2 && act == 2) stream.template run<kMT, (kMT < 2 ? 1 : 2)>(st, sh, a, wk, blk, lane, wave);
+    else stream.template run<kMT, 1>(st, sh, a, wk, blk, lane, wave);
 
     // Join the waves: component r of every accumulator in round r, of which
     // wave r writes kChans consecutive channels per (row, plane).
@@ -529,11 +581,11 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs a) {
         #pragma unroll
         for (int w = 0; w < kWaves; ++w) top[mt] = fmaxf(top[mt], sh.ref[w][mt][x]);
         const float ref = top[mt] == kNegInf ? 0.0f : top[mt];
-        const float mine = exp2_fast((st.ref[mt] - ref) * a.c);
+        const float mine = exp2_fast(st.ref[mt] - ref);
         total[mt] = 0.0f;
         #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            total[mt] += sh.sum[w][mt][x] * exp2_fast((sh.ref[w][mt][x] - ref) * a.c);
+            total[mt] += sh.sum[w][mt][x] * exp2_fast(sh.ref[w][mt][x] - ref);
         }
         #pragma unroll
         for (int p = 0; p < kPlanes; ++p) {
@@ -562,8 +614,8 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs a) {
                 const int row = (wk.rb * kMT + mt) * 16 + x;
                 if (row >= rows) continue;
                 const int t = row / a.group;
-                const long long part = (long long)blockIdx.x * (16 * kMT) + mt * 16 + x;
-                if (!wk.whole && r == 0 && quad == 0) {
+                const long long part = wk.part(16 * kMT, mt * 16 + x);
+                if (wk.n > 1 && r == 0 && quad == 0) {
                     a.part_ml[part] = make_float2(top[mt], total[mt]);
                 }
                 const float inv = 1.0f / total[mt];
@@ -579,7 +631,7 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs a) {
                         v[c] = (sh.o[0][i][lane] + sh.o[1][i][lane]) +
                                (sh.o[2][i][lane] + sh.o[3][i][lane]);
                     }
-                    if (wk.whole) {
+                    if (wk.n == 1) {
                         unsigned w[kChans / 2];
                         #pragma unroll
                         for (int c = 0; c < kChans; c += 2) {
@@ -599,43 +651,75 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs a) {
     }
 }
 
-// Joins the splits of one row: one wavefront per row, in the order of the
-// splits.
+// Joins the splits of a unit's rows: a workgroup per unit and four rows, a
+// wavefront each. Lanes hold 4 channels, 256 / D splits lie side by side in a
+// wavefront, and the partials of kDeep of them each are in flight. The running
+// reference keeps this to one pass; the order of the sums is fixed by the
+// shapes and lengths.
 template <int D, int kMT>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int T = a.K + 1;
-    const int i = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (i >= a.B * T * a.Hq) return;
-    const int head = i % a.Hq, t = i / a.Hq % T, b = i / a.Hq / T;
-    const Block blk = block_of(a.ctx_lens, a.budgets, b, T, a.pages, nullptr, false);
-    if (t >= blk.len) return;
+    constexpr int kSide = 256 / D, kLanes = 64 / kSide;     // splits side by side, lanes of each
+    constexpr int kDeep = 8;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int side = lane / kLanes, ch = lane % kLanes * 4;
+    int id = blockIdx.x;
+    const int in = id % (4 * kMT) * kWaves + wave;          // row of the row block
+    id /= 4 * kMT;
+    const int rb = id % a.row_blocks;
+    id /= a.row_blocks;
+    const int h = id % a.pages.heads, b = id / a.pages.heads;
+    const Block blk = block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, nullptr, false);
+    const int rows = blk.len * a.group, row = rb * (16 * kMT) + in;
+    if (row >= rows) return;
     const int2 cut = a.cut[b];
     const int n = (span_of(blk, a.window).size() + cut.y - 1) / cut.y;
     if (n == 1) return;
-    const int units = (blk.len * a.group + 16 * kMT - 1) / (16 * kMT) * a.pages.heads;
-    const int h = head / a.group, r = t * a.group + head % a.group;
-    const int rb = r / (16 * kMT), in = r % (16 * kMT);
-    const long long part = (long long)(cut.x + rb * a.pages.heads + h) * (16 * kMT) + in;
-    const long long step = (long long)units * (16 * kMT);
-    float top = kNegInf;
-    for (int s = 0; s < n; ++s) top = fmaxf(top, a.part_ml[part + s * step].x);
-    const float ref = top == kNegInf ? 0.0f : top;
-    float sum = 0.0f;
-    float acc[D / 64] = {};
-    for (int s = 0; s < n; ++s) {
-        const long long p = part + s * step;
-        const float2 ml = a.part_ml[p];
-        const float f = exp2_fast((ml.x - ref) * a.c);
-        sum += ml.y * f;
+    const long long part = (long long)(cut.x + (rb * a.pages.heads + h) * n) * (16 * kMT) + in * n;
+
+    float ref = kNegInf, sum = 0.0f;
+    f32x4 acc = {0, 0, 0, 0};
+    for (int s0 = side; s0 < n; s0 += kDeep * kSide) {
+        f32x4 v[kDeep];
+        float2 ml[kDeep];
         #pragma unroll
-        for (int c = 0; c < D / 64; ++c) acc[c] += a.part_o[p * D + lane * (D / 64) + c] * f;
+        for (int k = 0; k < kDeep; ++k) {
+            const long long p = part + min(s0 + k * kSide, n - 1);
+            ml[k] = a.part_ml[p];
+            v[k] = *reinterpret_cast<const f32x4*>(a.part_o + p * D + ch);
+        }
+        float top = ref;
+        #pragma unroll
+        for (int k = 0; k < kDeep; ++k) top = fmaxf(top, ml[k].x);
+        const float base = top == kNegInf ? 0.0f : top;
+        const float keep = exp2_fast(ref - base);
+        sum *= keep;
+        acc *= keep;
+        ref = top;
+        #pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            if (s0 + k * kSide >= n) break;
+            const float f = exp2_fast(ml[k].x - base);
+            sum += ml[k].y * f;
+            acc += v[k] * f;
+        }
     }
-    const float inv = 1.0f / sum;
-    uint16_t* dst = a.out + (long long)i * D + lane * (D / 64);
     #pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-        dst[c] = __builtin_bit_cast(uint16_t, (__bf16)(acc[c] * inv));
+    for (int o = kLanes; o < 64; o <<= 1) {
+        const float other = __shfl_xor(ref, o), top = fmaxf(ref, other);
+        const float base = top == kNegInf ? 0.0f : top;
+        const float f = exp2_fast(ref - base), g = exp2_fast(other - base);
+        sum = sum * f + __shfl_xor(sum, o) * g;
+        #pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] = acc[c] * f + __shfl_xor(acc[c], o) * g;
+        ref = top;
+    }
+    if (side == 0) {
+        const int t = row / a.group, head = h * a.group + (row - t * a.group);
+        const float inv = 1.0f / sum;
+        const unsigned w[2] = {pack_bf16(acc[0] * inv, acc[1] * inv),
+                               pack_bf16(acc[2] * inv, acc[3] * inv)};
+        uint16_t* dst = a.out + (((long long)b * (a.K + 1) + t) * a.Hq + head) * D + ch;
+        __builtin_memcpy(__builtin_assume_aligned(dst, 8), w, 8);
     }
 }
 
@@ -653,12 +737,12 @@ Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_p
     p.mt = (rows + 15) / 16 < most ? (rows + 15) / 16 : most;
     p.row_blocks = (rows + 16 * p.mt - 1) / (16 * p.mt);
     const long long units = (long long)B * kv_heads * p.row_blocks;
-    p.direct = units >= kDirectUnits;
     // Splits: every unit's last one, and no more than kManySplits full ones
     // or than the page table row can hold.
     long long tokens = (long long)max_pages * page_size;
     if (window > 0 && tokens > (long long)window + K + kTile) tokens = (long long)window + K + kTile;
     const long long tiles = (tokens + kTile - 1) / kTile + 1;
+    p.direct = units >= kDirectUnits || tiles <= kDirectTiles;
     const long long per_unit = (tiles + kLeastChunk - 1) / kLeastChunk;
     p.slots = p.direct ? units : std::min(units + kManySplits, units * per_unit);
     return p;
@@ -678,10 +762,8 @@ template <int D, int kMT>
 void launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
     hipLaunchKernelGGL((attend_kernel<D, kMT>), dim3((unsigned)p.slots), dim3(256), 0, s, a);
     if (!p.direct) {
-        // Fewer than kDirectUnits units: the rows fit 32 bits.
-        const int rows = a.B * (a.K + 1) * a.Hq;
-        hipLaunchKernelGGL((attend_join_kernel<D, kMT>), dim3((unsigned)((rows + 3) / 4)),
-                           dim3(256), 0, s, a);
+        const unsigned blocks = (unsigned)(a.B * a.pages.heads * p.row_blocks * 4 * kMT);
+        hipLaunchKernelGGL((attend_join_kernel<D, kMT>), dim3(blocks), dim3(256), 0, s, a);
     }
 }
 
