@@ -36,21 +36,19 @@ constexpr int kWaves = 4;
 constexpr float kNegInf = -INFINITY;
 
 // How the work is cut. A unit is a request's kv head and block of 16 kMT
-// rows; its tiles are cut into splits of `chunk` tiles, a workgroup each. The
-// lengths are on the device, so the cut is made there: every workgroup adds
-// up the tiles of all requests, takes
-//   chunk = max(total / kManySplits, min(total / kFewSplits, kChunk))
-// (rounded up, at least kLeastChunk), and finds its own split by a prefix sum
-// over the requests. kFewSplits workgroups are resident at once; chunks are
-// cut below kChunk tiles only to fill them, and above kChunk only when more
-// than kManySplits splits would come of it. With kDirectUnits units or more,
-// or page table rows of fewer than kDirectTiles tiles, every unit is one
-// workgroup and nothing is cut.
-constexpr int kFewSplits = 512;
-constexpr int kManySplits = 2048;
-constexpr int kChunk = 64;
-constexpr int kLeastChunk = 8;
-constexpr int kDirectUnits = 4096;
+// rows. All units' tiles lie on one line, a tile as long as its cost (kTileCost
+// plus its row tiles) and each unit led by a stretch for what starting and
+// ending one takes; every workgroup takes an equal share of the line, so that
+// ragged lengths and budgets load the chip evenly. The lengths are on the
+// device, so every workgroup lays the line out for itself (sums over the
+// requests and a prefix sum to find its place). A workgroup that ends inside a
+// unit leaves a partial result, which the join kernel puts together.
+// With page table rows of at most kDirectTiles tiles a workgroup per unit is
+// launched instead and nothing is joined: a second launch and the search
+// would cost more than the imbalance.
+constexpr int kTileCost = 2;
+constexpr int kUnitCost = 64;       // at most; a quarter of a share where shares are short
+constexpr int kLeastShare = 32;     // a few tiles for each of a workgroup's wavefronts
 constexpr int kDirectTiles = 32;
 
 struct AttendArgs {
@@ -61,9 +59,9 @@ struct AttendArgs {
     const int32_t* budgets;
     uint16_t* out;
     int32_t* status;
-    float* part_o;      // [unit][16 kMT rows][split][D], not normalised
-    float2* part_ml;    // [unit][16 kMT rows][split]: reference exponent, sum
-    int2* cut;          // [B]: the request's first slot, and chunk
+    float* part_o;      // [slot][16 kMT rows][D], not normalised
+    float2* part_ml;    // [slot][16 kMT rows]: reference exponent, sum
+    int4* parts;        // [slot]: unit, its parts, which one this is, workgroup of the first
     Pages pages;
     int B, K, Hq, group;
     int row_blocks;     // blocks of 16 kMT rows of a full block's (K + 1) group rows
@@ -83,16 +81,11 @@ __device__ __forceinline__ Span span_of(const Block& blk, int window) {
     return Span{lo / kTile, (blk.ctx + blk.len + kTile - 1) / kTile};
 }
 
-// What a workgroup works on: tiles [t0, t1) of (b, h, row block rb), one of
-// the unit's n splits; slot: the unit's first.
+// A run of one unit's tiles: [t0, t1) of (b, h, row block rb); slot: where its
+// partial result goes (slot 2 g + 1 of the workgroup g that starts the unit,
+// 2 g of those that go on with it), or -1 when the run is the whole unit.
 struct Work {
-    int b, h, rb, t0, t1;
-    int n, split, slot;
-    // Where the partial of the unit's row `in` lies: a row's splits follow
-    // each other, so that the join reads one run.
-    __device__ __forceinline__ long long part(int rows, int in) const {
-        return (long long)slot * rows + in * n + split;
-    }
+    int b, h, rb, t0, t1, slot;
 };
 
 __device__ __forceinline__ unsigned pack_bf16(float a, float b) {
@@ -101,6 +94,13 @@ __device__ __forceinline__ unsigned pack_bf16(float a, float b) {
     v[1] = (__bf16)b;
     return __builtin_bit_cast(unsigned, v);
 }
+
+// A value that is the same in every lane, as a scalar.
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ unsigned long long scalar(unsigned long long v) {
+    return (unsigned long long)(unsigned)scalar((int)(v >> 32)) << 32 | (unsigned)scalar((int)v);
+}
+__device__ __forceinline__ Block scalar(const Block& k) { return Block{scalar(k.ctx), scalar(k.len)}; }
 
 // Maximum / sum over the four lanes that hold the same row (lane ^ 16, ^ 32).
 __device__ __forceinline__ float quad_max(float v) {
@@ -164,13 +164,16 @@ struct State {
 
 template <int D, int kMT>
 struct Lds {
-    static constexpr int kPieces = kMT * Tile<D>::kPlanes * (D == 64 ? 4 : 8) / 4;  // float4 per lane and round
-    u32x4 q[kMT][D / 32][64];           // right operands of K Q^T
-    f32x4 o[kWaves][kPieces][64];
+    static constexpr int kPieces = kMT * Tile<D>::kPlanes * (D == 64 ? 4 : 8) / 4;  // float4 per lane and component
+    union {
+        u32x4 q[kMT][D / 32][64];           // right operands of K Q^T
+        f32x4 o[kWaves][2][kPieces][64];    // two components of the accumulators at a time
+    };
     float ref[kWaves][kMT][16];
     float sum[kWaves][kMT][16];
-    unsigned scan[kWaves];
-    int found[7];
+    unsigned long long scan[kWaves], before;
+    unsigned scan_units[kWaves];
+    int found;
 };
 
 // One tile. kAct: row tiles that hold rows of the block. kMasked: some row
@@ -332,42 +335,51 @@ __device__ __forceinline__ void tile_step(State<D, kMT>& st, const Frag<D>& f,
 }
 
 // This wavefront's share of the tiles [t0, t1). The tiles that every row sees
-// whole come in a loop that keeps the bytes of the next kAhead tiles in
-// flight; the few at the ends that some row does not see whole (the block's
+// whole come in a loop that keeps the next tile's bytes in flight; the few at the ends that some row does not see whole (the block's
 // own, and the windows' edges) are worked on one by one while the loop's first
 // bytes are on their way.
-template <int D, int kAhead>
+template <int D>
 struct Stream {
     using L = Tile<D>;
-    Frag<D> f[kAhead + 1];
-    long long at[kAhead + 1];
+    Frag<D> f[2];
+    long long at[2];
     int t, u0, u1;
+    // Page numbers of this wavefront's next 64 tiles, one a lane. They come in
+    // one load: a lookup per tile would wait for every load before it, the
+    // tiles in flight among them.
+    int pages;
 
     // A tile whose page is bad is flagged and skipped; the first tile of the
     // cache stands in for its bytes, and past the end for the bytes of no tile.
-    __device__ __forceinline__ long long locate(const AttendArgs& a, const Work& wk, int tile,
-                                                int lane) const {
-        const long long p = a.pages.tile<true>(wk.b, wk.h, tile * kTile, L::kBytes);
+    __device__ __forceinline__ long long locate(const AttendArgs& a, const Work& wk, int page,
+                                                int tile, int lane) const {
+        const long long p = a.pages.tile_in(page, wk.h, tile * kTile, L::kBytes);
         if (p < 0 && lane == 0) flag(a.status, SV_FLAG_BAD_PAGE);
         return p;
     }
+    // The wavefront's tile number n = (tile - u0 - wave) / kWaves into f[i].
     template <int i>
-    __device__ __forceinline__ void fetch(const AttendArgs& a, const Work& wk, int tile, int lane) {
-        at[i] = tile < u1 ? locate(a, wk, tile, lane) : -1;
+    __device__ __forceinline__ void fetch(const AttendArgs& a, const Work& wk, int tile, int n,
+                                          int lane) {
+        at[i] = -1;
+        if (tile < u1) {
+            if ((n & 63) == 0) {
+                const int mine = tile + lane * kWaves;
+                pages = mine < u1 ? a.pages.page(wk.b, mine * kTile) : -1;
+            }
+            at[i] = locate(a, wk, __builtin_amdgcn_readlane(pages, n & 63), tile, lane);
+        }
         f[i].load(a.cache + max(at[i], 0ll), lane);
     }
     __device__ __forceinline__ void start(const AttendArgs& a, const Work& wk, const Block& blk,
                                           int lane, int wave) {
-        // Tiles [u0, u1) of this split lie wholly in [all_lo, ctx + 1), the
+        // Tiles [u0, u1) of this run lie wholly in [all_lo, ctx + 1), the
         // tokens that every row of the block sees.
         const int all_lo = a.window > 0 ? max(0, blk.ctx + blk.len - a.window) : 0;
         u0 = min(max(wk.t0, (all_lo + kTile - 1) / kTile), wk.t1);
         u1 = max(u0, min(wk.t1, (blk.ctx + 1) / kTile));
         t = u0 + wave;
-        if (t < u1) {
-            fetch<0>(a, wk, t, lane);
-            if constexpr (kAhead == 2) fetch<1>(a, wk, t + kWaves, lane);
-        }
+        if (t < u1) fetch<0>(a, wk, t, 0, lane);
     }
     template <int kMT, int kAct>
     __device__ __forceinline__ void run(State<D, kMT>& st, const Lds<D, kMT>& sh,
@@ -377,171 +389,83 @@ struct Stream {
         const int edges = (u0 - wk.t0) + (wk.t1 - u1);
         for (int i = kWaves - 1 - wave; i < edges; i += kWaves) {
             const int e = wk.t0 + i < u0 ? wk.t0 + i : u1 + (i - (u0 - wk.t0));
-            const long long edge = locate(a, wk, e, lane);
+            const long long edge = locate(a, wk, scalar(a.pages.page(wk.b, e * kTile)), e, lane);
             if (edge < 0) continue;
             Frag<D> g;
             g.load(a.cache + edge, lane);
             tile_step<D, kMT, kAct, true>(st, g, sh, a, lane, e * kTile, last, a.cache + edge);
         }
-        while (t < u1) {
-            step<kMT, kAct, 0>(st, sh, a, wk, lane);
-            step<kMT, kAct, 1>(st, sh, a, wk, lane);
-            if constexpr (kAhead == 2) step<kMT, kAct, 2>(st, sh, a, wk, lane);
+        for (int n = 1; t < u1; n += 2) {
+            step<kMT, kAct, 0>(st, sh, a, wk, n, lane);
+            step<kMT, kAct, 1>(st, sh, a, wk, n + 1, lane);
         }
     }
     template <int kMT, int kAct, int i>
     __device__ __forceinline__ void step(State<D, kMT>& st, const Lds<D, kMT>& sh,
-                                         const AttendArgs& a, const Work& wk, int lane) {
-        fetch<(i + kAhead) % (kAhead + 1)>(a, wk, t + kAhead * kWaves, lane);
+                                         const AttendArgs& a, const Work& wk, int n, int lane) {
+        fetch<1 - i>(a, wk, t + kWaves, n, lane);
         if (at[i] >= 0) tile_step<D, kMT, kAct, false>(st, f[i], sh, a, lane, 0, 0, nullptr);
         t += kWaves;
     }
 };
 
-// Finds the split of workgroup `slot`; false when there is none.
-template <int D, int kMT>
-__device__ bool find_work(const AttendArgs& a, Lds<D, kMT>& sh, Work& wk) {
-    const int slot = blockIdx.x;
-    if (a.direct) {
-        wk.rb = slot % a.row_blocks;
-        wk.h = slot / a.row_blocks % a.pages.heads;
-        wk.b = slot / a.row_blocks / a.pages.heads;
-        const Block blk = block_of(a.ctx_lens, a.budgets, wk.b, a.K + 1, a.pages, nullptr, false);
-        if (wk.rb * 16 * kMT >= blk.len * a.group) return false;
-        const Span s = span_of(blk, a.window);
-        wk.t0 = s.first;
-        wk.t1 = s.end;
-        wk.n = 1;
-        return true;
-    }
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int per = (a.B + 255) / 256;
-    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    // Tiles of a request (0: nothing to do) and its units.
-    auto tiles_of = [&](int b, int& units, int& first) {
-        const Block blk = block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, nullptr, false);
-        units = (blk.len * a.group + 16 * kMT - 1) / (16 * kMT) * a.pages.heads;
+// A request's share of the line.
+template <int kMT>
+struct Share {
+    Block blk;
+    Span span;
+    int rows, blocks;           // rows, row blocks that hold some
+    __device__ __forceinline__ Share(const AttendArgs& a, const Block& k)
+        : blk(k), span(span_of(k, a.window)), rows(k.len * a.group),
+          blocks((rows + 16 * kMT - 1) / (16 * kMT)) {}
+    // Row tiles of row block rb, and what one tile of its units costs.
+    __device__ __forceinline__ int act(int rb) const { return min((rows - rb * 16 * kMT + 15) / 16, kMT); }
+    __device__ __forceinline__ int cost(int rb) const { return kTileCost + act(rb); }
+    // All tiles of a unit of row block rb, and of all the request's units.
+    __device__ __forceinline__ int tiles(int rb) const { return span.size() * cost(rb); }
+    __device__ __forceinline__ unsigned long long tiles_of_all(int heads) const {
         if (blk.len == 0) return 0;
-        const Span s = span_of(blk, a.window);
-        first = s.first;
-        return s.size();
-    };
-    auto block_total = [&](unsigned v, unsigned& before) {      // inclusive scan over threads
-        unsigned incl = v;
-        #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const unsigned u = __shfl_up(incl, o, 64);
-            if (lane >= o) incl += u;
-        }
-        __syncthreads();
-        if (lane == 63) sh.scan[wave] = incl;
-        __syncthreads();
-        before = incl - v;
-        unsigned total = 0;
-        #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            if (w < wave) before += sh.scan[w];
-            total += sh.scan[w];
-        }
-        return total;
-    };
-    if (tid == 0) sh.found[0] = -1;
-    // The first of this thread's requests (the only one up to 256) is kept.
-    int units0 = 0, first0 = 0, n0 = 0;
-    unsigned mine = 0, before;
-    if (b0 < b1) n0 = tiles_of(b0, units0, first0);
-    mine = n0 * units0;
-    for (int b = b0 + 1; b < b1; ++b) {
-        int units, first = 0;
-        const int n = tiles_of(b, units, first);
-        mine += n * units;
+        return (unsigned long long)heads * ((unsigned long long)(blocks - 1) * tiles(0) + tiles(blocks - 1));
     }
-    const unsigned total = block_total(mine, before);
-    unsigned chunk = max((total + kManySplits - 1) / kManySplits,
-                         min((total + kFewSplits - 1) / kFewSplits, (unsigned)kChunk));
-    chunk = max(chunk, (unsigned)kLeastChunk);
-    mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        int units = units0, first, n = n0;
-        if (b > b0) n = tiles_of(b, units, first);
-        mine += (n + chunk - 1) / chunk * units;
-    }
-    block_total(mine, before);
-    for (int b = b0; b < b1; ++b) {
-        int units = units0, first = first0, n = n0;
-        if (b > b0) n = tiles_of(b, units, first);
-        const unsigned count = (n + chunk - 1) / chunk * units;
-        if ((unsigned)slot >= before && (unsigned)slot < before + count) {
-            const int in = slot - before, split = in / units;
-            sh.found[0] = b;
-            sh.found[1] = in % units;
-            sh.found[2] = first + split * chunk;
-            sh.found[3] = min(first + (split + 1) * (int)chunk, first + n);
-            sh.found[4] = count / units;
-            sh.found[5] = split;
-            sh.found[6] = before + in % units * (count / units);
-            if (in == 0) a.cut[b] = make_int2(before, chunk);
-        }
-        before += count;
-    }
-    __syncthreads();
-    if (sh.found[0] < 0) return false;
-    wk.b = __builtin_amdgcn_readfirstlane(sh.found[0]);
-    const int unit = __builtin_amdgcn_readfirstlane(sh.found[1]);
-    wk.h = unit % a.pages.heads;
-    wk.rb = unit / a.pages.heads;
-    wk.t0 = __builtin_amdgcn_readfirstlane(sh.found[2]);
-    wk.t1 = __builtin_amdgcn_readfirstlane(sh.found[3]);
-    wk.n = __builtin_amdgcn_readfirstlane(sh.found[4]);
-    wk.split = __builtin_amdgcn_readfirstlane(sh.found[5]);
-    wk.slot = __builtin_amdgcn_readfirstlane(sh.found[6]);
-    return true;
-}
+};
 
-// Waves per SIMD that the registers leave room for, and tiles in flight.
+// Waves per SIMD that the registers leave room for.
 template <int D, int kMT>
 constexpr int occupancy() {
-    return D == 256 || kMT == 4 ? 2 : D * kMT <= 128 ? 4 : D * kMT <= 256 ? 3 : 2;
-}
-template <int D, int kMT>
-constexpr int ahead() {
-    return D * kMT == 384 || (D == 256 && kMT == 1) ? 2 : 1;
+    return D == 256 || kMT == 4 ? 2 : D * kMT <= 128 ? 3 : 2;
 }
 
+// One run of tiles, from the queries to the output or a partial result.
 template <int D, int kMT>
-__global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(AttendArgs a) {
+__device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& wk, const Block& blk,
+                                           Lds<D, kMT>& sh, int lane, int wave) {
     using S = State<D, kMT>;
-    constexpr int kPlanes = S::kPlanes, kChans = S::kChans;
-    __shared__ Lds<D, kMT> sh;
-    const int lane = threadIdx.x & 63, x = lane & 15, quad = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-
-    if (blockIdx.x == 0) {            // report bad budgets and lengths, once per call
-        for (int b = threadIdx.x; b < a.B; b += 256) {
-            block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, a.status, true);
-        }
-    }
-    Work wk;
-    if (!find_work<D, kMT>(a, sh, wk)) return;
-    const Block blk = block_of(a.ctx_lens, a.budgets, wk.b, a.K + 1, a.pages, nullptr, false);
+    constexpr int kPlanes = S::kPlanes, kChans = S::kChans, kPieces = Lds<D, kMT>::kPieces;
+    constexpr int kOwn = (kMT * S::kSteps + kWaves - 1) / kWaves;
+    // Opaque: what derives from the lane is computed again for every run
+    // rather than kept in registers across the loop over runs.
+    asm volatile("" : "+v"(lane));
+    const int x = lane & 15, quad = lane >> 4;
     const int rows = blk.len * a.group;
-
-    Stream<D, ahead<D, kMT>()> stream;
-    stream.start(a, wk, blk, lane, wave);
+    const int act = min((rows - wk.rb * 16 * kMT + 15) / 16, kMT);
 
     // The queries as right operands: lane holds row x, 8 channels of its unit.
-    for (int i = wave; i < kMT * S::kSteps; i += kWaves) {
-        const int mt = i / S::kSteps, s = i % S::kSteps;
+    u32x4 own[kOwn];
+    #pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+        const int i = k * kWaves + wave, mt = i / S::kSteps, s = i % S::kSteps;
         const int r = (wk.rb * kMT + mt) * 16 + x, t = r / a.group;
-        u32x4 w = {0, 0, 0, 0};
-        if (r < rows) {
+        own[k] = u32x4{0, 0, 0, 0};
+        if (r < rows && mt < kMT) {
             const int ch = (s / S::kUnitSteps * 4 + quad) * (8 * S::kUnitSteps) + 8 * (s % S::kUnitSteps);
-            w = *reinterpret_cast<const u32x4*>(a.q + ((long long)wk.b * (a.K + 1) + t) * a.q_stride +
-                                                (wk.h * a.group + (r - t * a.group)) * D + ch);
-            if (a.negate) w ^= u32x4{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
+            own[k] = *reinterpret_cast<const u32x4*>(
+                a.q + ((long long)wk.b * (a.K + 1) + t) * a.q_stride +
+                (wk.h * a.group + (r - t * a.group)) * D + ch);
+            if (a.negate) own[k] ^= u32x4{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
         }
-        sh.q[mt][s][lane] = w;
     }
+    Stream<D> stream;
+    stream.start(a, wk, blk, lane, wave);
     S st;
     #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
@@ -555,16 +479,20 @@ __global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(Atte
             for (int j = 0; j < kChans; ++j) st.o[mt][p][j] = f32x4{0, 0, 0, 0};
         }
     }
+    #pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+        const int i = k * kWaves + wave;
+        if (i < kMT * S::kSteps) sh.q[i / S::kSteps][i % S::kSteps][lane] = own[k];
+    }
     __syncthreads();
 
-    const int act = min((rows - wk.rb * 16 * kMT + 15) / 16, kMT);
     if (kMT >= 4 && act == 4) stream.template run<kMT, (kMT < 4 ? 1 : 4)>(st, sh, a, wk, blk, lane, wave);
     else if (kMT >= 3 && act == 3) stream.template run<kMT, (kMT < 3 ? 1 : 3)>(st, sh, a, wk, blk, lane, wave);
     else if (kMT >= 2 && act == 2) stream.template run<kMT, (kMT < 2 ? 1 : 2)>(st, sh, a, wk, blk, lane, wave);
     else stream.template run<kMT, 1>(st, sh, a, wk, blk, lane, wave);
 
-    // Join the waves: component r of every accumulator in round r, of which
-    // wave r writes kChans consecutive channels per (row, plane).
+    // Join the waves, two components of every accumulator in each of two
+    // rounds; a wave adds up and writes every other piece of 4 channels of one.
     #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
         const float sum = quad_sum(st.sum[mt]);
@@ -594,141 +522,289 @@ __global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(Atte
         }
     }
     #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int round = 0; round < 2; ++round) {
         #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
+        for (int i = 0; i < kPieces; ++i) {
+            const int mt = i / (kPieces / kMT), p = i / (kChans / 4) % kPlanes, c = i % (kChans / 4) * 4;
+            if (mt >= act) continue;
             #pragma unroll
-            for (int p = 0; p < kPlanes; ++p) {
-                #pragma unroll
-                for (int c = 0; c < kChans; c += 4) {
-                    const f32x4 v = {st.o[mt][p][c][r], st.o[mt][p][c + 1][r],
-                                     st.o[mt][p][c + 2][r], st.o[mt][p][c + 3][r]};
-                    sh.o[wave][((mt * kPlanes + p) * kChans + c) / 4][lane] = v;
-                }
+            for (int k = 0; k < 2; ++k) {
+                const int r = 2 * round + k;
+                sh.o[wave][k][i][lane] = f32x4{st.o[mt][p][c][r], st.o[mt][p][c + 1][r],
+                                               st.o[mt][p][c + 2][r], st.o[mt][p][c + 3][r]};
             }
         }
         __syncthreads();
-        if (wave == r) {
+        const int k = wave & 1, m = 4 * quad + 2 * round + k;     // the lane's pieces of channels
+        #pragma unroll
+        for (int j = 0; j < (kPieces + 1) / 2; ++j) {
+            const int i = 2 * j + (wave >> 1);
+            if (i >= kPieces) continue;
+            const int mt = i / (kPieces / kMT), p = i / (kChans / 4) % kPlanes, c = i % (kChans / 4) * 4;
+            const int in = mt * 16 + x, row = wk.rb * (16 * kMT) + in;
+            if (row >= rows) continue;
+            const f32x4 v = (sh.o[0][k][i][lane] + sh.o[1][k][i][lane]) +
+                            (sh.o[2][k][i][lane] + sh.o[3][k][i][lane]);
+            const int ch = p * 128 + m * kChans + c;
+            // mt is the same for the whole wave but no constant.
+            float sum = total[0], ref = top[0];
             #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-                const int row = (wk.rb * kMT + mt) * 16 + x;
-                if (row >= rows) continue;
+            for (int n = 1; n < kMT; ++n) {
+                sum = mt == n ? total[n] : sum;
+                ref = mt == n ? top[n] : ref;
+            }
+            if (wk.slot < 0) {
                 const int t = row / a.group;
-                const long long part = wk.part(16 * kMT, mt * 16 + x);
-                if (wk.n > 1 && r == 0 && quad == 0) {
-                    a.part_ml[part] = make_float2(top[mt], total[mt]);
-                }
-                const float inv = 1.0f / total[mt];
+                const float inv = 1.0f / sum;
+                const unsigned w[2] = {pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)};
                 uint16_t* dst = a.out + (((long long)wk.b * (a.K + 1) + t) * a.Hq + wk.h * a.group +
-                                         (row - t * a.group)) * D;
-                #pragma unroll
-                for (int p = 0; p < kPlanes; ++p) {
-                    const int ch = p * 128 + (4 * quad + r) * kChans;
-                    f32x4 v[kChans / 4];
-                    #pragma unroll
-                    for (int c = 0; c < kChans / 4; ++c) {
-                        const int i = (mt * kPlanes + p) * (kChans / 4) + c;
-                        v[c] = (sh.o[0][i][lane] + sh.o[1][i][lane]) +
-                               (sh.o[2][i][lane] + sh.o[3][i][lane]);
-                    }
-                    if (wk.n == 1) {
-                        unsigned w[kChans / 2];
-                        #pragma unroll
-                        for (int c = 0; c < kChans; c += 2) {
-                            w[c / 2] = pack_bf16(v[c / 4][c % 4] * inv, v[c / 4][c % 4 + 1] * inv);
-                        }
-                        __builtin_memcpy(__builtin_assume_aligned(dst + ch, 2 * kChans), w, 2 * kChans);
-                    } else {
-                        #pragma unroll
-                        for (int c = 0; c < kChans / 4; ++c) {
-                            *reinterpret_cast<f32x4*>(a.part_o + part * D + ch + 4 * c) = v[c];
-                        }
-                    }
-                }
+                                         (row - t * a.group)) * D + ch;
+                __builtin_memcpy(__builtin_assume_aligned(dst, 8), w, 8);
+            } else {
+                const long long part = (long long)wk.slot * (16 * kMT) + in;
+                *reinterpret_cast<f32x4*>(a.part_o + part * D + ch) = v;
+                if (ch == 0) a.part_ml[part] = make_float2(ref, sum);
             }
         }
         __syncthreads();
     }
 }
 
-// Joins the splits of a unit's rows: a workgroup per unit and four rows, a
-// wavefront each. Lanes hold 4 channels, 256 / D splits lie side by side in a
-// wavefront, and the partials of kDeep of them each are in flight. The running
-// reference keeps this to one pass; the order of the sums is fixed by the
-// shapes and lengths.
+__device__ __forceinline__ Block plain_block(const AttendArgs& a, int b) {
+    return block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, nullptr, false);
+}
+template <int D, int kMT>
+__global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(AttendArgs a) {
+    __shared__ Lds<D, kMT> sh;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = scalar(tid >> 6);
+    const int heads = a.pages.heads, g = blockIdx.x;
+
+    if (g == 0) {                     // report bad budgets and lengths, once per call
+        for (int b = tid; b < a.B; b += 256) {
+            block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, a.status, true);
+        }
+    }
+    // Where this workgroup is: unit (b, h, rb), request b's first place on the
+    // line, and its stretch [lo, hi).
+    int b = -1, h = 0, rb = 0, lead = 0;
+    unsigned long long at = 0, lo = 0, hi = 0, share = 1;
+    Block blk{0, 0};
+    if (a.direct) {
+        rb = g % a.row_blocks;
+        h = g / a.row_blocks % heads;
+        const int mine = g / a.row_blocks / heads;
+        blk = scalar(plain_block(a, mine));
+        if (rb < Share<kMT>(a, blk).blocks) b = mine;
+    } else {
+        const int per = (a.B + 255) / 256;
+        const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+        if (tid == 0) sh.found = -1;
+        if (tid < 2) a.parts[2 * g + tid] = make_int4(0, 0, 0, 0);
+        unsigned long long mine = 0;
+        unsigned units = 0;
+        for (int i = b0; i < b1; ++i) {
+            const Share<kMT> s(a, plain_block(a, i));
+            mine += s.tiles_of_all(heads);
+            units += s.blocks * heads;
+        }
+        unsigned long long upto = mine;
+        unsigned units_upto = units;
+        #pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const unsigned long long u = __shfl_up(upto, o, 64);
+            const unsigned v = __shfl_up(units_upto, o, 64);
+            if (lane >= o) {
+                upto += u;
+                units_upto += v;
+            }
+        }
+        if (lane == 63) {
+            sh.scan[wave] = upto;
+            sh.scan_units[wave] = units_upto;
+        }
+        __syncthreads();
+        unsigned long long all = 0;
+        unsigned all_units = 0;
+        #pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) {
+                upto += sh.scan[w];
+                units_upto += sh.scan_units[w];
+            }
+            all += sh.scan[w];
+            all_units += sh.scan_units[w];
+        }
+        lead = scalar((int)min(all / (4 * gridDim.x), (unsigned long long)kUnitCost));
+        all += (unsigned long long)all_units * lead;
+        share = scalar(max((all + gridDim.x - 1) / gridDim.x, (unsigned long long)kLeastShare));
+        lo = g * share;
+        hi = lo + share;
+        upto += (unsigned long long)units_upto * lead;
+        mine += (unsigned long long)units * lead;
+        if (mine > 0 && upto - mine <= lo && lo < upto) {
+            at = upto - mine;
+            int i = b0;
+            for (; i < b1 - 1; ++i) {
+                const Share<kMT> s(a, plain_block(a, i));
+                const unsigned long long n = s.tiles_of_all(heads) + (unsigned long long)(s.blocks * heads) * lead;
+                if (lo < at + n) break;
+                at += n;
+            }
+            sh.found = i;
+            sh.before = at;
+        }
+        __syncthreads();
+        b = scalar(sh.found);
+        if (b >= 0) {
+            at = scalar(sh.before);
+            blk = scalar(plain_block(a, b));
+        }
+    }
+
+    while (b >= 0) {
+        const Share<kMT> s(a, blk);
+        Work wk{b, h, rb, s.span.first, s.span.end, -1};
+        const int unit = lead + s.tiles(rb);
+        if (!a.direct) {
+            const int cost = s.cost(rb), n = s.span.size();
+            const unsigned long long start = at + (unsigned long long)h * unit + lead;
+            const int i0 = lo > start ? (int)min((lo - start + cost - 1) / cost, (unsigned long long)n) : 0;
+            const int i1 = hi > start ? (int)min((hi - start + cost - 1) / cost, (unsigned long long)n) : 0;
+            wk.t0 = s.span.first + i0;
+            wk.t1 = s.span.first + i1;
+            if (i0 < i1 && (i0 > 0 || i1 < n)) {
+                wk.slot = 2 * g + (i0 == 0);
+                const int from = (int)(start / share);
+                const int to = (int)((start + (unsigned long long)(n - 1) * cost) / share);
+                if (tid == 0) {
+                    a.parts[wk.slot] = make_int4((b * heads + h) * a.row_blocks + rb, to - from + 1, g - from, from);
+                }
+            }
+        }
+        if (wk.t0 < wk.t1) attend_run<D, kMT>(a, wk, blk, sh, lane, wave);
+        if (a.direct) break;
+        // On to the next unit: heads, row blocks, requests.
+        if (++h == heads) {
+            at += (unsigned long long)heads * unit;
+            h = 0;
+            if (++rb == s.blocks) {
+                rb = 0;
+                int next = b + 1;
+                b = -1;
+                for (; next < a.B && b < 0; next += 64) {     // the next request that holds anything
+                    Block k{0, 0};
+                    if (next + lane < a.B) k = plain_block(a, next + lane);
+                    const unsigned long long some = __ballot(k.len > 0);
+                    if (some != 0) {
+                        const int i = __builtin_ctzll(some);
+                        b = next + i;
+                        blk = Block{__builtin_amdgcn_readlane(k.ctx, i), __builtin_amdgcn_readlane(k.len, i)};
+                    }
+                }
+            }
+        }
+        if (b >= 0 && at + (unsigned long long)h * (lead + Share<kMT>(a, blk).tiles(rb)) >= hi) b = -1;
+    }
+}
+
+// A sum of partial results under its running reference.
+struct Joined {
+    float ref, sum;
+    f32x4 acc;
+    __device__ __forceinline__ void add(float other_ref, float other_sum, const f32x4& other) {
+        const float top = fmaxf(ref, other_ref), base = top == kNegInf ? 0.0f : top;
+        const float f = exp2_fast(ref - base), g = exp2_fast(other_ref - base);
+        sum = sum * f + other_sum * g;
+        acc = acc * f + other * g;
+        ref = top;
+    }
+};
+
+// Joins the units that workgroups of the first kernel left in parts: the part
+// of workgroup `from` that starts the unit is in slot 2 from + 1, those of the
+// next ones in slots 2 (from + 1), 2 (from + 2), ... A workgroup here belongs
+// to one workgroup g there and four rows. A unit of fewer than four parts is
+// joined by the workgroups of its first part, a wavefront a row; of more, by
+// those of its first four parts, each taking one of the four rows with all its
+// wavefronts. Lanes hold 4 channels, 256 / D parts lie side by side in a
+// wavefront, kDeep of them each are in flight. The order of the sums is fixed
+// by the shapes and lengths of the call.
 template <int D, int kMT>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
-    constexpr int kSide = 256 / D, kLanes = 64 / kSide;     // splits side by side, lanes of each
+    constexpr int kSide = 256 / D, kLanes = 64 / kSide;     // parts side by side, lanes of each
     constexpr int kDeep = 8;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __shared__ Joined sh[kWaves][64];
+    const int lane = threadIdx.x & 63, wave = scalar((int)threadIdx.x >> 6);
     const int side = lane / kLanes, ch = lane % kLanes * 4;
-    int id = blockIdx.x;
-    const int in = id % (4 * kMT) * kWaves + wave;          // row of the row block
-    id /= 4 * kMT;
-    const int rb = id % a.row_blocks;
-    id /= a.row_blocks;
-    const int h = id % a.pages.heads, b = id / a.pages.heads;
-    const Block blk = block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, nullptr, false);
-    const int rows = blk.len * a.group, row = rb * (16 * kMT) + in;
-    if (row >= rows) return;
-    const int2 cut = a.cut[b];
-    const int n = (span_of(blk, a.window).size() + cut.y - 1) / cut.y;
-    if (n == 1) return;
-    const long long part = (long long)(cut.x + (rb * a.pages.heads + h) * n) * (16 * kMT) + in * n;
-
-    float ref = kNegInf, sum = 0.0f;
-    f32x4 acc = {0, 0, 0, 0};
-    for (int s0 = side; s0 < n; s0 += kDeep * kSide) {
-        f32x4 v[kDeep];
-        float2 ml[kDeep];
-        #pragma unroll
-        for (int k = 0; k < kDeep; ++k) {
-            const long long p = part + min(s0 + k * kSide, n - 1);
-            ml[k] = a.part_ml[p];
-            v[k] = *reinterpret_cast<const f32x4*>(a.part_o + p * D + ch);
-        }
-        float top = ref;
-        #pragma unroll
-        for (int k = 0; k < kDeep; ++k) top = fmaxf(top, ml[k].x);
-        const float base = top == kNegInf ? 0.0f : top;
-        const float keep = exp2_fast(ref - base);
-        sum *= keep;
-        acc *= keep;
-        ref = top;
-        #pragma unroll
-        for (int k = 0; k < kDeep; ++k) {
-            if (s0 + k * kSide >= n) break;
-            const float f = exp2_fast(ml[k].x - base);
-            sum += ml[k].y * f;
-            acc += v[k] * f;
-        }
-    }
+    const int g = blockIdx.x / (4 * kMT), in0 = blockIdx.x % (4 * kMT) * 4;
+    const int4 both[2] = {a.parts[2 * g], a.parts[2 * g + 1]};
     #pragma unroll
-    for (int o = kLanes; o < 64; o <<= 1) {
-        const float other = __shfl_xor(ref, o), top = fmaxf(ref, other);
-        const float base = top == kNegInf ? 0.0f : top;
-        const float f = exp2_fast(ref - base), g = exp2_fast(other - base);
-        sum = sum * f + __shfl_xor(sum, o) * g;
+    for (int slot = 0; slot < 2; ++slot) {
+        const int n = both[slot].y, s0 = both[slot].z, from = both[slot].w;
+        const bool many = n >= 4;
+        if (n == 0 || s0 >= (many ? 4 : 1)) continue;
+        const int rb = both[slot].x % a.row_blocks, h = both[slot].x / a.row_blocks % a.pages.heads;
+        const int b = both[slot].x / a.row_blocks / a.pages.heads;
+        const int in = in0 + (many ? s0 : wave);
+        const int row = rb * (16 * kMT) + in;
+        const Block blk = plain_block(a, b);
+        const bool live = row < blk.len * a.group;
+        const int by = many ? kWaves * kSide : kSide;
+
+        Joined j{kNegInf, 0.0f, {0, 0, 0, 0}};
+        for (int s = (many ? wave * kSide : 0) + side; live && s < n; s += kDeep * by) {
+            f32x4 v[kDeep];
+            float2 ml[kDeep];
+            #pragma unroll
+            for (int k = 0; k < kDeep; ++k) {
+                const int i = min(s + k * by, n - 1);
+                const long long p = (long long)(2 * (from + i) + (i == 0)) * (16 * kMT) + in;
+                ml[k] = a.part_ml[p];
+                v[k] = *reinterpret_cast<const f32x4*>(a.part_o + p * D + ch);
+            }
+            #pragma unroll
+            for (int k = 0; k < kDeep; ++k) {
+                if (s + k * by < n) j.add(ml[k].x, ml[k].y, v[k]);
+            }
+        }
         #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[c] = acc[c] * f + __shfl_xor(acc[c], o) * g;
-        ref = top;
-    }
-    if (side == 0) {
-        const int t = row / a.group, head = h * a.group + (row - t * a.group);
-        const float inv = 1.0f / sum;
-        const unsigned w[2] = {pack_bf16(acc[0] * inv, acc[1] * inv),
-                               pack_bf16(acc[2] * inv, acc[3] * inv)};
-        uint16_t* dst = a.out + (((long long)b * (a.K + 1) + t) * a.Hq + head) * D + ch;
-        __builtin_memcpy(__builtin_assume_aligned(dst, 8), w, 8);
+        for (int o = kLanes; o < 64; o <<= 1) {
+            f32x4 other;
+            #pragma unroll
+            for (int c = 0; c < 4; ++c) other[c] = __shfl_xor(j.acc[c], o);
+            j.add(__shfl_xor(j.ref, o), __shfl_xor(j.sum, o), other);
+        }
+        if (many) {
+            __syncthreads();
+            sh[wave][lane] = j;
+            __syncthreads();
+            j = sh[0][lane];
+            #pragma unroll
+            for (int w = 1; w < kWaves; ++w) j.add(sh[w][lane].ref, sh[w][lane].sum, sh[w][lane].acc);
+        }
+        if (live && side == 0 && (!many || wave == 0)) {
+            const int t = row / a.group, head = h * a.group + (row - t * a.group);
+            const float inv = 1.0f / j.sum;
+            const unsigned w[2] = {pack_bf16(j.acc[0] * inv, j.acc[1] * inv),
+                                   pack_bf16(j.acc[2] * inv, j.acc[3] * inv)};
+            uint16_t* dst = a.out + (((long long)b * (a.K + 1) + t) * a.Hq + head) * D + ch;
+            __builtin_memcpy(__builtin_assume_aligned(dst, 8), w, 8);
+        }
     }
 }
 
 // What the host fixes of a call: rows per wavefront, row blocks, workgroups.
 struct Plan {
-    int mt, row_blocks;
+    int mt, row_blocks, groups;
     bool direct;
-    long long slots;
 };
+
+template <int D>
+int resident(int mt) {      // workgroups of a kernel that the 256 CUs hold at once
+    return 256 * (mt == 1 ? occupancy<D, 1>() : mt == 2 ? occupancy<D, 2>()
+                  : mt == 3 ? occupancy<D, 3>() : occupancy<D, 4>());
+}
 
 Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_pages, int window) {
     Plan p;
@@ -737,20 +813,20 @@ Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_p
     p.mt = (rows + 15) / 16 < most ? (rows + 15) / 16 : most;
     p.row_blocks = (rows + 16 * p.mt - 1) / (16 * p.mt);
     const long long units = (long long)B * kv_heads * p.row_blocks;
-    // Splits: every unit's last one, and no more than kManySplits full ones
-    // or than the page table row can hold.
     long long tokens = (long long)max_pages * page_size;
     if (window > 0 && tokens > (long long)window + K + kTile) tokens = (long long)window + K + kTile;
     const long long tiles = (tokens + kTile - 1) / kTile + 1;
-    p.direct = units >= kDirectUnits || tiles <= kDirectTiles;
-    const long long per_unit = (tiles + kLeastChunk - 1) / kLeastChunk;
-    p.slots = p.direct ? units : std::min(units + kManySplits, units * per_unit);
+    p.direct = tiles <= kDirectTiles;
+    // No more workgroups than the longest line has shares for.
+    const long long most_shares = (units * (kUnitCost + tiles * (kTileCost + p.mt)) + kLeastShare - 1) / kLeastShare;
+    const int held = D == 64 ? resident<64>(p.mt) : D == 128 ? resident<128>(p.mt) : resident<256>(p.mt);
+    p.groups = (int)(p.direct ? units : std::min<long long>(held, most_shares));
     return p;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-size_t parts_of(const Plan& p) { return (size_t)p.slots * 16 * p.mt; }
+size_t parts_of(const Plan& p) { return (size_t)p.groups * 2 * 16 * p.mt; }
 
 bool shape_ok(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_pages, int window) {
     return B >= 0 && B <= SV_MAX_BATCH && K >= 0 && K <= SV_MAX_K && window >= 0 &&
@@ -760,9 +836,9 @@ bool shape_ok(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_
 
 template <int D, int kMT>
 void launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
-    hipLaunchKernelGGL((attend_kernel<D, kMT>), dim3((unsigned)p.slots), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((attend_kernel<D, kMT>), dim3((unsigned)p.groups), dim3(256), 0, s, a);
     if (!p.direct) {
-        const unsigned blocks = (unsigned)(a.B * a.pages.heads * p.row_blocks * 4 * kMT);
+        const unsigned blocks = (unsigned)(p.groups * 4 * kMT);
         hipLaunchKernelGGL((attend_join_kernel<D, kMT>), dim3(blocks), dim3(256), 0, s, a);
     }
 }
@@ -777,7 +853,7 @@ extern "C" size_t spec_verify_attention_workspace_bytes(int B, int K, int q_head
     }
     const Plan p = plan_of(B, K, q_heads, kv_heads, head_dim, page_size, max_pages, window);
     if (p.direct) return 256;
-    return round256((size_t)B * sizeof(int2)) + round256(parts_of(p) * sizeof(float2)) +
+    return round256((size_t)p.groups * 2 * sizeof(int4)) + round256(parts_of(p) * sizeof(float2)) +
            parts_of(p) * head_dim * sizeof(float);
 }
 
@@ -816,9 +892,9 @@ extern "C" int spec_verify_attention(const void* queries, int64_t query_stride, 
     a.out = static_cast<uint16_t*>(out);
     a.status = out_status;
     char* ws = static_cast<char*>(workspace);
-    a.cut = reinterpret_cast<int2*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(ws + round256((size_t)B * sizeof(int2)));
-    a.part_o = reinterpret_cast<float*>(ws + round256((size_t)B * sizeof(int2)) +
+    a.parts = reinterpret_cast<int4*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(ws + round256((size_t)p.groups * 2 * sizeof(int4)));
+    a.part_o = reinterpret_cast<float*>(ws + round256((size_t)p.groups * 2 * sizeof(int4)) +
                                         round256(parts_of(p) * sizeof(float2)));
     a.pages = make_pages(page_table, kv_heads, page_size, max_pages, num_pages);
     a.B = B;

@@ -100,16 +100,19 @@ struct Pages {
     int shift;              // log2(page_size)
     int heads;
 
-    // Tile of token position pos (>= 0) of request b, head h: byte offset in
-    // the cache, or -1 when the page is outside the pool. kUniform: the
-    // arguments are the same for the whole wavefront.
-    template <bool kUniform = false>
-    __device__ __forceinline__ long long tile(int b, int h, int pos, int tile_bytes) const {
-        int page = table[(size_t)b * max_pages + (pos >> shift)];
-        if (kUniform) page = __builtin_amdgcn_readfirstlane(page);
+    // The page that holds position pos (>= 0) of request b, as the table has it.
+    __device__ __forceinline__ int page(int b, int pos) const {
+        return table[(size_t)b * max_pages + (pos >> shift)];
+    }
+    // Tile of head h with position pos in that page: byte offset in the cache,
+    // or -1 when the page is outside the pool.
+    __device__ __forceinline__ long long tile_in(int page, int h, int pos, int tile_bytes) const {
         if ((unsigned)page >= (unsigned)num_pages) return -1;
         const int per = 1 << (shift - 5);
         return (((long long)page * heads + h) * per + ((pos >> 5) & (per - 1))) * tile_bytes;
+    }
+    __device__ __forceinline__ long long tile(int b, int h, int pos, int tile_bytes) const {
+        return tile_in(page(b, pos), h, pos, tile_bytes);
     }
 };
 
