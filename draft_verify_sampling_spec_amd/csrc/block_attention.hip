@@ -23,6 +23,7 @@
 #include <cmath>
 
 #include "cache_tile.h"
+#include "lds_dma.h"
 
 namespace {
 
@@ -36,19 +37,24 @@ constexpr int kWaves = 4;
 constexpr float kNegInf = -INFINITY;
 
 // How the work is cut. A unit is a request's kv head and block of 16 kMT
-// rows. All units' tiles lie on one line, a tile as long as its cost (kTileCost
-// plus its row tiles) and each unit led by a stretch for what starting and
-// ending one takes; every workgroup takes an equal share of the line, so that
-// ragged lengths and budgets load the chip evenly. The lengths are on the
-// device, so every workgroup lays the line out for itself (sums over the
-// requests and a prefix sum to find its place). A workgroup that ends inside a
-// unit leaves a partial result, which the join kernel puts together.
-// With page table rows of at most kDirectTiles tiles a workgroup per unit is
-// launched instead and nothing is joined: a second launch and the search
-// would cost more than the imbalance.
-constexpr int kTileCost = 2;
-constexpr int kUnitCost = 64;       // at most; a quarter of a share where shares are short
-constexpr int kLeastShare = 32;     // a few tiles for each of a workgroup's wavefronts
+// rows, its cost the tiles times (kTileCost plus their row tiles). The lengths
+// are on the device, so every workgroup adds up the requests for itself and
+// finds its place by a prefix sum. With `groups` workgroups resident at once
+// and C the cost of all units, one of two cuts is made:
+//  - aligned, C < kAlignedCost groups (short work): every unit is cut into
+//    round(cost / share) equal parts, at least one, for share = C / groups,
+//    and a workgroup takes one part. Starting and ending a run costs about as
+//    much as kAlignedCost / 4, so none takes two.
+//  - line: all units lie on one line, each led by a stretch of kUnitCost for
+//    starting and ending it, and each of `groups` workgroups takes an equal
+//    stretch, so that ragged lengths and budgets load the chip evenly.
+// Parts of a unit are put together by the join kernel. With page table rows of
+// at most kDirectTiles tiles a workgroup per unit is launched instead and
+// nothing is joined: the second launch and the search would cost more.
+constexpr int kTileCost = 5;
+constexpr int kUnitCost = 160;
+constexpr int kAlignedCost = 1536;
+constexpr int kLeastShare = 48;     // a few tiles for each of a workgroup's wavefronts
 constexpr int kDirectTiles = 32;
 
 struct AttendArgs {
@@ -61,9 +67,10 @@ struct AttendArgs {
     int32_t* status;
     float* part_o;      // [slot][16 kMT rows][D], not normalised
     float2* part_ml;    // [slot][16 kMT rows]: reference exponent, sum
-    int4* parts;        // [slot]: unit, its parts, which one this is, workgroup of the first
+    int4* parts;        // [workgroup][2]: unit, its parts, which one this is, first slot (see slot_of)
     Pages pages;
     int B, K, Hq, group;
+    int groups;         // workgroups resident at once
     int row_blocks;     // blocks of 16 kMT rows of a full block's (K + 1) group rows
     int window;
     bool direct;        // a workgroup per unit
@@ -82,11 +89,17 @@ __device__ __forceinline__ Span span_of(const Block& blk, int window) {
 }
 
 // A run of one unit's tiles: [t0, t1) of (b, h, row block rb); slot: where its
-// partial result goes (slot 2 g + 1 of the workgroup g that starts the unit,
-// 2 g of those that go on with it), or -1 when the run is the whole unit.
+// partial result goes, or -1 when the run is the whole unit.
 struct Work {
     int b, h, rb, t0, t1, slot;
 };
+
+// Slot of part i of a unit whose first part has slot `first`. On the line a
+// workgroup g may end one unit (slot 2 g) and start another (slot 2 g + 1);
+// aligned parts follow each other (first >= 0 there, ~first on the line).
+__device__ __forceinline__ int slot_of(int first, int i) {
+    return first >= 0 ? first + i : ~first + (i > 0 ? 2 * i - 1 : 0);
+}
 
 __device__ __forceinline__ unsigned pack_bf16(float a, float b) {
     bf16x2 v;
@@ -117,93 +130,89 @@ __device__ __forceinline__ float quad_sum(float v) {
 }
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-// A tile's bytes as one lane holds them.
-template <int D>
-struct Frag {
-    using L = Tile<D>;
-    static constexpr int kWords = L::U / 4;             // words of a key unit
-    unsigned k[2][L::kPlanes][kWords];                  // half, plane: a token's unit of channels
-    unsigned v[2][L::kPlanes][L::C];                    // half, plane: 4 tokens' pieces
-    unsigned ks[L::kPlanes];                            // key scales of both halves
-    unsigned vs[L::kPlanes][2];                         // value scales of 4 + 4 tokens
-
-    // The tile is the same for the whole wavefront: one scalar base, a 32-bit
-    // offset per lane.
-    __device__ __forceinline__ void load(const uint8_t* tile, unsigned lane) {
-        const unsigned x = lane & 15, quad = lane >> 4;
-        #pragma unroll
-        for (int p = 0; p < L::kPlanes; ++p) {
-            #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                __builtin_memcpy(k[half][p], __builtin_assume_aligned(
-                    tile + (half * 8 * D + p * 64 * L::U) + lane * L::U, L::U), L::U);
-                __builtin_memcpy(v[half][p], __builtin_assume_aligned(
-                    tile + (L::kVCodes + (p * 2 + half) * 256 * L::C) + lane * (4 * L::C), 4 * L::C), 4 * L::C);
-            }
-            const unsigned kg = D == 64 ? quad >> 1 : quad, vg = D == 64 ? x >> 3 : x >> 2;
-            ks[p] = *reinterpret_cast<const uint16_t*>(tile + (L::kKScales + p * 128) + (kg * 32 + x * 2));
-            __builtin_memcpy(vs[p], __builtin_assume_aligned(
-                tile + (L::kVScales + p * 128) + (vg * 4 + quad) * 8, 8), 8);
-        }
-    }
-};
-
-// Registers of one wavefront over its tiles.
-template <int D, int kMT>
+// Registers of one wavefront over its tiles, for kAct row tiles.
+template <int D, int kAct>
 struct State {
     using L = Tile<D>;
     static constexpr int kPlanes = L::kPlanes;
     static constexpr int kUnitSteps = D == 64 ? 2 : 4;  // products of 32 channels in a key unit
     static constexpr int kSteps = D / 32;
     static constexpr int kChans = D == 64 ? 4 : 8;      // channels of a value piece
-    f32x4 o[kMT][kPlanes][kChans];
-    float ref[kMT];     // reference of the exponents; -inf: nothing seen
-    float sum[kMT];     // this lane's share of the row's sum
-    int pos[kMT];       // the row's position; -1 past the block
+    f32x4 o[kAct][kPlanes][kChans];
+    float ref[kAct];     // reference of the exponents; -inf: nothing seen
+    float sum[kAct];     // this lane's share of the row's sum
+    int pos[kAct];       // the row's position; -1 past the block
 };
+
+// Tiles of a wavefront's ring in LDS: one worked on, the others on their way.
+// Two where a third would cost a resident workgroup.
+template <int D, int kMT>
+constexpr int depth() {
+    return D * kMT == 128 || D * kMT == 256 ? 2 : 3;
+}
+
+// Bytes of a place: a tile, and what a load of the scales writes behind it.
+template <int D>
+constexpr int ring_bytes() {
+    return 32 * D + (2 * D + 255) / 256 * 256;
+}
 
 template <int D, int kMT>
 struct Lds {
     static constexpr int kPieces = kMT * Tile<D>::kPlanes * (D == 64 ? 4 : 8) / 4;  // float4 per lane and component
-    union {
+    struct Loop {
         u32x4 q[kMT][D / 32][64];           // right operands of K Q^T
+        unsigned char ring[kWaves][depth<D, kMT>()][ring_bytes<D>()];
+    };
+    union {
+        Loop loop;
         f32x4 o[kWaves][2][kPieces][64];    // two components of the accumulators at a time
     };
     float ref[kWaves][kMT][16];
     float sum[kWaves][kMT][16];
-    unsigned long long scan[kWaves], before;
-    unsigned scan_units[kWaves];
+    unsigned long long cost[kWaves], scan[kWaves], before;
+    unsigned units[kWaves];
     int found;
 };
 
-// One tile. kAct: row tiles that hold rows of the block. kMasked: some row
-// does not see some token of the tile.
+// One tile. kMasked: some row does not see some token of it.
 template <int D, int kMT, int kAct, bool kMasked>
-__device__ __forceinline__ void tile_step(State<D, kMT>& st, const Frag<D>& f,
-                                          const Lds<D, kMT>& sh, const AttendArgs& a, int lane,
-                                          int tok0, int last, const uint8_t* tile) {
+__device__ __forceinline__ void tile_step(State<D, kAct>& st, const Lds<D, kMT>& sh,
+                                          const AttendArgs& a, int lane, int tok0, int last,
+                                          const unsigned char* tile) {
     using L = Tile<D>;
-    using S = State<D, kMT>;
-    const int quad = lane >> 4;
+    using S = State<D, kAct>;
+    // Opaque: the masks' token numbers are computed here, not kept in
+    // registers throughout the loop over tiles.
+    if (kMasked) asm volatile("" : "+v"(lane));
+    const int x = lane & 15, quad = lane >> 4;
     // Scores of 2 x 16 tokens (lane: tokens 16 half + 4 quad + r).
     f32x4 z[kAct][2] = {};
     #pragma unroll
     for (int p = 0; p < S::kPlanes; ++p) {
-        const float s[2] = {scale_of(f.ks[p] & 255u), scale_of(f.ks[p] >> 8)};
+        unsigned k[2][L::U / 4];
+        #pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            __builtin_memcpy(k[half], __builtin_assume_aligned(
+                tile + (half * 8 * D + p * 64 * L::U) + lane * L::U, L::U), L::U);
+        }
+        const int kg = D == 64 ? quad >> 1 : p * 4 + quad;
+        const unsigned ks = *reinterpret_cast<const uint16_t*>(tile + L::kKScales + kg * 32 + x * 2);
+        const float s[2] = {scale_of(ks & 255u), scale_of(ks >> 8)};
         #pragma unroll
         for (int j = 0; j < S::kUnitSteps; ++j) {
             __builtin_amdgcn_sched_barrier(0);
             bf16x8 kf[2];
             #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const unsigned w = f.k[half][p][j];
+                const unsigned w = k[half][j];
                 const u32x4 kw = {decode2<0>(w, s[half]), decode2<1>(w, s[half]),
                                   decode2<2>(w, s[half]), decode2<3>(w, s[half])};
                 kf[half] = __builtin_bit_cast(bf16x8, kw);
             }
             #pragma unroll
             for (int mt = 0; mt < kAct; ++mt) {
-                const bf16x8 qf = __builtin_bit_cast(bf16x8, sh.q[mt][p * S::kUnitSteps + j][lane]);
+                const bf16x8 qf = __builtin_bit_cast(bf16x8, sh.loop.q[mt][p * S::kUnitSteps + j][lane]);
                 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     z[mt][half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[half], qf, z[mt][half], 0, 0, 0);
@@ -262,18 +271,26 @@ __device__ __forceinline__ void tile_step(State<D, kMT>& st, const Frag<D>& f,
     // Values: 8 tokens (4 quad + r of both halves) x kChans channels a plane.
     #pragma unroll
     for (int p = 0; p < S::kPlanes; ++p) {
-        unsigned w[8];
+        unsigned v[2][L::C], sc2[2], w[8];
+        #pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            __builtin_memcpy(v[half], __builtin_assume_aligned(
+                tile + (L::kVCodes + (p * 2 + half) * 256 * L::C) + lane * (4 * L::C), 4 * L::C), 4 * L::C);
+        }
+        const int vg = D == 64 ? x >> 3 : p * 4 + (x >> 2);
+        __builtin_memcpy(sc2, __builtin_assume_aligned(
+            tile + L::kVScales + (vg * 4 + quad) * 8, 8), 8);
         float vs[8];
         bool poison = false;
         #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int half = i >> 2, r = i & 3;
             if constexpr (D == 64) {
-                w[i] = r & 1 ? f.v[half][p][r >> 1] >> 16 : f.v[half][p][r >> 1];
+                w[i] = r & 1 ? v[half][r >> 1] >> 16 : v[half][r >> 1];
             } else {
-                w[i] = f.v[half][p][r];
+                w[i] = v[half][r];
             }
-            const unsigned sc = f.vs[p][half];
+            const unsigned sc = sc2[half];
             unsigned bits = (r == 3 ? sc >> 1 : sc << (23 - 8 * r)) & 0x7f800000u;
             if (kMasked) {
                 // What some row does not see must not reach it as 0 * NaN:
@@ -322,90 +339,120 @@ __device__ __forceinline__ void tile_step(State<D, kMT>& st, const Frag<D>& f,
             const int og = D == 64 ? quad >> 1 : p * 4 + quad;
             for (int tok = 0; tok < kTile; ++tok) {
                 const int j = tok0 + tok;
-                if (j > last || tile[L::v_scale(tok, og)] != 255u) continue;
+                const bool nan = j <= last && tile[L::v_scale(tok, og)] == 255u;
                 #pragma unroll
                 for (int mt = 0; mt < kAct; ++mt) {
-                    if (j > st.pos[mt] || (a.window > 0 && j <= st.pos[mt] - a.window)) continue;
+                    const bool seen = j <= st.pos[mt] && (a.window == 0 || j > st.pos[mt] - a.window);
+                    const float add = nan && seen ? NAN : 0.0f;
                     #pragma unroll
-                    for (int c = 0; c < S::kChans; ++c) st.o[mt][p][c] *= NAN;
+                    for (int c = 0; c < S::kChans; ++c) st.o[mt][p][c] += add;
                 }
             }
         }
     }
 }
 
-// This wavefront's share of the tiles [t0, t1). The tiles that every row sees
-// whole come in a loop that keeps the next tile's bytes in flight; the few at the ends that some row does not see whole (the block's
-// own, and the windows' edges) are worked on one by one while the loop's first
-// bytes are on their way.
-template <int D>
+// This wavefront's share of a run: of the run's tiles, those that some row
+// does not see whole first (the block's own, the windows' edges), then the
+// others, every kWaves-th by number n = 0, 1, ... Their bytes come into the
+// wavefront's ring in LDS by buffer-to-LDS loads, kDepth - 1 tiles ahead, which
+// takes no registers and no barrier.
+template <int D, int kMT>
 struct Stream {
     using L = Tile<D>;
-    Frag<D> f[2];
-    long long at[2];
-    int t, u0, u1;
-    // Page numbers of this wavefront's next 64 tiles, one a lane. They come in
-    // one load: a lookup per tile would wait for every load before it, the
-    // tiles in flight among them.
+    static constexpr int kDepth = depth<D, kMT>();
+    static constexpr int kWide = 32 * D / 1024;             // loads of 64 x 16 bytes: the codes
+    static constexpr int kNarrow = (2 * D + 255) / 256;     // loads of 64 x 4 bytes: the scales
+    static constexpr int kLoads = kWide + kNarrow;
+    static_assert(32 * D % 1024 == 0, "whole loads");
+    unsigned char* ring;
+    int wave, first, low, u0, u1, edges, count;     // tiles [u0, u1) are seen whole by every row
+    int n, place;           // the next tile and its place in the ring
+    bool bad;               // a page was outside the pool
+    // Page numbers of the next 64 tiles, one a lane. They come in one load: a
+    // lookup per tile would wait for every load before it, the tiles in flight
+    // among them.
     int pages;
 
-    // A tile whose page is bad is flagged and skipped; the first tile of the
-    // cache stands in for its bytes, and past the end for the bytes of no tile.
-    __device__ __forceinline__ long long locate(const AttendArgs& a, const Work& wk, int page,
-                                                int tile, int lane) const {
-        const long long p = a.pages.tile_in(page, wk.h, tile * kTile, L::kBytes);
-        if (p < 0 && lane == 0) flag(a.status, SV_FLAG_BAD_PAGE);
-        return p;
+    __device__ __forceinline__ int tile_of(int number) const {
+        const int i = wave + number * kWaves;
+        return i < low ? first + i : i < edges ? u1 + (i - low) : u0 + (i - edges);
     }
-    // The wavefront's tile number n = (tile - u0 - wave) / kWaves into f[i].
-    template <int i>
-    __device__ __forceinline__ void fetch(const AttendArgs& a, const Work& wk, int tile, int n,
+    __device__ __forceinline__ void fetch(const AttendArgs& a, const Work& wk, int number, int to,
                                           int lane) {
-        at[i] = -1;
-        if (tile < u1) {
-            if ((n & 63) == 0) {
-                const int mine = tile + lane * kWaves;
-                pages = mine < u1 ? a.pages.page(wk.b, mine * kTile) : -1;
-            }
-            at[i] = locate(a, wk, __builtin_amdgcn_readlane(pages, n & 63), tile, lane);
+        // No branch in the loop over tiles depends on the lane: where one does,
+        // the compiler may keep a second set of accumulators.
+        if ((number & 63) == 0) {
+            pages = a.pages.page(wk.b, tile_of(min(number + lane, count - 1)) * kTile);
         }
-        f[i].load(a.cache + max(at[i], 0ll), lane);
+        long long at = a.pages.tile_in(__builtin_amdgcn_readlane(pages, number & 63), wk.h,
+                                       tile_of(number) * kTile, L::kBytes);
+        // The first tile of the cache stands in for one whose page is bad (the
+        // request is flagged and its outputs are undefined).
+        if (at < 0) {
+            bad = true;
+            at = 0;
+        }
+        const __amdgpu_buffer_rsrc_t src = svdma::rsrc(a.cache + at, L::kBytes);
+        unsigned char* dst = ring + to * ring_bytes<D>();
+        #pragma unroll
+        for (int i = 0; i < kWide; ++i) svdma::load16(src, i * 1024 + lane * 16, dst + i * 1024);
+        #pragma unroll
+        for (int i = 0; i < kNarrow; ++i) {
+            svdma::load4(src, 32 * D + i * 256 + lane * 4, dst + 32 * D + i * 256);
+        }
     }
     __device__ __forceinline__ void start(const AttendArgs& a, const Work& wk, const Block& blk,
-                                          int lane, int wave) {
-        // Tiles [u0, u1) of this run lie wholly in [all_lo, ctx + 1), the
-        // tokens that every row of the block sees.
+                                          unsigned char* lds, int lane, int its_wave) {
+        ring = lds;
+        wave = its_wave;
+        // Tokens that every row of the block sees: [all_lo, ctx + 1).
         const int all_lo = a.window > 0 ? max(0, blk.ctx + blk.len - a.window) : 0;
+        first = wk.t0;
         u0 = min(max(wk.t0, (all_lo + kTile - 1) / kTile), wk.t1);
         u1 = max(u0, min(wk.t1, (blk.ctx + 1) / kTile));
-        t = u0 + wave;
-        if (t < u1) fetch<0>(a, wk, t, 0, lane);
+        low = u0 - wk.t0;
+        edges = low + wk.t1 - u1;
+        count = (wk.t1 - wk.t0 - wave + kWaves - 1) / kWaves;
+        n = place = 0;
+        bad = false;
+        #pragma unroll
+        for (int i = 0; i < kDepth - 1; ++i) {
+            if (i < count) fetch(a, wk, i, i, lane);
+        }
     }
-    template <int kMT, int kAct>
-    __device__ __forceinline__ void run(State<D, kMT>& st, const Lds<D, kMT>& sh,
+    // Makes tile n's bytes ready. The place of tile n - 1 is read out (its
+    // values were used): the tile kDepth - 1 ahead goes there. Loads complete
+    // in order, so tile n is here when at most those of the tiles after it are
+    // outstanding.
+    __device__ __forceinline__ const unsigned char* next(const AttendArgs& a, const Work& wk,
+                                                         int lane) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (n + kDepth - 1 < count) {
+            fetch(a, wk, n + kDepth - 1, place == 0 ? kDepth - 1 : place - 1, lane);
+            svdma::wait_vm<(kDepth - 1) * kLoads>();
+        } else {
+            svdma::wait_vm<0>();
+        }
+        asm volatile("" ::: "memory");
+        return ring + place * ring_bytes<D>();
+    }
+    __device__ __forceinline__ void step() {
+        ++n;
+        place = place == kDepth - 1 ? 0 : place + 1;
+    }
+    template <int kAct>
+    __device__ __forceinline__ void run(State<D, kAct>& st, const Lds<D, kMT>& sh,
                                         const AttendArgs& a, const Work& wk, const Block& blk,
-                                        int lane, int wave) {
-        const int last = blk.ctx + blk.len - 1;
-        const int edges = (u0 - wk.t0) + (wk.t1 - u1);
-        for (int i = kWaves - 1 - wave; i < edges; i += kWaves) {
-            const int e = wk.t0 + i < u0 ? wk.t0 + i : u1 + (i - (u0 - wk.t0));
-            const long long edge = locate(a, wk, scalar(a.pages.page(wk.b, e * kTile)), e, lane);
-            if (edge < 0) continue;
-            Frag<D> g;
-            g.load(a.cache + edge, lane);
-            tile_step<D, kMT, kAct, true>(st, g, sh, a, lane, e * kTile, last, a.cache + edge);
+                                        int lane) {
+        for (; wave + n * kWaves < edges; step()) {
+            const unsigned char* tile = next(a, wk, lane);
+            tile_step<D, kMT, kAct, true>(st, sh, a, lane, tile_of(n) * kTile, blk.ctx + blk.len - 1, tile);
         }
-        for (int n = 1; t < u1; n += 2) {
-            step<kMT, kAct, 0>(st, sh, a, wk, n, lane);
-            step<kMT, kAct, 1>(st, sh, a, wk, n + 1, lane);
+        for (; n < count; step()) {
+            const unsigned char* tile = next(a, wk, lane);
+            tile_step<D, kMT, kAct, false>(st, sh, a, lane, 0, 0, tile);
         }
-    }
-    template <int kMT, int kAct, int i>
-    __device__ __forceinline__ void step(State<D, kMT>& st, const Lds<D, kMT>& sh,
-                                         const AttendArgs& a, const Work& wk, int n, int lane) {
-        fetch<1 - i>(a, wk, t + kWaves, n, lane);
-        if (at[i] >= 0) tile_step<D, kMT, kAct, false>(st, f[i], sh, a, lane, 0, 0, nullptr);
-        t += kWaves;
     }
 };
 
@@ -421,33 +468,43 @@ struct Share {
     // Row tiles of row block rb, and what one tile of its units costs.
     __device__ __forceinline__ int act(int rb) const { return min((rows - rb * 16 * kMT + 15) / 16, kMT); }
     __device__ __forceinline__ int cost(int rb) const { return kTileCost + act(rb); }
-    // All tiles of a unit of row block rb, and of all the request's units.
+    // Parts of a unit when the cut is aligned: tiles / share, rounded, at
+    // least 1 and at most one a tile.
+    __device__ __forceinline__ int parts(int rb, int share) const {
+        return min(max((tiles(rb) + share / 2) / share, 1), max(span.size(), 1));
+    }
+    // All tiles of a unit of row block rb.
     __device__ __forceinline__ int tiles(int rb) const { return span.size() * cost(rb); }
-    __device__ __forceinline__ unsigned long long tiles_of_all(int heads) const {
+    // Sum over all the request's units of f(row block).
+    template <typename F>
+    __device__ __forceinline__ unsigned long long sum(int heads, F f) const {
         if (blk.len == 0) return 0;
-        return (unsigned long long)heads * ((unsigned long long)(blocks - 1) * tiles(0) + tiles(blocks - 1));
+        return (unsigned long long)heads * ((unsigned long long)(blocks - 1) * f(0) + f(blocks - 1));
     }
 };
 
 // Waves per SIMD that the registers leave room for.
 template <int D, int kMT>
 constexpr int occupancy() {
-    return D == 256 || kMT == 4 ? 2 : D * kMT <= 128 ? 3 : 2;
+    return D * kMT == 512 && D == 256 ? 1 : D == 256 ? 2 : kMT == 1 ? 4 : kMT == 2 ? 3 : 2;
 }
 
-// One run of tiles, from the queries to the output or a partial result.
-template <int D, int kMT>
-__device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& wk, const Block& blk,
+// One run of tiles, from the queries to the output or a partial result, for a
+// row block of which kAct row tiles hold rows.
+template <int D, int kMT, int kAct>
+__device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any, const Block& its,
                                            Lds<D, kMT>& sh, int lane, int wave) {
-    using S = State<D, kMT>;
-    constexpr int kPlanes = S::kPlanes, kChans = S::kChans, kPieces = Lds<D, kMT>::kPieces;
-    constexpr int kOwn = (kMT * S::kSteps + kWaves - 1) / kWaves;
+    // The same for the whole wavefront, and to be kept in scalar registers.
+    const Work wk{scalar(any.b), scalar(any.h), scalar(any.rb), scalar(any.t0), scalar(any.t1), scalar(any.slot)};
+    const Block blk = scalar(its);
+    using S = State<D, kAct>;
+    constexpr int kPlanes = S::kPlanes, kChans = S::kChans, kPieces = kAct * kPlanes * kChans / 4;
+    constexpr int kOwn = (kAct * S::kSteps + kWaves - 1) / kWaves;
     // Opaque: what derives from the lane is computed again for every run
     // rather than kept in registers across the loop over runs.
     asm volatile("" : "+v"(lane));
     const int x = lane & 15, quad = lane >> 4;
     const int rows = blk.len * a.group;
-    const int act = min((rows - wk.rb * 16 * kMT + 15) / 16, kMT);
 
     // The queries as right operands: lane holds row x, 8 channels of its unit.
     u32x4 own[kOwn];
@@ -456,7 +513,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& wk, 
         const int i = k * kWaves + wave, mt = i / S::kSteps, s = i % S::kSteps;
         const int r = (wk.rb * kMT + mt) * 16 + x, t = r / a.group;
         own[k] = u32x4{0, 0, 0, 0};
-        if (r < rows && mt < kMT) {
+        if (r < rows && mt < kAct) {
             const int ch = (s / S::kUnitSteps * 4 + quad) * (8 * S::kUnitSteps) + 8 * (s % S::kUnitSteps);
             own[k] = *reinterpret_cast<const u32x4*>(
                 a.q + ((long long)wk.b * (a.K + 1) + t) * a.q_stride +
@@ -464,11 +521,11 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& wk, 
             if (a.negate) own[k] ^= u32x4{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
         }
     }
-    Stream<D> stream;
-    stream.start(a, wk, blk, lane, wave);
+    Stream<D, kMT> stream;
+    stream.start(a, wk, blk, sh.loop.ring[wave][0], lane, wave);
     S st;
     #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
+    for (int mt = 0; mt < kAct; ++mt) {
         const int r = (wk.rb * kMT + mt) * 16 + x;
         st.pos[mt] = r < rows ? blk.ctx + r / a.group : -1;
         st.ref[mt] = kNegInf;
@@ -482,29 +539,26 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& wk, 
     #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
         const int i = k * kWaves + wave;
-        if (i < kMT * S::kSteps) sh.q[i / S::kSteps][i % S::kSteps][lane] = own[k];
+        if (i < kAct * S::kSteps) sh.loop.q[i / S::kSteps][i % S::kSteps][lane] = own[k];
     }
-    __syncthreads();
-
-    if (kMT >= 4 && act == 4) stream.template run<kMT, (kMT < 4 ? 1 : 4)>(st, sh, a, wk, blk, lane, wave);
-    else if (kMT >= 3 && act == 3) stream.template run<kMT, (kMT < 3 ? 1 : 3)>(st, sh, a, wk, blk, lane, wave);
-    else if (kMT >= 2 && act == 2) stream.template run<kMT, (kMT < 2 ? 1 : 2)>(st, sh, a, wk, blk, lane, wave);
-    else stream.template run<kMT, 1>(st, sh, a, wk, blk, lane, wave);
+    svdma::ring_barrier();            // leaves the tiles in flight
+    stream.run(st, sh, a, wk, blk, lane);
+    if (stream.bad && lane == 0) flag(a.status, SV_FLAG_BAD_PAGE);
 
     // Join the waves, two components of every accumulator in each of two
     // rounds; a wave adds up and writes every other piece of 4 channels of one.
     #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
+    for (int mt = 0; mt < kAct; ++mt) {
         const float sum = quad_sum(st.sum[mt]);
         if (quad == 0) {
             sh.ref[wave][mt][x] = st.ref[mt];
             sh.sum[wave][mt][x] = sum;
         }
     }
-    __syncthreads();
-    float total[kMT], top[kMT];
+    svdma::ring_barrier();
+    float total[kAct], top[kAct];
     #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
+    for (int mt = 0; mt < kAct; ++mt) {
         top[mt] = kNegInf;
         #pragma unroll
         for (int w = 0; w < kWaves; ++w) top[mt] = fmaxf(top[mt], sh.ref[w][mt][x]);
@@ -525,8 +579,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& wk, 
     for (int round = 0; round < 2; ++round) {
         #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int mt = i / (kPieces / kMT), p = i / (kChans / 4) % kPlanes, c = i % (kChans / 4) * 4;
-            if (mt >= act) continue;
+            const int mt = i / (kPieces / kAct), p = i / (kChans / 4) % kPlanes, c = i % (kChans / 4) * 4;
             #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int r = 2 * round + k;
@@ -534,13 +587,13 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& wk, 
                                                st.o[mt][p][c + 2][r], st.o[mt][p][c + 3][r]};
             }
         }
-        __syncthreads();
+        svdma::ring_barrier();
         const int k = wave & 1, m = 4 * quad + 2 * round + k;     // the lane's pieces of channels
         #pragma unroll
         for (int j = 0; j < (kPieces + 1) / 2; ++j) {
             const int i = 2 * j + (wave >> 1);
             if (i >= kPieces) continue;
-            const int mt = i / (kPieces / kMT), p = i / (kChans / 4) % kPlanes, c = i % (kChans / 4) * 4;
+            const int mt = i / (kPieces / kAct), p = i / (kChans / 4) % kPlanes, c = i % (kChans / 4) * 4;
             const int in = mt * 16 + x, row = wk.rb * (16 * kMT) + in;
             if (row >= rows) continue;
             const f32x4 v = (sh.o[0][k][i][lane] + sh.o[1][k][i][lane]) +
@@ -549,7 +602,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& wk, 
             // mt is the same for the whole wave but no constant.
             float sum = total[0], ref = top[0];
             #pragma unroll
-            for (int n = 1; n < kMT; ++n) {
+            for (int n = 1; n < kAct; ++n) {
                 sum = mt == n ? total[n] : sum;
                 ref = mt == n ? top[n] : ref;
             }
@@ -566,7 +619,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& wk, 
                 if (ch == 0) a.part_ml[part] = make_float2(ref, sum);
             }
         }
-        __syncthreads();
+        svdma::ring_barrier();
     }
 }
 
@@ -585,15 +638,16 @@ __global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(Atte
             block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, a.status, true);
         }
     }
-    // Where this workgroup is: unit (b, h, rb), request b's first place on the
-    // line, and its stretch [lo, hi).
-    int b = -1, h = 0, rb = 0, lead = 0;
+    // Where this workgroup is: unit (b, h, rb); on the line, its stretch
+    // [lo, hi) and request b's first place; of an aligned unit, its part.
+    int b = -1, h = 0, rb = 0, part = 0;
     unsigned long long at = 0, lo = 0, hi = 0, share = 1;
+    bool aligned = false;
     Block blk{0, 0};
     if (a.direct) {
-        rb = g % a.row_blocks;
-        h = g / a.row_blocks % heads;
-        const int mine = g / a.row_blocks / heads;
+        rb = scalar(g % a.row_blocks);
+        h = scalar(g / a.row_blocks % heads);
+        const int mine = scalar(g / a.row_blocks / heads);
         blk = scalar(plain_block(a, mine));
         if (rb < Share<kMT>(a, blk).blocks) b = mine;
     } else {
@@ -601,53 +655,55 @@ __global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(Atte
         const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
         if (tid == 0) sh.found = -1;
         if (tid < 2) a.parts[2 * g + tid] = make_int4(0, 0, 0, 0);
-        unsigned long long mine = 0;
+        // The first of this thread's requests (the only one up to 256) is kept.
+        const Share<kMT> first(a, b0 < b1 ? plain_block(a, b0) : Block{0, 0});
+        unsigned long long cost = 0;
         unsigned units = 0;
         for (int i = b0; i < b1; ++i) {
-            const Share<kMT> s(a, plain_block(a, i));
-            mine += s.tiles_of_all(heads);
+            const Share<kMT> s = i == b0 ? first : Share<kMT>(a, plain_block(a, i));
+            cost += s.sum(heads, [&](int r) { return s.tiles(r); });
             units += s.blocks * heads;
         }
+        #pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            cost += __shfl_xor(cost, o, 64);
+            units += __shfl_xor(units, o, 64);
+        }
+        if (lane == 0) {
+            sh.cost[wave] = cost;
+            sh.units[wave] = units;
+        }
+        __syncthreads();
+        cost = scalar((sh.cost[0] + sh.cost[1]) + (sh.cost[2] + sh.cost[3]));
+        units = scalar((int)((sh.units[0] + sh.units[1]) + (sh.units[2] + sh.units[3])));
+        // Aligned parts: no more than groups + units workgroups.
+        aligned = cost < (unsigned long long)kAlignedCost * a.groups && a.groups + units <= gridDim.x;
+        if (!aligned) cost += (unsigned long long)units * kUnitCost;
+        share = scalar(max((cost + a.groups - 1) / a.groups, (unsigned long long)kLeastShare));
+        auto length = [&](const Share<kMT>& s) {
+            if (aligned) return s.sum(heads, [&](int r) { return s.parts(r, (int)share); });
+            return s.sum(heads, [&](int r) { return kUnitCost + s.tiles(r); });
+        };
+        lo = aligned ? g : g * share;
+        hi = aligned ? g + 1 : lo + share;
+        unsigned long long mine = 0;
+        for (int i = b0; i < b1; ++i) {
+            mine += length(i == b0 ? first : Share<kMT>(a, plain_block(a, i)));
+        }
         unsigned long long upto = mine;
-        unsigned units_upto = units;
         #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const unsigned long long u = __shfl_up(upto, o, 64);
-            const unsigned v = __shfl_up(units_upto, o, 64);
-            if (lane >= o) {
-                upto += u;
-                units_upto += v;
-            }
+            if (lane >= o) upto += u;
         }
-        if (lane == 63) {
-            sh.scan[wave] = upto;
-            sh.scan_units[wave] = units_upto;
-        }
+        if (lane == 63) sh.scan[wave] = upto;
         __syncthreads();
-        unsigned long long all = 0;
-        unsigned all_units = 0;
-        #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            if (w < wave) {
-                upto += sh.scan[w];
-                units_upto += sh.scan_units[w];
-            }
-            all += sh.scan[w];
-            all_units += sh.scan_units[w];
-        }
-        lead = scalar((int)min(all / (4 * gridDim.x), (unsigned long long)kUnitCost));
-        all += (unsigned long long)all_units * lead;
-        share = scalar(max((all + gridDim.x - 1) / gridDim.x, (unsigned long long)kLeastShare));
-        lo = g * share;
-        hi = lo + share;
-        upto += (unsigned long long)units_upto * lead;
-        mine += (unsigned long long)units * lead;
+        for (int w = 0; w < wave; ++w) upto += sh.scan[w];
         if (mine > 0 && upto - mine <= lo && lo < upto) {
             at = upto - mine;
             int i = b0;
             for (; i < b1 - 1; ++i) {
-                const Share<kMT> s(a, plain_block(a, i));
-                const unsigned long long n = s.tiles_of_all(heads) + (unsigned long long)(s.blocks * heads) * lead;
+                const unsigned long long n = length(Share<kMT>(a, plain_block(a, i)));
                 if (lo < at + n) break;
                 at += n;
             }
@@ -656,34 +712,67 @@ __global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(Atte
         }
         __syncthreads();
         b = scalar(sh.found);
-        if (b >= 0) {
+        if (b >= 0 && (aligned || g < a.groups)) {
             at = scalar(sh.before);
             blk = scalar(plain_block(a, b));
+            if (aligned) {
+                const Share<kMT> s(a, blk);
+                const int full = heads * scalar(s.parts(0, (int)share));    // of a full row block
+                part = (int)(lo - at);
+                rb = scalar(min(part / full, s.blocks - 1));
+                part -= rb * full;
+                const int each = scalar(s.parts(rb, (int)share));
+                h = scalar(part / each);
+                part -= h * each;
+            }
+        } else {
+            b = -1;
         }
     }
 
     while (b >= 0) {
         const Share<kMT> s(a, blk);
-        Work wk{b, h, rb, s.span.first, s.span.end, -1};
-        const int unit = lead + s.tiles(rb);
-        if (!a.direct) {
-            const int cost = s.cost(rb), n = s.span.size();
-            const unsigned long long start = at + (unsigned long long)h * unit + lead;
-            const int i0 = lo > start ? (int)min((lo - start + cost - 1) / cost, (unsigned long long)n) : 0;
-            const int i1 = hi > start ? (int)min((hi - start + cost - 1) / cost, (unsigned long long)n) : 0;
-            wk.t0 = s.span.first + i0;
-            wk.t1 = s.span.first + i1;
-            if (i0 < i1 && (i0 > 0 || i1 < n)) {
-                wk.slot = 2 * g + (i0 == 0);
-                const int from = (int)(start / share);
-                const int to = (int)((start + (unsigned long long)(n - 1) * cost) / share);
+        const int unit = kUnitCost + s.tiles(rb), n = s.span.size();
+        int i0 = 0, i1 = n, slot = -1;
+        if (aligned) {
+            const int parts = s.parts(rb, (int)share);
+            i0 = (int)((long long)n * part / parts);
+            i1 = (int)((long long)n * (part + 1) / parts);
+            if (parts > 1) {
+                slot = g;
                 if (tid == 0) {
-                    a.parts[wk.slot] = make_int4((b * heads + h) * a.row_blocks + rb, to - from + 1, g - from, from);
+                    a.parts[2 * g] = make_int4((b * heads + h) * a.row_blocks + rb, parts, part, g - part);
+                }
+            }
+        } else if (!a.direct) {
+            // Places relative to the unit's first tile; beyond it either way
+            // is as good as 2^30.
+            const unsigned cost = s.cost(rb);
+            const long long start = (long long)(at + (unsigned long long)h * unit + kUnitCost);
+            const int from = (int)min(max((long long)lo - start, -(1ll << 30)), 1ll << 30);
+            const int to = (int)min(max((long long)hi - start, -(1ll << 30)), 1ll << 30);
+            i0 = from > 0 ? min((int)((from + cost - 1) / cost), n) : 0;
+            i1 = to > 0 ? min((int)((to + cost - 1) / cost), n) : 0;
+            if (i0 < i1 && (i0 > 0 || i1 < n)) {
+                slot = 2 * g + (i0 == 0);
+                const unsigned width = (unsigned)min(share, 1ull << 31);
+                const int before = from > 0 ? (int)((from + width - 1) / width) : 0;
+                const int after = (int)((unsigned)((n - 1) * (int)cost - from) / width);
+                if (tid == 0) {
+                    a.parts[slot] = make_int4((b * heads + h) * a.row_blocks + rb, before + after + 1, before,
+                                              ~(2 * (g - before) + 1));
                 }
             }
         }
-        if (wk.t0 < wk.t1) attend_run<D, kMT>(a, wk, blk, sh, lane, wave);
-        if (a.direct) break;
+        if (i0 < i1) {
+            const Work wk{b, h, rb, s.span.first + scalar(i0), s.span.first + scalar(i1), slot};
+            const int act = scalar(s.act(rb));
+            if (kMT >= 4 && act == 4) attend_run<D, kMT, (kMT < 4 ? 1 : 4)>(a, wk, blk, sh, lane, wave);
+            else if (kMT >= 3 && act == 3) attend_run<D, kMT, (kMT < 3 ? 1 : 3)>(a, wk, blk, sh, lane, wave);
+            else if (kMT >= 2 && act == 2) attend_run<D, kMT, (kMT < 2 ? 1 : 2)>(a, wk, blk, sh, lane, wave);
+            else attend_run<D, kMT, 1>(a, wk, blk, sh, lane, wave);
+        }
+        if (a.direct || aligned) break;
         // On to the next unit: heads, row blocks, requests.
         if (++h == heads) {
             at += (unsigned long long)heads * unit;
@@ -704,7 +793,7 @@ __global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(Atte
                 }
             }
         }
-        if (b >= 0 && at + (unsigned long long)h * (lead + Share<kMT>(a, blk).tiles(rb)) >= hi) b = -1;
+        if (b >= 0 && at + (unsigned long long)h * (kUnitCost + Share<kMT>(a, blk).tiles(rb)) >= hi) b = -1;
     }
 }
 
@@ -721,15 +810,14 @@ struct Joined {
     }
 };
 
-// Joins the units that workgroups of the first kernel left in parts: the part
-// of workgroup `from` that starts the unit is in slot 2 from + 1, those of the
-// next ones in slots 2 (from + 1), 2 (from + 2), ... A workgroup here belongs
-// to one workgroup g there and four rows. A unit of fewer than four parts is
-// joined by the workgroups of its first part, a wavefront a row; of more, by
-// those of its first four parts, each taking one of the four rows with all its
-// wavefronts. Lanes hold 4 channels, 256 / D parts lie side by side in a
-// wavefront, kDeep of them each are in flight. The order of the sums is fixed
-// by the shapes and lengths of the call.
+// Joins the units that the first kernel left in parts. A workgroup here belongs
+// to one there and to 16 rows of a row block. The 16 rows of a unit of fewer
+// than 16 parts are dealt to the workgroups of its first four parts, a
+// wavefront a row; those of a unit of more to the workgroups of its first 16
+// parts, which take one row with all their wavefronts. Lanes
+// hold 4 channels, 256 / D parts lie side by side in a wavefront, kDeep of them
+// each are in flight. The order of the sums is fixed by the shapes and lengths
+// of the call.
 template <int D, int kMT>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     constexpr int kSide = 256 / D, kLanes = 64 / kSide;     // parts side by side, lanes of each
@@ -737,66 +825,67 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     __shared__ Joined sh[kWaves][64];
     const int lane = threadIdx.x & 63, wave = scalar((int)threadIdx.x >> 6);
     const int side = lane / kLanes, ch = lane % kLanes * 4;
-    const int g = blockIdx.x / (4 * kMT), in0 = blockIdx.x % (4 * kMT) * 4;
+    const int g = blockIdx.x / kMT, in0 = blockIdx.x % kMT * 16;
     const int4 both[2] = {a.parts[2 * g], a.parts[2 * g + 1]};
     #pragma unroll
     for (int slot = 0; slot < 2; ++slot) {
-        const int n = both[slot].y, s0 = both[slot].z, from = both[slot].w;
-        const bool many = n >= 4;
-        if (n == 0 || s0 >= (many ? 4 : 1)) continue;
+        const int n = both[slot].y, s0 = both[slot].z, first = both[slot].w;
+        const bool many = n >= 16;
+        if (n == 0 || s0 >= (many ? 16 : 4)) continue;
         const int rb = both[slot].x % a.row_blocks, h = both[slot].x / a.row_blocks % a.pages.heads;
         const int b = both[slot].x / a.row_blocks / a.pages.heads;
-        const int in = in0 + (many ? s0 : wave);
-        const int row = rb * (16 * kMT) + in;
-        const Block blk = plain_block(a, b);
-        const bool live = row < blk.len * a.group;
+        const int rows = plain_block(a, b).len * a.group - rb * (16 * kMT);
         const int by = many ? kWaves * kSide : kSide;
-
-        Joined j{kNegInf, 0.0f, {0, 0, 0, 0}};
-        for (int s = (many ? wave * kSide : 0) + side; live && s < n; s += kDeep * by) {
-            f32x4 v[kDeep];
-            float2 ml[kDeep];
-            #pragma unroll
-            for (int k = 0; k < kDeep; ++k) {
-                const int i = min(s + k * by, n - 1);
-                const long long p = (long long)(2 * (from + i) + (i == 0)) * (16 * kMT) + in;
-                ml[k] = a.part_ml[p];
-                v[k] = *reinterpret_cast<const f32x4*>(a.part_o + p * D + ch);
+        for (int i = many ? s0 : s0 * kWaves + wave; i < 16 && in0 + i < rows; i += many ? 16 : min(n, 4) * kWaves) {
+            const int in = in0 + i;
+            Joined j{kNegInf, 0.0f, {0, 0, 0, 0}};
+            for (int s = (many ? wave * kSide : 0) + side; s < n; s += kDeep * by) {
+                f32x4 v[kDeep];
+                float2 ml[kDeep];
+                #pragma unroll
+                for (int k = 0; k < kDeep; ++k) {
+                    const long long p = (long long)slot_of(first, min(s + k * by, n - 1)) * (16 * kMT) + in;
+                    ml[k] = a.part_ml[p];
+                    v[k] = *reinterpret_cast<const f32x4*>(a.part_o + p * D + ch);
+                }
+                #pragma unroll
+                for (int k = 0; k < kDeep; ++k) {
+                    if (s + k * by < n) j.add(ml[k].x, ml[k].y, v[k]);
+                }
             }
             #pragma unroll
-            for (int k = 0; k < kDeep; ++k) {
-                if (s + k * by < n) j.add(ml[k].x, ml[k].y, v[k]);
+            for (int o = kLanes; o < 64; o <<= 1) {
+                f32x4 other;
+                #pragma unroll
+                for (int c = 0; c < 4; ++c) other[c] = __shfl_xor(j.acc[c], o);
+                j.add(__shfl_xor(j.ref, o), __shfl_xor(j.sum, o), other);
             }
-        }
-        #pragma unroll
-        for (int o = kLanes; o < 64; o <<= 1) {
-            f32x4 other;
-            #pragma unroll
-            for (int c = 0; c < 4; ++c) other[c] = __shfl_xor(j.acc[c], o);
-            j.add(__shfl_xor(j.ref, o), __shfl_xor(j.sum, o), other);
-        }
-        if (many) {
-            __syncthreads();
-            sh[wave][lane] = j;
-            __syncthreads();
-            j = sh[0][lane];
-            #pragma unroll
-            for (int w = 1; w < kWaves; ++w) j.add(sh[w][lane].ref, sh[w][lane].sum, sh[w][lane].acc);
-        }
-        if (live && side == 0 && (!many || wave == 0)) {
-            const int t = row / a.group, head = h * a.group + (row - t * a.group);
-            const float inv = 1.0f / j.sum;
-            const unsigned w[2] = {pack_bf16(j.acc[0] * inv, j.acc[1] * inv),
-                                   pack_bf16(j.acc[2] * inv, j.acc[3] * inv)};
-            uint16_t* dst = a.out + (((long long)b * (a.K + 1) + t) * a.Hq + head) * D + ch;
-            __builtin_memcpy(__builtin_assume_aligned(dst, 8), w, 8);
+            if (many) {
+                __syncthreads();
+                sh[wave][lane] = j;
+                __syncthreads();
+                j = sh[0][lane];
+                #pragma unroll
+                for (int w = 1; w < kWaves; ++w) j.add(sh[w][lane].ref, sh[w][lane].sum, sh[w][lane].acc);
+            }
+            if (side == 0 && (!many || wave == 0)) {
+                const int row = rb * (16 * kMT) + in;
+                const int t = row / a.group, head = h * a.group + (row - t * a.group);
+                const float inv = 1.0f / j.sum;
+                const unsigned w[2] = {pack_bf16(j.acc[0] * inv, j.acc[1] * inv),
+                                       pack_bf16(j.acc[2] * inv, j.acc[3] * inv)};
+                uint16_t* dst = a.out + (((long long)b * (a.K + 1) + t) * a.Hq + head) * D + ch;
+                __builtin_memcpy(__builtin_assume_aligned(dst, 8), w, 8);
+            }
         }
     }
 }
 
 // What the host fixes of a call: rows per wavefront, row blocks, workgroups.
 struct Plan {
-    int mt, row_blocks, groups;
+    int mt, row_blocks;
+    int groups;         // workgroups resident at once (and no more than there is work for)
+    int grid, slots;
     bool direct;
 };
 
@@ -809,24 +898,26 @@ int resident(int mt) {      // workgroups of a kernel that the 256 CUs hold at o
 Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_pages, int window) {
     Plan p;
     const int rows = (K + 1) * (Hq / kv_heads);
-    const int most = D == 256 ? 2 : 4;       // accumulators: kMT D / 4 registers a lane
-    p.mt = (rows + 15) / 16 < most ? (rows + 15) / 16 : most;
+    const int widest = D == 256 ? 2 : 4;     // accumulators: kMT D / 4 registers a lane
+    p.mt = std::min((rows + 15) / 16, widest);
     p.row_blocks = (rows + 16 * p.mt - 1) / (16 * p.mt);
     const long long units = (long long)B * kv_heads * p.row_blocks;
     long long tokens = (long long)max_pages * page_size;
     if (window > 0 && tokens > (long long)window + K + kTile) tokens = (long long)window + K + kTile;
     const long long tiles = (tokens + kTile - 1) / kTile + 1;
     p.direct = tiles <= kDirectTiles;
-    // No more workgroups than the longest line has shares for.
-    const long long most_shares = (units * (kUnitCost + tiles * (kTileCost + p.mt)) + kLeastShare - 1) / kLeastShare;
+    const long long most = (units * tiles * (kTileCost + p.mt) + kLeastShare - 1) / kLeastShare;
     const int held = D == 64 ? resident<64>(p.mt) : D == 128 ? resident<128>(p.mt) : resident<256>(p.mt);
-    p.groups = (int)(p.direct ? units : std::min<long long>(held, most_shares));
+    p.groups = (int)std::min<long long>(held, most);
+    // Room for aligned parts of as many units as twice what is held at once.
+    p.grid = (int)(p.direct ? units : p.groups + std::min<long long>(units, 2 * held));
+    p.slots = p.direct ? 0 : std::max(2 * p.groups, p.grid);
     return p;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-size_t parts_of(const Plan& p) { return (size_t)p.groups * 2 * 16 * p.mt; }
+size_t parts_of(const Plan& p) { return (size_t)p.slots * 16 * p.mt; }
 
 bool shape_ok(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_pages, int window) {
     return B >= 0 && B <= SV_MAX_BATCH && K >= 0 && K <= SV_MAX_K && window >= 0 &&
@@ -836,9 +927,9 @@ bool shape_ok(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_
 
 template <int D, int kMT>
 void launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
-    hipLaunchKernelGGL((attend_kernel<D, kMT>), dim3((unsigned)p.groups), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((attend_kernel<D, kMT>), dim3((unsigned)p.grid), dim3(256), 0, s, a);
     if (!p.direct) {
-        const unsigned blocks = (unsigned)(p.groups * 4 * kMT);
+        const unsigned blocks = (unsigned)(p.grid * kMT);
         hipLaunchKernelGGL((attend_join_kernel<D, kMT>), dim3(blocks), dim3(256), 0, s, a);
     }
 }
@@ -853,7 +944,7 @@ extern "C" size_t spec_verify_attention_workspace_bytes(int B, int K, int q_head
     }
     const Plan p = plan_of(B, K, q_heads, kv_heads, head_dim, page_size, max_pages, window);
     if (p.direct) return 256;
-    return round256((size_t)p.groups * 2 * sizeof(int4)) + round256(parts_of(p) * sizeof(float2)) +
+    return round256((size_t)p.grid * 2 * sizeof(int4)) + round256(parts_of(p) * sizeof(float2)) +
            parts_of(p) * head_dim * sizeof(float);
 }
 
@@ -893,14 +984,15 @@ extern "C" int spec_verify_attention(const void* queries, int64_t query_stride, 
     a.status = out_status;
     char* ws = static_cast<char*>(workspace);
     a.parts = reinterpret_cast<int4*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(ws + round256((size_t)p.groups * 2 * sizeof(int4)));
-    a.part_o = reinterpret_cast<float*>(ws + round256((size_t)p.groups * 2 * sizeof(int4)) +
+    a.part_ml = reinterpret_cast<float2*>(ws + round256((size_t)p.grid * 2 * sizeof(int4)));
+    a.part_o = reinterpret_cast<float*>(ws + round256((size_t)p.grid * 2 * sizeof(int4)) +
                                         round256(parts_of(p) * sizeof(float2)));
     a.pages = make_pages(page_table, kv_heads, page_size, max_pages, num_pages);
     a.B = B;
     a.K = K;
     a.Hq = q_heads;
     a.group = q_heads / kv_heads;
+    a.groups = p.groups;
     a.row_blocks = p.row_blocks;
     a.window = window;
     a.direct = p.direct;
