@@ -37,25 +37,28 @@ constexpr int kWaves = 4;
 constexpr float kNegInf = -INFINITY;
 
 // How the work is cut. A unit is a request's kv head and block of 16 kMT
-// rows, its cost the tiles times (kTileCost plus their row tiles). The lengths
-// are on the device, so every workgroup adds up the requests for itself and
-// finds its place by a prefix sum. With `groups` workgroups resident at once
-// and C the cost of all units, one of two cuts is made:
-//  - aligned, C < kAlignedCost groups (short work): every unit is cut into
-//    round(cost / share) equal parts, at least one, for share = C / groups,
-//    and a workgroup takes one part. Starting and ending a run costs about as
-//    much as kAlignedCost / 4, so none takes two.
+// rows, its cost the tiles times (kTileCost plus their row tiles; measured
+// times per tile grow like that, one unit about 0.05 us). Three cuts:
+//  - direct: a workgroup per unit and nothing to join, where page table rows
+//    have at most kDirectTiles tiles (searching and joining would cost more),
+//    or where there are kDirectUnits units for every workgroup that is
+//    resident at once (they even out by themselves).
+// Else the lengths, which are on the device, decide. Every workgroup adds up
+// the requests for itself and finds its place by a prefix sum. With `groups`
+// workgroups resident at once and share = (cost of all units) / groups:
+//  - aligned: every unit is cut into round(cost / share) equal parts, at least
+//    one, and a workgroup takes one part; if the longest part is no more than
+//    kSlack over the share, about what the line's extra runs cost.
 //  - line: all units lie on one line, each led by a stretch of kUnitCost for
 //    starting and ending it, and each of `groups` workgroups takes an equal
 //    stretch, so that ragged lengths and budgets load the chip evenly.
-// Parts of a unit are put together by the join kernel. With page table rows of
-// at most kDirectTiles tiles a workgroup per unit is launched instead and
-// nothing is joined: the second launch and the search would cost more.
+// Parts of a unit are put together by the join kernel.
 constexpr int kTileCost = 5;
-constexpr int kUnitCost = 160;
-constexpr int kAlignedCost = 1536;
+constexpr int kUnitCost = 120;
+constexpr int kSlack = 400;
 constexpr int kLeastShare = 48;     // a few tiles for each of a workgroup's wavefronts
 constexpr int kDirectTiles = 32;
+constexpr int kDirectUnits = 4;
 
 struct AttendArgs {
     const uint16_t* q;
@@ -171,7 +174,7 @@ struct Lds {
     float ref[kWaves][kMT][16];
     float sum[kWaves][kMT][16];
     unsigned long long cost[kWaves], scan[kWaves], before;
-    unsigned units[kWaves];
+    unsigned units[kWaves], longest[kWaves];
     int found;
 };
 
@@ -473,7 +476,7 @@ struct Share {
     __device__ __forceinline__ int parts(int rb, int share) const {
         return min(max((tiles(rb) + share / 2) / share, 1), max(span.size(), 1));
     }
-    // All tiles of a unit of row block rb.
+    // Cost of all tiles of a unit of row block rb.
     __device__ __forceinline__ int tiles(int rb) const { return span.size() * cost(rb); }
     // Sum over all the request's units of f(row block).
     template <typename F>
@@ -676,10 +679,25 @@ __global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(Atte
         __syncthreads();
         cost = scalar((sh.cost[0] + sh.cost[1]) + (sh.cost[2] + sh.cost[3]));
         units = scalar((int)((sh.units[0] + sh.units[1]) + (sh.units[2] + sh.units[3])));
-        // Aligned parts: no more than groups + units workgroups.
-        aligned = cost < (unsigned long long)kAlignedCost * a.groups && a.groups + units <= gridDim.x;
-        if (!aligned) cost += (unsigned long long)units * kUnitCost;
         share = scalar(max((cost + a.groups - 1) / a.groups, (unsigned long long)kLeastShare));
+        // Aligned parts: no more than groups + units workgroups, which the
+        // grid has room for or not.
+        unsigned longest = 0;
+        const int width = (int)min(share, 1ull << 30);
+        for (int i = b0; i < b1; ++i) {
+            const Share<kMT> s = i == b0 ? first : Share<kMT>(a, plain_block(a, i));
+            if (s.blocks > 0) longest = max(longest, (unsigned)(s.tiles(0) / s.parts(0, width)));
+        }
+        #pragma unroll
+        for (int o = 1; o < 64; o <<= 1) longest = max(longest, (unsigned)__shfl_xor((int)longest, o, 64));
+        if (lane == 0) sh.longest[wave] = longest;
+        __syncthreads();
+        longest = max(max(sh.longest[0], sh.longest[1]), max(sh.longest[2], sh.longest[3]));
+        aligned = scalar((int)(a.groups + units <= gridDim.x && longest <= share + kSlack)) != 0;
+        if (!aligned) {
+            cost += (unsigned long long)units * kUnitCost;
+            share = scalar(max((cost + a.groups - 1) / a.groups, (unsigned long long)kLeastShare));
+        }
         auto length = [&](const Share<kMT>& s) {
             if (aligned) return s.sum(heads, [&](int r) { return s.parts(r, (int)share); });
             return s.sum(heads, [&](int r) { return kUnitCost + s.tiles(r); });
@@ -905,12 +923,11 @@ Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_p
     long long tokens = (long long)max_pages * page_size;
     if (window > 0 && tokens > (long long)window + K + kTile) tokens = (long long)window + K + kTile;
     const long long tiles = (tokens + kTile - 1) / kTile + 1;
-    p.direct = tiles <= kDirectTiles;
     const long long most = (units * tiles * (kTileCost + p.mt) + kLeastShare - 1) / kLeastShare;
     const int held = D == 64 ? resident<64>(p.mt) : D == 128 ? resident<128>(p.mt) : resident<256>(p.mt);
     p.groups = (int)std::min<long long>(held, most);
-    // Room for aligned parts of as many units as twice what is held at once.
-    p.grid = (int)(p.direct ? units : p.groups + std::min<long long>(units, 2 * held));
+    p.direct = tiles <= kDirectTiles || units >= (long long)kDirectUnits * held;
+    p.grid = (int)(p.direct ? units : p.groups + std::min<long long>(units, held));
     p.slots = p.direct ? 0 : std::max(2 * p.groups, p.grid);
     return p;
 }
