@@ -133,6 +133,36 @@ __device__ __forceinline__ float quad_sum(float v) {
 }
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
+// A tile's bytes as one lane holds them.
+template <int D>
+struct Frag {
+    using L = Tile<D>;
+    unsigned k[L::kPlanes][2][L::U / 4];        // plane, half: a token's unit of channels
+    unsigned v[L::kPlanes][2][L::C];            // plane, half: 4 tokens' pieces
+    unsigned ks[L::kPlanes];                    // key scales of both halves
+    unsigned vs[L::kPlanes][2];                 // value scales of 4 + 4 tokens
+
+    // The tile is the same for the whole wavefront: one scalar base, a 32-bit
+    // offset per lane.
+    __device__ __forceinline__ void load(const uint8_t* tile, unsigned lane) {
+        const unsigned x = lane & 15, quad = lane >> 4;
+        #pragma unroll
+        for (int p = 0; p < L::kPlanes; ++p) {
+            #pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                __builtin_memcpy(k[p][half], __builtin_assume_aligned(
+                    tile + (half * 8 * D + p * 64 * L::U) + lane * L::U, L::U), L::U);
+                __builtin_memcpy(v[p][half], __builtin_assume_aligned(
+                    tile + (L::kVCodes + (p * 2 + half) * 256 * L::C) + lane * (4 * L::C), 4 * L::C), 4 * L::C);
+            }
+            const unsigned kg = D == 64 ? quad >> 1 : quad, vg = D == 64 ? x >> 3 : x >> 2;
+            ks[p] = *reinterpret_cast<const uint16_t*>(tile + (L::kKScales + p * 128) + (kg * 32 + x * 2));
+            __builtin_memcpy(vs[p], __builtin_assume_aligned(
+                tile + (L::kVScales + p * 128) + (vg * 4 + quad) * 8, 8), 8);
+        }
+    }
+};
+
 // Registers of one wavefront over its tiles, for kAct row tiles.
 template <int D, int kAct>
 struct State {
@@ -147,28 +177,11 @@ struct State {
     int pos[kAct];       // the row's position; -1 past the block
 };
 
-// Tiles of a wavefront's ring in LDS: one worked on, the others on their way.
-// Two where a third would cost a resident workgroup.
-template <int D, int kMT>
-constexpr int depth() {
-    return D * kMT == 128 || D * kMT == 256 ? 2 : 3;
-}
-
-// Bytes of a place: a tile, and what a load of the scales writes behind it.
-template <int D>
-constexpr int ring_bytes() {
-    return 32 * D + (2 * D + 255) / 256 * 256;
-}
-
 template <int D, int kMT>
 struct Lds {
     static constexpr int kPieces = kMT * Tile<D>::kPlanes * (D == 64 ? 4 : 8) / 4;  // float4 per lane and component
-    struct Loop {
-        u32x4 q[kMT][D / 32][64];           // right operands of K Q^T
-        unsigned char ring[kWaves][depth<D, kMT>()][ring_bytes<D>()];
-    };
     union {
-        Loop loop;
+        u32x4 q[kMT][D / 32][64];           // right operands of K Q^T
         f32x4 o[kWaves][2][kPieces][64];    // two components of the accumulators at a time
     };
     float ref[kWaves][kMT][16];
@@ -180,42 +193,37 @@ struct Lds {
 
 // One tile. kMasked: some row does not see some token of it.
 template <int D, int kMT, int kAct, bool kMasked>
-__device__ __forceinline__ void tile_step(State<D, kAct>& st, const Lds<D, kMT>& sh,
-                                          const AttendArgs& a, int lane, int tok0, int last,
-                                          const unsigned char* tile) {
+__device__ __forceinline__ void tile_step(State<D, kAct>& st, const Frag<D>& f,
+                                          const Lds<D, kMT>& sh, const AttendArgs& a, int lane,
+                                          int tok0, int last, const uint8_t* tile) {
     using L = Tile<D>;
     using S = State<D, kAct>;
+    // These accumulators leave no registers for steps that overlap (D = 256, of
+    // as many, has one wave per SIMD and so twice the registers).
+    constexpr bool kTight = D == 128 && kAct == 4;
     // Opaque: the masks' token numbers are computed here, not kept in
     // registers throughout the loop over tiles.
     if (kMasked) asm volatile("" : "+v"(lane));
-    const int x = lane & 15, quad = lane >> 4;
+    const int quad = lane >> 4;
     // Scores of 2 x 16 tokens (lane: tokens 16 half + 4 quad + r).
     f32x4 z[kAct][2] = {};
     #pragma unroll
     for (int p = 0; p < S::kPlanes; ++p) {
-        unsigned k[2][L::U / 4];
-        #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            __builtin_memcpy(k[half], __builtin_assume_aligned(
-                tile + (half * 8 * D + p * 64 * L::U) + lane * L::U, L::U), L::U);
-        }
-        const int kg = D == 64 ? quad >> 1 : p * 4 + quad;
-        const unsigned ks = *reinterpret_cast<const uint16_t*>(tile + L::kKScales + kg * 32 + x * 2);
-        const float s[2] = {scale_of(ks & 255u), scale_of(ks >> 8)};
+        const float s[2] = {scale_of(f.ks[p] & 255u), scale_of(f.ks[p] >> 8)};
         #pragma unroll
         for (int j = 0; j < S::kUnitSteps; ++j) {
-            __builtin_amdgcn_sched_barrier(0);
+            if (kTight) __builtin_amdgcn_sched_barrier(0);
             bf16x8 kf[2];
             #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const unsigned w = k[half][j];
+                const unsigned w = f.k[p][half][j];
                 const u32x4 kw = {decode2<0>(w, s[half]), decode2<1>(w, s[half]),
                                   decode2<2>(w, s[half]), decode2<3>(w, s[half])};
                 kf[half] = __builtin_bit_cast(bf16x8, kw);
             }
             #pragma unroll
             for (int mt = 0; mt < kAct; ++mt) {
-                const bf16x8 qf = __builtin_bit_cast(bf16x8, sh.loop.q[mt][p * S::kUnitSteps + j][lane]);
+                const bf16x8 qf = __builtin_bit_cast(bf16x8, sh.q[mt][p * S::kUnitSteps + j][lane]);
                 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     z[mt][half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[half], qf, z[mt][half], 0, 0, 0);
@@ -226,7 +234,7 @@ __device__ __forceinline__ void tile_step(State<D, kAct>& st, const Lds<D, kMT>&
 
     // Probabilities 2^(c z - ref). The reference follows the running maximum
     // only when a term exceeds 2^8: until then nothing has to be rescaled.
-    __builtin_amdgcn_sched_barrier(0);
+    if (kTight) __builtin_amdgcn_sched_barrier(0);
     bf16x8 pf[kAct];
     #pragma unroll
     for (int mt = 0; mt < kAct; ++mt) {
@@ -274,26 +282,18 @@ __device__ __forceinline__ void tile_step(State<D, kAct>& st, const Lds<D, kMT>&
     // Values: 8 tokens (4 quad + r of both halves) x kChans channels a plane.
     #pragma unroll
     for (int p = 0; p < S::kPlanes; ++p) {
-        unsigned v[2][L::C], sc2[2], w[8];
-        #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            __builtin_memcpy(v[half], __builtin_assume_aligned(
-                tile + (L::kVCodes + (p * 2 + half) * 256 * L::C) + lane * (4 * L::C), 4 * L::C), 4 * L::C);
-        }
-        const int vg = D == 64 ? x >> 3 : p * 4 + (x >> 2);
-        __builtin_memcpy(sc2, __builtin_assume_aligned(
-            tile + L::kVScales + (vg * 4 + quad) * 8, 8), 8);
+        unsigned w[8];
         float vs[8];
         bool poison = false;
         #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int half = i >> 2, r = i & 3;
             if constexpr (D == 64) {
-                w[i] = r & 1 ? v[half][r >> 1] >> 16 : v[half][r >> 1];
+                w[i] = r & 1 ? f.v[p][half][r >> 1] >> 16 : f.v[p][half][r >> 1];
             } else {
-                w[i] = v[half][r];
+                w[i] = f.v[p][half][r];
             }
-            const unsigned sc = sc2[half];
+            const unsigned sc = f.vs[p][half];
             unsigned bits = (r == 3 ? sc >> 1 : sc << (23 - 8 * r)) & 0x7f800000u;
             if (kMasked) {
                 // What some row does not see must not reach it as 0 * NaN:
@@ -312,7 +312,7 @@ __device__ __forceinline__ void tile_step(State<D, kAct>& st, const Lds<D, kMT>&
         }
         #pragma unroll
         for (int cb = 0; cb < S::kChans / 2; ++cb) {
-            __builtin_amdgcn_sched_barrier(0);
+            if (kTight) __builtin_amdgcn_sched_barrier(0);
             unsigned e[8];
             #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -357,57 +357,46 @@ __device__ __forceinline__ void tile_step(State<D, kAct>& st, const Lds<D, kMT>&
 
 // This wavefront's share of a run: of the run's tiles, those that some row
 // does not see whole first (the block's own, the windows' edges), then the
-// others, every kWaves-th by number n = 0, 1, ... Their bytes come into the
-// wavefront's ring in LDS by buffer-to-LDS loads, kDepth - 1 tiles ahead, which
-// takes no registers and no barrier.
+// others, every kWaves-th by number n = 0, 1, ... The next tile's bytes are in
+// flight while one is worked on. (Two tiles ahead, or a ring in LDS filled by
+// buffer-to-LDS loads, measured slower: 174-186 against 153 us for 128
+// requests over 1,024..8,192 tokens.)
 template <int D, int kMT>
 struct Stream {
     using L = Tile<D>;
-    static constexpr int kDepth = depth<D, kMT>();
-    static constexpr int kWide = 32 * D / 1024;             // loads of 64 x 16 bytes: the codes
-    static constexpr int kNarrow = (2 * D + 255) / 256;     // loads of 64 x 4 bytes: the scales
-    static constexpr int kLoads = kWide + kNarrow;
-    static_assert(32 * D % 1024 == 0, "whole loads");
-    unsigned char* ring;
+    Frag<D> f[2];
     int wave, first, low, u0, u1, edges, count;     // tiles [u0, u1) are seen whole by every row
-    int n, place;           // the next tile and its place in the ring
-    bool bad;               // a page was outside the pool
     // Page numbers of the next 64 tiles, one a lane. They come in one load: a
     // lookup per tile would wait for every load before it, the tiles in flight
     // among them.
     int pages;
+    bool bad;               // a page was outside the pool
 
-    __device__ __forceinline__ int tile_of(int number) const {
-        const int i = wave + number * kWaves;
+    __device__ __forceinline__ int tile_of(int n) const {
+        const int i = wave + n * kWaves;
         return i < low ? first + i : i < edges ? u1 + (i - low) : u0 + (i - edges);
     }
-    __device__ __forceinline__ void fetch(const AttendArgs& a, const Work& wk, int number, int to,
-                                          int lane) {
-        // No branch in the loop over tiles depends on the lane: where one does,
-        // the compiler may keep a second set of accumulators.
-        if ((number & 63) == 0) {
-            pages = a.pages.page(wk.b, tile_of(min(number + lane, count - 1)) * kTile);
+    // No branch in the loops over tiles depends on the lane: where one does,
+    // the compiler may keep a second set of accumulators.
+    template <int i>
+    __device__ __forceinline__ const uint8_t* fetch(const AttendArgs& a, const Work& wk, int n, int lane) {
+        if ((n & 63) == 0) {
+            pages = a.pages.page(wk.b, tile_of(min(n + lane, count - 1)) * kTile);
         }
-        long long at = a.pages.tile_in(__builtin_amdgcn_readlane(pages, number & 63), wk.h,
-                                       tile_of(number) * kTile, L::kBytes);
+        long long at = a.pages.tile_in(__builtin_amdgcn_readlane(pages, n & 63), wk.h,
+                                       tile_of(n) * kTile, L::kBytes);
         // The first tile of the cache stands in for one whose page is bad (the
         // request is flagged and its outputs are undefined).
         if (at < 0) {
             bad = true;
             at = 0;
         }
-        const __amdgpu_buffer_rsrc_t src = svdma::rsrc(a.cache + at, L::kBytes);
-        unsigned char* dst = ring + to * ring_bytes<D>();
-        #pragma unroll
-        for (int i = 0; i < kWide; ++i) svdma::load16(src, i * 1024 + lane * 16, dst + i * 1024);
-        #pragma unroll
-        for (int i = 0; i < kNarrow; ++i) {
-            svdma::load4(src, 32 * D + i * 256 + lane * 4, dst + 32 * D + i * 256);
-        }
+        const uint8_t* tile = a.cache + at;
+        f[i].load(tile, lane);
+        return tile;
     }
-    __device__ __forceinline__ void start(const AttendArgs& a, const Work& wk, const Block& blk,
-                                          unsigned char* lds, int lane, int its_wave) {
-        ring = lds;
+    __device__ __forceinline__ const uint8_t* start(const AttendArgs& a, const Work& wk,
+                                                    const Block& blk, int lane, int its_wave) {
         wave = its_wave;
         // Tokens that every row of the block sees: [all_lo, ctx + 1).
         const int all_lo = a.window > 0 ? max(0, blk.ctx + blk.len - a.window) : 0;
@@ -417,44 +406,29 @@ struct Stream {
         low = u0 - wk.t0;
         edges = low + wk.t1 - u1;
         count = (wk.t1 - wk.t0 - wave + kWaves - 1) / kWaves;
-        n = place = 0;
         bad = false;
-        #pragma unroll
-        for (int i = 0; i < kDepth - 1; ++i) {
-            if (i < count) fetch(a, wk, i, i, lane);
-        }
-    }
-    // Makes tile n's bytes ready. The place of tile n - 1 is read out (its
-    // values were used): the tile kDepth - 1 ahead goes there. Loads complete
-    // in order, so tile n is here when at most those of the tiles after it are
-    // outstanding.
-    __device__ __forceinline__ const unsigned char* next(const AttendArgs& a, const Work& wk,
-                                                         int lane) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (n + kDepth - 1 < count) {
-            fetch(a, wk, n + kDepth - 1, place == 0 ? kDepth - 1 : place - 1, lane);
-            svdma::wait_vm<(kDepth - 1) * kLoads>();
-        } else {
-            svdma::wait_vm<0>();
-        }
-        asm volatile("" ::: "memory");
-        return ring + place * ring_bytes<D>();
-    }
-    __device__ __forceinline__ void step() {
-        ++n;
-        place = place == kDepth - 1 ? 0 : place + 1;
+        return count > 0 ? fetch<0>(a, wk, 0, lane) : a.cache;
     }
     template <int kAct>
     __device__ __forceinline__ void run(State<D, kAct>& st, const Lds<D, kMT>& sh,
                                         const AttendArgs& a, const Work& wk, const Block& blk,
-                                        int lane) {
-        for (; wave + n * kWaves < edges; step()) {
-            const unsigned char* tile = next(a, wk, lane);
-            tile_step<D, kMT, kAct, true>(st, sh, a, lane, tile_of(n) * kTile, blk.ctx + blk.len - 1, tile);
+                                        const uint8_t* tile, int lane) {
+        int n = 0;
+        for (; wave + n * kWaves < edges; ++n) {
+            const uint8_t* next = tile;
+            if (n + 1 < count) next = fetch<1>(a, wk, n + 1, lane);
+            tile_step<D, kMT, kAct, true>(st, f[0], sh, a, lane, tile_of(n) * kTile, blk.ctx + blk.len - 1, tile);
+            f[0] = f[1];
+            tile = next;
         }
-        for (; n < count; step()) {
-            const unsigned char* tile = next(a, wk, lane);
-            tile_step<D, kMT, kAct, false>(st, sh, a, lane, 0, 0, tile);
+        while (n < count) {
+            if (n + 1 < count) fetch<1>(a, wk, n + 1, lane);
+            tile_step<D, kMT, kAct, false>(st, f[0], sh, a, lane, 0, 0, nullptr);
+            if (n + 1 < count) {
+                if (n + 2 < count) fetch<0>(a, wk, n + 2, lane);
+                tile_step<D, kMT, kAct, false>(st, f[1], sh, a, lane, 0, 0, nullptr);
+            }
+            n += 2;
         }
     }
 };
@@ -489,7 +463,7 @@ struct Share {
 // Waves per SIMD that the registers leave room for.
 template <int D, int kMT>
 constexpr int occupancy() {
-    return D * kMT == 512 && D == 256 ? 1 : D == 256 ? 2 : kMT == 1 ? 4 : kMT == 2 ? 3 : 2;
+    return D == 256 ? 3 - kMT : D * kMT <= 64 ? 4 : D * kMT <= 128 ? 3 : 2;
 }
 
 // One run of tiles, from the queries to the output or a partial result, for a
@@ -525,7 +499,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any,
         }
     }
     Stream<D, kMT> stream;
-    stream.start(a, wk, blk, sh.loop.ring[wave][0], lane, wave);
+    const uint8_t* tile = stream.start(a, wk, blk, lane, wave);
     S st;
     #pragma unroll
     for (int mt = 0; mt < kAct; ++mt) {
@@ -542,10 +516,10 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any,
     #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
         const int i = k * kWaves + wave;
-        if (i < kAct * S::kSteps) sh.loop.q[i / S::kSteps][i % S::kSteps][lane] = own[k];
+        if (i < kAct * S::kSteps) sh.q[i / S::kSteps][i % S::kSteps][lane] = own[k];
     }
     svdma::ring_barrier();            // leaves the tiles in flight
-    stream.run(st, sh, a, wk, blk, lane);
+    stream.run(st, sh, a, wk, blk, tile, lane);
     if (stream.bad && lane == 0) flag(a.status, SV_FLAG_BAD_PAGE);
 
     // Join the waves, two components of every accumulator in each of two

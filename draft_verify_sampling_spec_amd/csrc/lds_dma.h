@@ -36,12 +36,6 @@ __device__ __forceinline__ void load16(__amdgpu_buffer_rsrc_t r, unsigned off, u
                                              (int)off, 0, 0, kAux);
 }
 
-// The same with 4 bytes per lane: lane l's land at lds + 4 l.
-__device__ __forceinline__ void load4(__amdgpu_buffer_rsrc_t r, unsigned off, unsigned char* lds) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4,
-                                             (int)off, 0, 0, 0);
-}
-
 // Wait until at most N of this wave's vector memory operations are
 // outstanding, leaving the other counters.
 template <int N>
