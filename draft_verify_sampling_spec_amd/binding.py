@@ -11,7 +11,6 @@ the HIP runtime torch already loaded (one runtime per process).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -661,45 +660,46 @@ def spec_head_logits(h_codes, h_scales, w_codes, w_scales, R, H, V, dtype, out, 
                                    stream)
 
 
-@contextlib.contextmanager
-def _enqueue(device, stream):
-    """Makes ``device`` current and yields the stream's handle. Tensors that
-    torch allocates inside belong to ``stream``, so that one freed when the
-    call returns is not handed out again before the stream is done with it."""
-    if stream is None:
-        if device.index is None or device.index == torch.cuda.current_device():
-            yield _stream_handle(device)
-        else:
-            with torch.cuda.device(device):
-                yield _stream_handle(device)
-    else:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+# A serving step makes these calls for every layer, so what they cost on the
+# host counts: arguments are checked without building messages, the stream and
+# device are read through torch's own accessors, and the C function is called
+# directly. A call for another stream, or from another current device, enters
+# torch's context for it and calls itself: tensors that torch allocates inside
+# belong to that stream, so that one freed when the call returns is not handed
+# out again before the stream is done with it.
+
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _need(t, name, dtype, shape, device):
-    """A contiguous tensor of exactly this type, shape and device."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device \
-            or not t.is_contiguous():
+def _need(t, name, dtype, shape, index):
+    """The address of a contiguous tensor of exactly this type, shape and GPU."""
+    if isinstance(t, torch.Tensor):
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+                         f"cuda:{index}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    raise TypeError(f"{name} must be a torch.Tensor")
 
 
-def _token_stride(t, name, device):
+def _other_stream(stream, index):
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    return torch.cuda.stream(stream)
+
+
+def _token_stride(t, name, index):
     """Elements between tokens of a [B, T, heads, head_dim] tensor whose heads
     are contiguous and whose requests follow each other."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
     B, T, heads, dim = t.shape
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if t.is_contiguous():
+        return heads * dim
     sb, st, sh, sd = t.stride()
     stride = st if T > 1 else sb if B > 1 else heads * dim
-    if ((dim > 1 and sd != 1) or (heads > 1 and sh != dim)
-            or (B > 1 and T > 1 and sb != T * stride) or stride < heads * dim):
+    if (sd != 1 or (heads > 1 and sh != dim) or (B > 1 and T > 1 and sb != T * stride)
+            or stride < heads * dim):
         raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens, got "
                          f"strides {t.stride()}")
     return stride
@@ -723,7 +723,7 @@ class BlockCache:
             raise ValueError("BlockCache needs a GPU device")
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
-        self.device = device
+        self.device, self._index = device, device.index
         self.num_pages, self.kv_heads = int(num_pages), int(kv_heads)
         self.head_dim, self.page_size = int(head_dim), int(page_size)
         if spec_verify_cache_bytes(num_pages, kv_heads, head_dim, page_size) == 0:
@@ -732,39 +732,47 @@ class BlockCache:
         shape = (self.num_pages, self.kv_heads, self.page_size // 32, 34 * self.head_dim)
         if pool is None:
             pool = torch.zeros(shape, dtype=torch.uint8, device=device)
-        self._pool_ptr = _need(pool, "pool", torch.uint8, shape, device)
+        self._pool_ptr = _need(pool, "pool", torch.uint8, shape, self._index)
         self.pool = pool
+        self._workspace_bytes = {}          # by attention shape
 
     def _table(self, page_table, B):
-        if page_table.dim() != 2 or page_table.shape[0] != B or page_table.shape[1] < 1:
-            raise ValueError(f"page_table must be [{B}, max_pages], got {tuple(page_table.shape)}")
-        return (_need(page_table, "page_table", torch.int32, page_table.shape, self.device),
-                int(page_table.shape[1]))
-
-    def _ints(self, t, name, n):
-        return None if t is None else _need(t, name, torch.int32, (n,), self.device)
+        shape = page_table.shape
+        if len(shape) != 2 or shape[0] != B or shape[1] < 1:
+            raise ValueError(f"page_table must be [{B}, max_pages], got {tuple(shape)}")
+        return _need(page_table, "page_table", torch.int32, shape, self._index), shape[1]
 
     def write(self, keys, values, page_table, ctx_lens, budgets=None, status=None, stream=None):
         """Quantise [B, T, kv_heads, head_dim] keys and values (float32 or
         bfloat16; slices of a fused projection's rows are fine) into positions
         ctx_lens[b] .. ctx_lens[b] + budgets[b] of every request."""
-        if keys.dim() != 4 or keys.shape[2:] != (self.kv_heads, self.head_dim):
+        index = self._index
+        if stream is not None:
+            with _other_stream(stream, index):
+                return self.write(keys, values, page_table, ctx_lens, budgets, status)
+        if _current_device() != index:
+            with torch.cuda.device(index):
+                return self.write(keys, values, page_table, ctx_lens, budgets, status)
+        shape = keys.shape
+        if len(shape) != 4 or shape[2] != self.kv_heads or shape[3] != self.head_dim:
             raise ValueError(f"keys must be [B, T, {self.kv_heads}, {self.head_dim}]")
-        if values.shape != keys.shape or values.dtype != keys.dtype or keys.dtype not in _DTYPES:
+        dtype = _DTYPES.get(keys.dtype)
+        if values.shape != shape or values.dtype is not keys.dtype or dtype is None:
             raise ValueError("keys and values must share their shape and be float32 or bfloat16")
-        B, T = keys.shape[:2]
-        ks = _token_stride(keys, "keys", self.device)
-        vs = _token_stride(values, "values", self.device)
+        B, T = shape[0], shape[1]
+        ks = _token_stride(keys, "keys", index)
+        vs = _token_stride(values, "values", index)
         table, width = self._table(page_table, B)
-        ctx = _need(ctx_lens, "ctx_lens", torch.int32, (B,), self.device)
-        bud = self._ints(budgets, "budgets", B)
-        st = self._ints(status, "status", 1)
-        with _enqueue(self.device, stream) as s:
-            rc = spec_verify_cache_write(keys.data_ptr(), values.data_ptr(), _DTYPES[keys.dtype],
-                                         ks, vs, table, ctx, bud, B, T, self.kv_heads,
-                                         self.head_dim, self.page_size, width, self.num_pages,
-                                         self._pool_ptr, st, s)
-        _check(rc, "spec_verify_cache_write")
+        rc = load().spec_verify_cache_write(
+            keys.data_ptr(), values.data_ptr(), dtype, ks, vs, table,
+            _need(ctx_lens, "ctx_lens", torch.int32, (B,), index),
+            None if budgets is None else _need(budgets, "budgets", torch.int32, (B,), index),
+            B, T, self.kv_heads, self.head_dim, self.page_size, width, self.num_pages,
+            self._pool_ptr,
+            None if status is None else _need(status, "status", torch.int32, (1,), index),
+            _raw_stream(index))
+        if rc != SV_OK:
+            _check(rc, "spec_verify_cache_write")
 
     def read(self, page_table, starts, lens, length: int, dtype=torch.bfloat16, out=None,
              status=None, stream=None):
@@ -772,25 +780,34 @@ class BlockCache:
         starts[b] .. starts[b] + lens[b] - 1 (starts None: 0). Rows behind
         lens[b] are left as ``out`` (a pair of tensors) holds them; fresh
         outputs are zero there."""
-        B, T = int(lens.shape[0]), int(length)
+        index = self._index
+        if stream is not None:
+            with _other_stream(stream, index):
+                return self.read(page_table, starts, lens, length, dtype, out, status)
+        if _current_device() != index:
+            with torch.cuda.device(index):
+                return self.read(page_table, starts, lens, length, dtype, out, status)
+        B, T = lens.shape[0], int(length)
         shape = (B, T, self.kv_heads, self.head_dim)
         table, width = self._table(page_table, B)
-        first = self._ints(starts, "starts", B)
-        n = _need(lens, "lens", torch.int32, (B,), self.device)
-        st = self._ints(status, "status", 1)
         if out is not None:
             dtype = out[0].dtype
-        if dtype not in _DTYPES:
+        code = _DTYPES.get(dtype)
+        if code is None:
             raise ValueError(f"values are read as float32 or bfloat16, not {dtype}")
-        with _enqueue(self.device, stream) as s:
-            if out is None:
-                out = tuple(torch.zeros(shape, dtype=dtype, device=self.device) for _ in range(2))
-            ok = _need(out[0], "out keys", dtype, shape, self.device)
-            ov = _need(out[1], "out values", dtype, shape, self.device)
-            rc = spec_verify_cache_read(self._pool_ptr, table, first, n, B, T, self.kv_heads,
-                                        self.head_dim, self.page_size, width, self.num_pages,
-                                        _DTYPES[dtype], ok, ov, st, s)
-        _check(rc, "spec_verify_cache_read")
+        if out is None:
+            out = tuple(torch.zeros(shape, dtype=dtype, device=self.device) for _ in range(2))
+        rc = load().spec_verify_cache_read(
+            self._pool_ptr, table,
+            None if starts is None else _need(starts, "starts", torch.int32, (B,), index),
+            _need(lens, "lens", torch.int32, (B,), index), B, T, self.kv_heads, self.head_dim,
+            self.page_size, width, self.num_pages, code,
+            _need(out[0], "out keys", dtype, shape, index),
+            _need(out[1], "out values", dtype, shape, index),
+            None if status is None else _need(status, "status", torch.int32, (1,), index),
+            _raw_stream(index))
+        if rc != SV_OK:
+            _check(rc, "spec_verify_cache_read")
         return out[0], out[1]
 
     def attend(self, queries, page_table, ctx_lens, budgets=None, scale: float | None = None,
@@ -800,32 +817,45 @@ class BlockCache:
         already holds the blocks' own tokens. ``scale`` None: head_dim ** -0.5.
         Rows behind budgets[b] and empty slots are left as ``out`` holds them;
         a fresh output is zero there."""
-        if queries.dim() != 4 or queries.dtype != torch.bfloat16 \
-                or queries.shape[3] != self.head_dim or queries.shape[1] < 1:
+        index = self._index
+        if stream is not None:
+            with _other_stream(stream, index):
+                return self.attend(queries, page_table, ctx_lens, budgets, scale, window, out,
+                                   status)
+        if _current_device() != index:
+            with torch.cuda.device(index):
+                return self.attend(queries, page_table, ctx_lens, budgets, scale, window, out,
+                                   status)
+        shape = queries.shape
+        if len(shape) != 4 or queries.dtype is not torch.bfloat16 or shape[3] != self.head_dim \
+                or shape[1] < 1:
             raise ValueError(f"queries must be bfloat16 [B, K+1, q_heads, {self.head_dim}]")
-        B, T, heads, dim = queries.shape
-        stride = _token_stride(queries, "queries", self.device)
+        B, T, heads, dim = shape
+        stride = _token_stride(queries, "queries", index)
         table, width = self._table(page_table, B)
-        ctx = _need(ctx_lens, "ctx_lens", torch.int32, (B,), self.device)
-        bud = self._ints(budgets, "budgets", B)
-        st = self._ints(status, "status", 1)
-        window = int(window)
-        nbytes = spec_verify_attention_workspace_bytes(max(B, 1), T - 1, heads, self.kv_heads, dim,
-                                                       self.page_size, width, window)
-        if nbytes == 0:
-            raise ValueError(f"bad attention shape: B={B} K={T - 1} q_heads={heads} kv_heads="
-                             f"{self.kv_heads} window={window} max_pages={width}")
-        with _enqueue(self.device, stream) as s:
-            if out is None:
-                out = torch.zeros((B, T, heads, dim), dtype=torch.bfloat16, device=self.device)
-            o = _need(out, "out", torch.bfloat16, (B, T, heads, dim), self.device)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            rc = spec_verify_attention(queries.data_ptr(), stride, self._pool_ptr, table, ctx, bud,
-                                       B, T - 1, heads, self.kv_heads, dim, self.page_size, width,
-                                       self.num_pages,
-                                       dim ** -0.5 if scale is None else float(scale), window, o,
-                                       st, ws.data_ptr(), nbytes, s)
-        _check(rc, "spec_verify_attention")
+        key = (B, T, heads, width, window)
+        nbytes = self._workspace_bytes.get(key)
+        if nbytes is None:
+            nbytes = spec_verify_attention_workspace_bytes(
+                max(B, 1), T - 1, heads, self.kv_heads, dim, self.page_size, width, window)
+            if nbytes == 0:
+                raise ValueError(f"bad attention shape: B={B} K={T - 1} q_heads={heads} kv_heads="
+                                 f"{self.kv_heads} window={window} max_pages={width}")
+            self._workspace_bytes[key] = nbytes
+        if out is None:
+            out = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        rc = load().spec_verify_attention(
+            queries.data_ptr(), stride, self._pool_ptr, table,
+            _need(ctx_lens, "ctx_lens", torch.int32, (B,), index),
+            None if budgets is None else _need(budgets, "budgets", torch.int32, (B,), index),
+            B, T - 1, heads, self.kv_heads, dim, self.page_size, width, self.num_pages,
+            dim ** -0.5 if scale is None else scale, window,
+            _need(out, "out", torch.bfloat16, shape, index),
+            None if status is None else _need(status, "status", torch.int32, (1,), index),
+            workspace.data_ptr(), nbytes, _raw_stream(index))
+        if rc != SV_OK:
+            _check(rc, "spec_verify_attention")
         return out
 
 
@@ -834,22 +864,30 @@ def head_quantize(x: torch.Tensor, block_rows: int = 1, out=None, stream=None):
     8 bits: (codes float8_e4m3fn [rows, Hp], scales float8_e8m0fnu
     [ceil(rows / block_rows), Hp / 128]), Hp = H rounded up to 128, zeros
     behind H. block_rows 1 for hidden states, 128 for a head."""
-    if x.dim() != 2 or x.dtype not in _DTYPES or not x.is_cuda or not x.is_contiguous():
+    index = x.get_device()
+    code = _DTYPES.get(x.dtype)
+    if code is None or index < 0 or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous float32 or bfloat16 [rows, H] GPU tensor")
-    block_rows = int(block_rows)
-    if block_rows not in (1, 128):
+    if stream is not None:
+        with _other_stream(stream, index):
+            return head_quantize(x, block_rows, out)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return head_quantize(x, block_rows, out)
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
     rows, H = x.shape
     blocks = -(-H // 128)
-    shapes = (rows, blocks * 128), (-(-rows // block_rows), blocks)
-    types = torch.float8_e4m3fn, torch.float8_e8m0fnu
-    with _enqueue(x.device, stream) as s:
-        if out is None:
-            out = tuple(torch.empty(n, dtype=t, device=x.device) for n, t in zip(shapes, types))
-        c = _need(out[0], "out codes", types[0], shapes[0], x.device)
-        sc = _need(out[1], "out scales", types[1], shapes[1], x.device)
-        rc = spec_head_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, H, block_rows, c, sc, s)
-    _check(rc, "spec_head_quantize")
+    codes, scales = (rows, blocks * 128), (-(-rows // block_rows), blocks)
+    if out is None:
+        out = (torch.empty(codes, dtype=torch.float8_e4m3fn, device=x.device),
+               torch.empty(scales, dtype=torch.float8_e8m0fnu, device=x.device))
+    rc = load().spec_head_quantize(
+        x.data_ptr(), code, rows, H, block_rows,
+        _need(out[0], "out codes", torch.float8_e4m3fn, codes, index),
+        _need(out[1], "out scales", torch.float8_e8m0fnu, scales, index), _raw_stream(index))
+    if rc != SV_OK:
+        _check(rc, "spec_head_quantize")
     return out[0], out[1]
 
 
@@ -857,27 +895,34 @@ def head_logits(h_codes: torch.Tensor, h_scales: torch.Tensor, w_codes: torch.Te
                 w_scales: torch.Tensor, dtype=torch.float32, out=None, stream=None):
     """Logits [R, V] (float32 or bfloat16) of quantised states (block_rows 1)
     under a quantised head (block_rows 128)."""
+    index = h_codes.get_device()
+    if index < 0:
+        raise ValueError("h_codes must be a GPU tensor")
+    if stream is not None:
+        with _other_stream(stream, index):
+            return head_logits(h_codes, h_scales, w_codes, w_scales, dtype, out)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return head_logits(h_codes, h_scales, w_codes, w_scales, dtype, out)
     if h_codes.dim() != 2 or w_codes.dim() != 2 or h_codes.shape[1] != w_codes.shape[1] \
             or h_codes.shape[1] % 128 != 0 or h_codes.shape[1] == 0:
         raise ValueError("h_codes [R, Hp] and w_codes [V, Hp] must share Hp, a multiple of 128")
-    if not h_codes.is_cuda:
-        raise ValueError("h_codes must be a GPU tensor")
-    dev = h_codes.device
     R, H = h_codes.shape
     V = w_codes.shape[0]
     e4m3, e8m0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
-    hc = _need(h_codes, "h_codes", e4m3, (R, H), dev)
-    hs = _need(h_scales, "h_scales", e8m0, (R, H // 128), dev)
-    wc = _need(w_codes, "w_codes", e4m3, (V, H), dev)
-    ws = _need(w_scales, "w_scales", e8m0, (-(-V // 128), H // 128), dev)
     if out is not None:
         dtype = out.dtype
-    if dtype not in _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise ValueError(f"logits are float32 or bfloat16, not {dtype}")
-    with _enqueue(dev, stream) as s:
-        if out is None:
-            out = torch.empty((R, V), dtype=dtype, device=dev)
-        o = _need(out, "out", dtype, (R, V), dev)
-        rc = spec_head_logits(hc, hs, wc, ws, R, H, V, _DTYPES[dtype], o, s)
-    _check(rc, "spec_head_logits")
+    if out is None:
+        out = torch.empty((R, V), dtype=dtype, device=h_codes.device)
+    rc = load().spec_head_logits(
+        _need(h_codes, "h_codes", e4m3, (R, H), index),
+        _need(h_scales, "h_scales", e8m0, (R, H // 128), index),
+        _need(w_codes, "w_codes", e4m3, (V, H), index),
+        _need(w_scales, "w_scales", e8m0, (-(-V // 128), H // 128), index), R, H, V, code,
+        _need(out, "out", dtype, (R, V), index), _raw_stream(index))
+    if rc != SV_OK:
+        _check(rc, "spec_head_logits")
     return out
