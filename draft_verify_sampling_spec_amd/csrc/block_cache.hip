@@ -77,42 +77,56 @@ __device__ __forceinline__ unsigned get_codes(const uint8_t* tile, bool value, i
             << 16);
 }
 
-// One thread: 8 channels of one token, head and side (keys, values).
-// blockIdx.y: request; x: (token, head, side, channels).
+// Which token and 8 channels task i of a workgroup is: a workgroup takes the
+// tokens of one cache tile and head, 8 channels at a time, so that the tile's
+// lines are its own: a wavefront's 4-byte pieces of them are runs of 64 bytes
+// (keys) or 256 bytes (values), its 16-byte pieces of the tensors whole rows.
+// (Tokens across all heads in a workgroup measured 169 against 110 us for a read
+// of eight contexts of 8,192..16,384 tokens.)
+template <int D>
+struct Task {
+    static constexpr int kPer = D / 8, kSide = kTile * kPer, kAll = 2 * kSide;
+    int c, tok;
+    bool value;
+    __device__ __forceinline__ explicit Task(int i)
+        : c(i % kPer), tok(i % kSide / kPer), value(i >= kSide) {}
+};
+
+// blockIdx.y: request; x: (tile of the block's tokens, head).
 template <int D, typename S>
 __global__ __launch_bounds__(256) void cache_write_kernel(
     const S* __restrict__ keys, const S* __restrict__ values, long long key_stride,
     long long value_stride, const int32_t* __restrict__ ctx_lens,
     const int32_t* __restrict__ budgets, int T, Pages pages, uint8_t* __restrict__ cache,
     int32_t* __restrict__ status) {
-    constexpr int kPer = D / 8;
-    const int b = blockIdx.y;
+    const int b = blockIdx.y, h = blockIdx.x % pages.heads;
     const Block blk = block_of(ctx_lens, budgets, b, T, pages, status,
                                blockIdx.x == 0 && threadIdx.x == 0);
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int c = (int)(i % kPer);
-    const long long u = i / kPer;
-    const bool value = u & 1;
-    const int h = (int)((u >> 1) % pages.heads);
-    const long long t = (u >> 1) / pages.heads;
-    if (t >= blk.len) return;
-    const S* src = value ? values + ((long long)b * T + t) * value_stride
-                         : keys + ((long long)b * T + t) * key_stride;
-    float x[8];
-    load8(src + h * D + 8 * c, x);
-    unsigned byte;
-    const unsigned w = quantise8(x, byte);
-    const int pos = blk.ctx + (int)t;
-    const long long at = pages.tile(b, h, pos, Tile<D>::kBytes);
+    if (blk.len == 0) return;
+    const int pos0 = (blk.ctx / kTile + (int)(blockIdx.x / pages.heads)) * kTile;
+    if (pos0 >= blk.ctx + blk.len) return;
+    const long long at = pages.tile(b, h, pos0, Tile<D>::kBytes);
     if (at < 0) {
-        if (c == 0 && !value) flag(status, SV_FLAG_BAD_PAGE);
+        if (threadIdx.x == 0) flag(status, SV_FLAG_BAD_PAGE);
         return;
     }
     uint8_t* tile = cache + at;
-    const int tok = pos & (kTile - 1);
-    put_codes<D>(tile, value, tok, c, w);
-    if ((c & 3) == 0) {
-        tile[value ? Tile<D>::v_scale(tok, c >> 2) : Tile<D>::k_scale(tok, c >> 2)] = (uint8_t)byte;
+    #pragma unroll
+    for (int i = threadIdx.x; i < Task<D>::kAll; i += 256) {
+        const Task<D> task(i);
+        const int t = pos0 + task.tok - blk.ctx;            // the 4 lanes of a group agree
+        if (t < 0 || t >= blk.len) continue;
+        const S* src = task.value ? values + ((long long)b * T + t) * value_stride
+                                  : keys + ((long long)b * T + t) * key_stride;
+        float x[8];
+        load8(src + h * D + 8 * task.c, x);
+        unsigned byte;
+        const unsigned w = quantise8(x, byte);
+        put_codes<D>(tile, task.value, task.tok, task.c, w);
+        if ((task.c & 3) == 0) {
+            tile[task.value ? Tile<D>::v_scale(task.tok, task.c >> 2)
+                            : Tile<D>::k_scale(task.tok, task.c >> 2)] = (uint8_t)byte;
+        }
     }
 }
 
@@ -129,55 +143,51 @@ __device__ __forceinline__ void store8(uint16_t* p, const unsigned (&v)[4]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// One thread: 8 channels, as in the write. Every value is exact in bf16.
+// Every value is exact in bf16.
 template <int D, typename S>
 __global__ __launch_bounds__(256) void cache_read_kernel(
     const uint8_t* __restrict__ cache, const int32_t* __restrict__ starts,
     const int32_t* __restrict__ lens, int T, Pages pages, S* __restrict__ out_keys,
     S* __restrict__ out_values, int32_t* __restrict__ status) {
-    constexpr int kPer = D / 8;
-    const int b = blockIdx.y;
-    const bool report = blockIdx.x == 0 && threadIdx.x == 0;
+    const int b = blockIdx.y, h = blockIdx.x % pages.heads;
     const int start = starts ? starts[b] : 0;
     const int n = lens[b];
     if (start < 0 || n <= 0) return;
     if (n > T || (long long)start + n > ((long long)pages.max_pages << pages.shift)) {
-        if (report) flag(status, SV_FLAG_BAD_LENGTH);
+        if (blockIdx.x == 0 && threadIdx.x == 0) flag(status, SV_FLAG_BAD_LENGTH);
         return;
     }
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int c = (int)(i % kPer);
-    const long long u = i / kPer;
-    const bool value = u & 1;
-    const int h = (int)((u >> 1) % pages.heads);
-    const long long t = (u >> 1) / pages.heads;
-    if (t >= n) return;
-    const int pos = start + (int)t;
-    const long long at = pages.tile(b, h, pos, Tile<D>::kBytes);
+    const int pos0 = (start / kTile + (int)(blockIdx.x / pages.heads)) * kTile;
+    if (pos0 >= start + n) return;
+    const long long at = pages.tile(b, h, pos0, Tile<D>::kBytes);
     if (at < 0) {
-        if (c == 0 && !value) flag(status, SV_FLAG_BAD_PAGE);
+        if (threadIdx.x == 0) flag(status, SV_FLAG_BAD_PAGE);
         return;
     }
     const uint8_t* tile = cache + at;
-    const int tok = pos & (kTile - 1);
-    const unsigned w = get_codes<D>(tile, value, tok, c);
-    const float s = scale_of(
-        tile[value ? Tile<D>::v_scale(tok, c >> 2) : Tile<D>::k_scale(tok, c >> 2)]);
-    const unsigned v[4] = {decode2<0>(w, s), decode2<1>(w, s), decode2<2>(w, s), decode2<3>(w, s)};
-    S* out = value ? out_values : out_keys;
-    store8(out + (((long long)b * T + t) * pages.heads + h) * D + 8 * c, v);
+    #pragma unroll
+    for (int i = threadIdx.x; i < Task<D>::kAll; i += 256) {
+        const Task<D> task(i);
+        const int t = pos0 + task.tok - start;
+        if (t < 0 || t >= n) continue;
+        const unsigned w = get_codes<D>(tile, task.value, task.tok, task.c);
+        const float s = scale_of(tile[task.value ? Tile<D>::v_scale(task.tok, task.c >> 2)
+                                                 : Tile<D>::k_scale(task.tok, task.c >> 2)]);
+        const unsigned v[4] = {decode2<0>(w, s), decode2<1>(w, s), decode2<2>(w, s), decode2<3>(w, s)};
+        S* out = task.value ? out_values : out_keys;
+        store8(out + (((long long)b * T + t) * pages.heads + h) * D + 8 * task.c, v);
+    }
 }
 
-long long blocks_for(int T, int heads, int D) {
-    return ((long long)T * heads * 2 * (D / 8) + 255) / 256;
-}
+// Tiles that T tokens from any position touch, times heads.
+unsigned blocks_for(int T, int heads) { return (unsigned)((T + 2ll * kTile - 2) / kTile * heads); }
 
 template <int D, typename S>
 void launch_write(const void* keys, const void* values, int64_t ks, int64_t vs,
                   const int32_t* ctx, const int32_t* budgets, int B, int T, const Pages& pages,
                   void* cache, int32_t* status, hipStream_t s) {
     hipLaunchKernelGGL((cache_write_kernel<D, S>),
-                       dim3((unsigned)blocks_for(T, pages.heads, D), (unsigned)B), dim3(256), 0, s,
+                       dim3(blocks_for(T, pages.heads), (unsigned)B), dim3(256), 0, s,
                        static_cast<const S*>(keys), static_cast<const S*>(values), ks, vs, ctx,
                        budgets, T, pages, static_cast<uint8_t*>(cache), status);
 }
@@ -186,7 +196,7 @@ template <int D, typename S>
 void launch_read(const void* cache, const int32_t* starts, const int32_t* lens, int B, int T,
                  const Pages& pages, void* ok, void* ov, int32_t* status, hipStream_t s) {
     hipLaunchKernelGGL((cache_read_kernel<D, S>),
-                       dim3((unsigned)blocks_for(T, pages.heads, D), (unsigned)B), dim3(256), 0, s,
+                       dim3(blocks_for(T, pages.heads), (unsigned)B), dim3(256), 0, s,
                        static_cast<const uint8_t*>(cache), starts, lens, T, pages,
                        static_cast<S*>(ok), static_cast<S*>(ov), status);
 }
