@@ -386,14 +386,29 @@ void launch_logits(const LogitArgs& a, hipStream_t s) {
                        band);
 }
 
-// Tiles by the number of rows: up to 64 rows the head's bytes decide and the
-// tile is as narrow as its rows; above, the largest tile that they fill.
+// Tiles by the number of rows and columns. Up to 64 rows the head's bytes
+// decide and the tile is as narrow as its rows. Above, the tile whose rounds of
+// workgroups take least: a round of 256 x 256 tiles (one workgroup per CU) as
+// the unit, one of 128 x 128 tiles (two) measured 0.62 of it and one of 64 x 64
+// tiles (three) 0.375, for an eighth more and twice the time per product. (20,000
+// columns x 5,120 channels, bf16: 300 rows take 62, 47, 71 us with them, 700
+// rows 68, 83, 136; 2,560 columns x 4,096, 1,024 rows: 50, 31, 27.)
 template <bool kF8, typename O>
 void launch_rows(const LogitArgs& a, hipStream_t s) {
-    if (a.R <= 32) launch_logits<Cfg<64, 32, 2, 1, 3, kF8, O>>(a, s);
-    else if (a.R <= 64) launch_logits<Cfg<64, 64, 2, 2, 3, kF8, O>>(a, s);
-    else if (a.R <= 128) launch_logits<Cfg<256, 128, 4, 2, 3, kF8, O>>(a, s);
-    else launch_logits<Cfg<256, 256, 2, 4, 2, kF8, O>>(a, s);
+    if (a.R <= 32) return launch_logits<Cfg<64, 32, 2, 1, 3, kF8, O>>(a, s);
+    if (a.R <= 64) {
+        // Twice the columns once every resident workgroup has some: 105 against
+        // 100 us for 48 rows of fp32 logits, but 30 against 31 at 20,000 columns.
+        if (a.V >= 128 * 512) return launch_logits<Cfg<128, 64, 4, 2, 3, kF8, O>>(a, s);
+        return launch_logits<Cfg<64, 64, 2, 2, 3, kF8, O>>(a, s);
+    }
+    auto rounds = [&](long long tile, long long held) {
+        return (double)(((a.V + tile - 1) / tile * ((a.R + tile - 1) / tile) + held - 1) / held);
+    };
+    const double large = rounds(256, 256), middle = 0.62 * rounds(128, 512), small = 0.375 * rounds(64, 768);
+    if (large <= middle && large <= small) launch_logits<Cfg<256, 256, 2, 4, 2, kF8, O>>(a, s);
+    else if (middle <= small) launch_logits<Cfg<128, 128, 2, 2, 2, kF8, O>>(a, s);
+    else launch_logits<Cfg<64, 64, 2, 2, 3, kF8, O>>(a, s);
 }
 
 }  // namespace
