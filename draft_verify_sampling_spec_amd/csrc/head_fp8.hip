@@ -8,7 +8,7 @@
 //   z[r, v] = sum_blk s_h[r, blk] s_w[v / 128, blk] sum_i h[r, i] w[v, i].
 // A scale that is a power of two costs the product nothing: decoding a code
 // to bf16 times its scale is exact.
-#include <cmath>
+#include <type_traits>
 
 #include "cache_tile.h"
 #include "lds_dma.h"
@@ -427,28 +427,26 @@ extern "C" int spec_head_quantize(const void* src, int dtype, int rows, int H, i
     const hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t* codes = static_cast<uint8_t*>(out_codes);
     uint8_t* scales = static_cast<uint8_t*>(out_scales);
-    const dim3 grid(block_rows == 1
-                        ? (unsigned)(((long long)rows * blocks * 16 + 255) / 256)
-                        : (unsigned)((rows + kBlock - 1) / kBlock * blocks));
-    if (dtype == SV_DTYPE_F32) {
-        const float* p = static_cast<const float*>(src);
-        if (block_rows == 1) {
-            hipLaunchKernelGGL((quantize_rows_kernel<float>), grid, dim3(256), 0, s, p, rows, H,
-                               blocks, codes, scales);
-        } else {
-            hipLaunchKernelGGL((quantize_blocks_kernel<float>), grid, dim3(256), 0, s, p, rows, H,
-                               blocks, codes, scales);
+    auto launch = [&](auto* p) {
+        using S = std::remove_pointer_t<decltype(p)>;
+        if (block_rows == kBlock) {
+            hipLaunchKernelGGL((quantize_blocks_kernel<std::remove_const_t<S>>),
+                               dim3((unsigned)((rows + kBlock - 1) / kBlock * blocks)), dim3(256), 0,
+                               s, p, rows, H, blocks, codes, scales);
+            return;
         }
-    } else {
-        const uint16_t* p = static_cast<const uint16_t*>(src);
-        if (block_rows == 1) {
-            hipLaunchKernelGGL((quantize_rows_kernel<uint16_t>), grid, dim3(256), 0, s, p, rows, H,
-                               blocks, codes, scales);
-        } else {
-            hipLaunchKernelGGL((quantize_blocks_kernel<uint16_t>), grid, dim3(256), 0, s, p, rows,
-                               H, blocks, codes, scales);
+        // A launch holds fewer than 2^32 threads, 16 a block.
+        const int most = (int)(((1ll << 31) / 16) / blocks);
+        for (int r = 0; r < rows; r += most) {
+            const int n = rows - r < most ? rows - r : most;
+            hipLaunchKernelGGL((quantize_rows_kernel<std::remove_const_t<S>>),
+                               dim3((unsigned)(((long long)n * blocks * 16 + 255) / 256)), dim3(256), 0,
+                               s, p + (long long)r * H, n, H, blocks,
+                               codes + (long long)r * blocks * kBlock, scales + (long long)r * blocks);
         }
-    }
+    };
+    if (dtype == SV_DTYPE_F32) launch(static_cast<const float*>(src));
+    else launch(static_cast<const uint16_t*>(src));
     return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 

@@ -473,8 +473,9 @@ size_t spec_markov_draft_workspace_bytes(int B, int V);
  *   page_table   int32 [B, max_pages] (device): the page of positions
  *                [i page_size, (i + 1) page_size) of request b. Entries that a
  *                call does not need are never read as pages; a needed entry
- *                outside [0, num_pages) sets SV_FLAG_BAD_PAGE and its tokens
- *                are skipped (never accessed out of bounds). max_pages *
+ *                outside [0, num_pages) sets SV_FLAG_BAD_PAGE and is never
+ *                accessed: writes and reads skip its tokens, the attention's
+ *                outputs of that request are undefined. max_pages *
  *                page_size is at most SV_MAX_CONTEXT.
  *   ctx_lens     int32 [B] (device): tokens of request b in the cache before
  *                this block; negative marks an empty slot, which is skipped
@@ -547,7 +548,9 @@ int spec_verify_cache_read(const void* cache, const int32_t* page_table, const i
  * Products accumulate in fp32, the softmax's statistics are fp32. A NaN group
  * of a key or value reaches exactly the rows that see its token. K = 0 is the
  * single-token form. Stream-ordered, no host sync, one launch, or two when the
- * contexts are split over workgroups (a choice by the shapes alone).
+ * contexts may be split over workgroups (a choice by the shapes alone; how they
+ * are split is decided on the device by all requests' lengths and budgets, so
+ * the order of a request's sums may depend on what else is in the batch).
  *   queries      bf16 [B, K+1, q_heads, head_dim] (device, 16-byte aligned),
  *                query_stride elements between tokens (at least q_heads *
  *                head_dim, a multiple of 8). Rows t > budgets[b] are never read.
@@ -558,7 +561,8 @@ int spec_verify_cache_read(const void* cache, const int32_t* page_table, const i
  *   window       0, or the number of positions a row sees, its own included.
  *                Pages wholly before every row's window are not needed.
  *   out          bf16 [B, K+1, q_heads, head_dim] (device, 16-byte aligned).
- *                Rows t > budgets[b] and empty slots keep their values.
+ *                Rows t > budgets[b] and empty slots keep their values. It may
+ *                not overlap any other argument.
  *   workspace    device scratch of at least
  *                spec_verify_attention_workspace_bytes() bytes (256-byte
  *                aligned), caller-owned, its contents of no account; calls

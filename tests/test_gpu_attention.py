@@ -141,6 +141,72 @@ def test_many_requests_in_one_launch():
     c.check(c.run())
 
 
+def _check_on_gpu(cache, q, got, table, ctx, budgets, window=0):
+    """Every row against fp64 products on the GPU of the values that the cache
+    reads back (which are exact, tested on their own): for batches too large
+    for the CPU."""
+    B, T, Hq, D = q.shape
+    Hkv = cache.kv_heads
+    for b in range(B):
+        c, k = int(ctx[b]), int(budgets[b])
+        if c < 0:
+            assert not got[b].any()
+            continue
+        first = max(0, c - window + 1) if window else 0
+        n = c + k + 1 - first
+        keys, values = cache.read(table[b:b + 1], _i32([first]), _i32([n]), n, dtype=torch.float32)
+        keys, values = (x[0].double().permute(1, 0, 2).contiguous() for x in (keys, values))
+        rows = q[b, :k + 1].double().unflatten(1, (Hkv, Hq // Hkv)).permute(1, 0, 2, 3).flatten(1, 2)
+        z = rows @ keys.transpose(1, 2) * D ** -0.5
+        pos = torch.arange(first, first + n, device=DEV)
+        row = (c + torch.arange(k + 1, device=DEV)).repeat_interleave(Hq // Hkv)[:, None]
+        hidden = (pos > row) | ((pos <= row - window) if window else False)
+        p = torch.softmax(z.masked_fill(hidden, -math.inf), -1)
+        ref, mag = p @ values, p @ values.abs()
+        reach = (rows.abs() @ keys.abs().transpose(1, 2)).amax(-1, keepdim=True) * D ** -0.5
+        tol = (2.0 ** -8 + 2 * (D + 2) * 2.0 ** -24 * reach + 2.0 ** -20 * (1 + n / 4096)) * mag \
+            + 2.0 ** -8 * (1 + 2.0 ** -7) * ref.abs() + 1e-30
+        mine = got[b, :k + 1].double().unflatten(1, (Hkv, Hq // Hkv)).permute(1, 0, 2, 3).flatten(1, 2)
+        assert bool(((mine - ref).abs() <= tol).all()), (b, float(((mine - ref).abs() / tol).max()))
+        assert not got[b, k + 1:].any()
+
+
+@pytest.mark.parametrize("B,K,Hq,Hkv,D,lo,hi,window", [
+    (8, 8, 224, 32, 64, 3000, 15000, 0),       # ragged, long: equal shares, units in several parts
+    (140, 2, 16, 8, 128, 300, 9000, 0),        # more units than workgroups
+    (500, 1, 16, 16, 64, 30, 1500, 0),         # a workgroup per unit, many of them
+    (6, 8, 64, 1, 128, 2000, 9000, 0),         # 576 rows a request: row blocks of one unit
+    (3, 32, 16, 2, 256, 1500, 6000, 0),        # 264 rows a head of 256 channels
+    (24, 5, 16, 8, 256, 200, 5000, 1024),      # windows, units of nearly one size
+    (2, 3, 8, 2, 128, 30000, 60000, 0),        # few units, many parts
+])
+def test_every_way_the_work_is_cut(B, K, Hq, Hkv, D, lo, hi, window):
+    _log(f"[attend] B={B} K={K} Hq={Hq} Hkv={Hkv} D={D} ctx {lo}..{hi} window={window}")
+    g = torch.Generator(device=DEV).manual_seed(B + K)
+    ctx = torch.randint(lo, hi + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+    ctx[B // 2] = lo
+    ctx[0] = hi
+    budgets = torch.randint(0, K + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+    if B > 2:
+        ctx[1] = -1
+    page = 64
+    need = (ctx.clamp_min(0) + budgets + page) // page
+    first = torch.cumsum(need, 0) - need
+    width, pages = int(need.max()), int(need.sum())
+    col = torch.arange(width, device=DEV)
+    order = torch.randperm(pages, generator=g, device=DEV)
+    table = torch.where(col < need[:, None], order[(first[:, None] + col).clamp_max(pages - 1)], -1).int()
+    cache = BlockCache(DEV, pages, Hkv, D, page)
+    cache.pool.random_(0, 256, generator=g)
+    cache.pool[..., 32 * D:].random_(122, 129, generator=g)
+    q = torch.randn(B, K + 1, Hq, D, generator=g, device=DEV).bfloat16()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = cache.attend(q, table, ctx, budgets, window=window, status=status)
+    _check_on_gpu(cache, q, got, table, ctx.tolist(), budgets.tolist(), window)
+    assert int(status) == 0
+    assert torch.equal(cache.attend(q, table, ctx, budgets, window=window), got)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
 def test_scales_and_sharp_softmax(scale):
     c = Case(3, 4, 4, 2, 128, 64, np.array([100, 0, 1000]), np.array([4, 4, 2]), seed=3)
