@@ -39,10 +39,11 @@ constexpr float kNegInf = -INFINITY;
 // How the work is cut. A unit is a request's kv head and block of 16 kMT
 // rows, its cost the tiles times (kTileCost plus their row tiles; measured
 // times per tile grow like that, one unit about 0.05 us). Three cuts:
-//  - direct: a workgroup per unit and nothing to join, where page table rows
-//    have at most kDirectTiles tiles (searching and joining would cost more),
-//    or where there are kDirectUnits units for every workgroup that is
-//    resident at once (they even out by themselves).
+//  - direct: a workgroup per unit and nothing to join, where rows see at most
+//    kDirectTiles tiles, or twice that if every workgroup that is resident at
+//    once has a unit (searching and joining, about 8 us, would cost more: 64
+//    requests under a window of 1,024 tokens 41 against 34 us), or where each
+//    has kDirectUnits units (they even out by themselves).
 // Else the lengths, which are on the device, decide. Every workgroup adds up
 // the requests for itself and finds its place by a prefix sum. With `groups`
 // workgroups resident at once and share = (cost of all units) / groups:
@@ -900,7 +901,8 @@ Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_p
     const long long most = (units * tiles * (kTileCost + p.mt) + kLeastShare - 1) / kLeastShare;
     const int held = D == 64 ? resident<64>(p.mt) : D == 128 ? resident<128>(p.mt) : resident<256>(p.mt);
     p.groups = (int)std::min<long long>(held, most);
-    p.direct = tiles <= kDirectTiles || units >= (long long)kDirectUnits * held;
+    p.direct = tiles <= kDirectTiles || (units >= held && tiles <= 2 * kDirectTiles) ||
+               units >= (long long)kDirectUnits * held;
     p.grid = (int)(p.direct ? units : p.groups + std::min<long long>(units, held));
     p.slots = p.direct ? 0 : std::max(2 * p.groups, p.grid);
     return p;
