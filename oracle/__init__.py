@@ -14,6 +14,7 @@ Modules:
   head    -- the shared output head's row statistics.
   hidden  -- a verify step whose logits come from hidden states and the head.
   markov  -- the drafter's low-rank Markov head (previous-token logit bias).
+  lowbit  -- the 4-bit cache, the blocks' attention over it and the 8-bit head.
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against facts that
 do not come from the oracle itself: library routines (rocRAND's Philox,
