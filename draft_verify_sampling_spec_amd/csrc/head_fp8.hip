@@ -156,8 +156,8 @@ struct LogitArgs {
 // logits. Otherwise the codes are decoded to bf16 (exact, scales included) in
 // registers and multiplied in bf16, for fp32 logits: the 8-bit instructions
 // keep a sum of products only to about 2^-17 of its terms (relative error
-// 1.4e-5 of a row's norm, measured at 128, 2,560 and 10,240 channels), an
-// eighth of a hundredth of a bf16 rounding but two hundred fp32 ones.
+// 1.4e-5 of a row's norm, measured at 128, 2,560 and 10,240 channels): under a
+// two-hundredth of a bf16 rounding, but two hundred fp32 ones.
 template <int TV_, int TR_, int WV_, int WR_, int kStages_, bool kF8_, typename O_>
 struct Cfg {
     static constexpr int TV = TV_, TR = TR_, WV = WV_, WR = WR_, kStages = kStages_;

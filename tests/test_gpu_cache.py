@@ -235,3 +235,61 @@ def test_python_refusals():
             BlockCache(DEV, *geometry)
     with pytest.raises(ValueError):
         BlockCache("cpu", 4, 2, 64, 32)
+
+
+def test_two_streams_and_a_replayed_graph():
+    """Writes of two halves of a batch on two streams at once, and a write and a
+    read captured together and replayed with new tokens and lengths between
+    eager calls of another cache."""
+    B, T, heads, D, page = 6, 40, 2, 128, 64
+    g = torch.Generator(device=DEV).manual_seed(9)
+    k, v = (torch.randn(B, T, heads, D, generator=g, device=DEV).bfloat16() for _ in range(2))
+    table = torch.randperm(12, generator=g, device=DEV).int().view(B, 2)
+    ctx, budgets = _i32([0, 31, 5, -1, 60, 88]), _i32([39, 0, 20, 3, 39, 39])
+    a, b = (BlockCache(DEV, 12, heads, D, page) for _ in range(2))
+    a.write(k, v, table, ctx, budgets)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i, s in enumerate(streams):
+        part = slice(3 * i, 3 * i + 3)
+        b.write(k[part], v[part], table[part], ctx[part], budgets[part], stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(a.pool, b.pool)
+    out = tuple(torch.zeros_like(k) for _ in range(2))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.write(k, v, table, ctx, budgets)
+        b.read(table, ctx, budgets, T, out=out)
+    for i in range(4):
+        k.mul_(-1.5)
+        v.add_(0.25)
+        budgets.copy_(_i32([30 + i, i, 39 - i, 3, 39, 7]))
+        for x in out:
+            x.zero_()
+        a.write(k, v, table, ctx, budgets)
+        want = a.read(table, ctx, budgets, T)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a.pool, b.pool)
+        assert all(torch.equal(x, y) for x, y in zip(out, want))
+
+
+def test_the_largest_batch():
+    B = 16384
+    g = torch.Generator(device=DEV).manual_seed(10)
+    k, v = (torch.randn(B, 1, 1, 64, generator=g, device=DEV) for _ in range(2))
+    table = torch.randperm(B, generator=g, device=DEV).int()[:, None]
+    ctx = torch.randint(0, 32, (B,), generator=g, device=DEV, dtype=torch.int32)
+    cache = BlockCache(DEV, B, 1, 64, 32)
+    cache.write(k, v, table, ctx)
+    got = cache.read(table, ctx, torch.ones_like(ctx), 1, dtype=torch.float32)
+    for x, y in zip((k, v), got):
+        ref = lb.cache_values(*lb.quantise_cache(x.double().cpu().numpy()))
+        assert np.array_equal(y.double().cpu().numpy(), ref)
+    # Batches, tokens and lists of none.
+    before = cache.pool.clone()
+    cache.write(k[:0], v[:0], table[:0], ctx[:0])
+    cache.write(k[:, :0], v[:, :0], table, ctx)
+    assert cache.read(table[:0], None, ctx[:0], 5)[0].shape == (0, 5, 1, 64)
+    assert cache.read(table, None, ctx, 0)[0].shape == (B, 0, 1, 64)
+    assert torch.equal(cache.pool, before)

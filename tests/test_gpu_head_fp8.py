@@ -227,3 +227,37 @@ def test_a_verify_step_from_few_bits():
         ctx = ctx + n + 1                                   # rejected tokens are simply overwritten
     assert int(status) == 0 and sv.status() == 0
     sv.close()
+
+
+def test_logits_past_32_bit_offsets():
+    """More than 2^32 logits: the last rows against fp64 products."""
+    R, H, V = 16450, 128, 1 << 18
+    g = torch.Generator(device=DEV).manual_seed(11)
+    h = torch.randn(R, H, generator=g, device=DEV)
+    w = torch.randn(V, H, generator=g, device=DEV) * (3.0 / H ** 0.5)
+    hc, hs = head_quantize(h, 1)
+    wc, ws = head_quantize(w, 128)
+    got = head_logits(hc, hs, wc, ws, dtype=torch.bfloat16)
+    pick = [0, 8191, 8192, R - 67, R - 1]
+    a = torch.tensor(lb.head_values(hc[pick].double().cpu().numpy(), _scales(hs[pick]), 1)).to(DEV)
+    b = torch.tensor(lb.head_values(wc.double().cpu().numpy(), _scales(ws), 128)).to(DEV).t().contiguous()
+    ref, S = a @ b, a.abs() @ b.abs()
+    tol = (4 * math.sqrt(H) * 2.0 ** -24 + 2.0 ** -15) * S + 1e-30 + 2.0 ** -8 * (1 + 2.0 ** -7) * ref.abs()
+    err = (got[pick].double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+def test_two_streams_at_once():
+    g = torch.Generator(device=DEV).manual_seed(12)
+    h = torch.randn(2, 70, 640, generator=g, device=DEV).bfloat16()
+    wq = head_quantize(torch.randn(5000, 640, generator=g, device=DEV).bfloat16(), 128)
+    want = [head_logits(*head_quantize(x), *wq) for x in h]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            got[i].append(head_logits(*head_quantize(h[i], stream=s), *wq, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
