@@ -830,6 +830,8 @@ class BlockCache:
         if len(shape) != 4 or queries.dtype is not torch.bfloat16 or shape[3] != self.head_dim \
                 or shape[1] < 1:
             raise ValueError(f"queries must be bfloat16 [B, K+1, q_heads, {self.head_dim}]")
+        if not 0 <= window <= 0x7fffffff:                   # ctypes would cut it to 32 bits
+            raise ValueError(f"window must be 0..2^31 - 1, got {window}")
         B, T, heads, dim = shape
         stride = _token_stride(queries, "queries", index)
         table, width = self._table(page_table, B)

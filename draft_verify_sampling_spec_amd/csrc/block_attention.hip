@@ -7,8 +7,8 @@
 // with the running maximum m and the sums held in fp32 over one pass. Keys
 // and values are decoded to bf16 (exact); products accumulate in fp32 on the
 // matrix cores. The probabilities 2^(z - m), in [0, 1], are rounded to bf16
-// for the value product (2^-9 relative each, the size of the output's own
-// rounding); their sum is taken before that rounding.
+// for the value product (at most 2^-8 relative each, the size of the output's
+// own rounding); their sum is taken before that rounding.
 //
 // Layout: a wavefront takes tiles of 32 tokens of one kv head and all query
 // rows that share it (up to 16 kMT rows of (t, head in the group), in
@@ -991,8 +991,9 @@ extern "C" int spec_verify_attention(const void* queries, int64_t query_stride, 
     a.direct = p.direct;
     a.negate = scale < 0.0f;
     // A scale of 0 becomes 2^-126, under which every seen score is as good as 0
-    // and an unseen one (-inf) still is -inf.
-    a.c = std::max((float)(std::fabs((double)scale) * 1.4426950408889634), FLT_MIN);
+    // and an unseen one (-inf) still is -inf; one too large for fp32 its largest
+    // value, under which a score of 0 still is 0.
+    a.c = (float)std::clamp(std::fabs((double)scale) * 1.4426950408889634, (double)FLT_MIN, (double)FLT_MAX);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     switch (head_dim * 8 + p.mt) {
         case 64 * 8 + 1: launch<64, 1>(a, p, s); break;

@@ -488,8 +488,8 @@ size_t spec_markov_draft_workspace_bytes(int B, int V);
  *                Outputs of a flagged request are undefined, apart from what
  *                is said to be skipped.
  * A block that does not fit its page table row sets SV_FLAG_BAD_LENGTH and is
- * skipped. Requests may share pages that are only read; two tokens written to
- * the same place in one call leave either of them.
+ * skipped. Requests may share pages that are only read; what two tokens written
+ * to the same place at once leave there is undefined.
  */
 
 /* spec_verify_cache_bytes -- bytes of a cache of num_pages pages; 0 on bad
@@ -557,7 +557,8 @@ int spec_verify_cache_read(const void* cache, const int32_t* page_table, const i
  *   B, K         requests (0..SV_MAX_BATCH; 0 is a no-op), drafted tokens
  *                (0..SV_MAX_K).
  *   q_heads      a multiple of kv_heads, up to SV_MAX_HEADS.
- *   scale        finite; usually 1 / sqrt(head_dim).
+ *   scale        finite; usually 1 / sqrt(head_dim). Scores scale log2(e) q . k
+ *                past fp32's range give NaN.
  *   window       0, or the number of positions a row sees, its own included.
  *                Pages wholly before every row's window are not needed.
  *   out          bf16 [B, K+1, q_heads, head_dim] (device, 16-byte aligned).
@@ -598,7 +599,7 @@ size_t spec_verify_attention_workspace_bytes(int B, int K, int q_heads, int kv_h
 
 /*
  * spec_head_quantize -- quantise hidden states or a head. Stream-ordered, one
- * launch.
+ * launch (several for states of more than 2^31 / 16 blocks).
  *   src         [rows, H] of type dtype (sv_dtype), row-major (device,
  *               16-byte aligned); rows 0..SV_MAX_VOCAB (0 is a no-op), H a
  *               multiple of 8, 8..SV_MAX_HIDDEN.

@@ -354,3 +354,112 @@ def test_python_refusals():
         c.attend(q, table, one, out=torch.zeros(1, 2, 4, 64, device=DEV))
     with pytest.raises(ValueError):
         c.attend(torch.zeros(1, 40, 4, 64, dtype=torch.bfloat16, device=DEV), table, one)
+
+
+def test_two_streams_at_once_over_shared_pages():
+    """Requests that share the pages of a prefix, attended on two streams at
+    the same time: each call has its own workspace."""
+    Hq, Hkv, D, page = 16, 4, 128, 64
+    g = torch.Generator(device=DEV).manual_seed(14)
+    cache = BlockCache(DEV, 220, Hkv, D, page)
+    cache.pool.random_(0, 256, generator=g)
+    cache.pool[..., 32 * D:].random_(122, 129, generator=g)
+    table = torch.arange(200, device=DEV).repeat(4, 1).int()
+    table[:, 199] = _i32([200, 201, 202, 203])               # every request's own last page
+    ctx, budgets = _i32([12736, 12790, 12750, 7000]), _i32([4, 4, 0, 2])
+    q = [torch.randn(4, 5, Hq, D, generator=g, device=DEV).bfloat16() for _ in range(2)]
+    want = [cache.attend(x, table, ctx, budgets) for x in q]
+    _check_on_gpu(cache, q[0], want[0], table, ctx, budgets)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            got[i].append(cache.attend(q[i], table, ctx, budgets, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+@pytest.mark.parametrize("K,window", [(0, 0), (3, 0), (3, 2**31 - 1)])
+def test_the_longest_context(K, window):
+    """2^24 positions over eight pages of 4,096 tokens in turn. Rows at the end
+    see every position before the block's first exactly as often, so K = 0 is
+    attention over the 32,768 distinct tokens."""
+    D, page, per = 64, 4096, 8
+    n = 1 << 24
+    _log(f"[attend] {n} positions, K={K} window={window}")
+    g = torch.Generator(device=DEV).manual_seed(15)
+    cache = BlockCache(DEV, per, 1, D, page)
+    cache.pool.random_(0, 256, generator=g)
+    cache.pool[..., 32 * D:].random_(122, 129, generator=g)
+    table = (torch.arange(n // page, device=DEV) % per).int()[None]
+    q = torch.randn(1, K + 1, 2, D, generator=g, device=DEV).bfloat16()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = cache.attend(q, table, _i32([n - 1 - K]), window=window, status=status)
+    assert int(status) == 0
+    keys, values = cache.read(table[:, :per], None, _i32([per * page]), per * page, dtype=torch.float32)
+    keys, values = keys[0, :, 0].double(), values[0, :, 0].double()
+    rows = q[0].double().flatten(0, 1)                       # (t, head)
+    z = rows @ keys.t().contiguous() * D ** -0.5
+    # How often row t sees each token: the last K - t positions are hidden.
+    seen = torch.full((K + 1, per * page), float(n // (per * page)), device=DEV).double()
+    for t in range(K):
+        seen[t, per * page - K + t:] -= 1.0
+    seen = seen.repeat_interleave(2, 0)
+    w = seen * torch.exp(z - z.amax(1, keepdim=True))
+    p = w / w.sum(1, keepdim=True)
+    ref, mag = p @ values, p @ values.abs()
+    reach = (rows.abs() @ keys.abs().t().contiguous()).amax(1, keepdim=True) * D ** -0.5
+    tol = (2.0 ** -8 + 2 * (D + 2) * 2.0 ** -24 * reach + 2.0 ** -20 * (1 + n / 4096)) * mag \
+        + 2.0 ** -8 * (1 + 2.0 ** -7) * ref.abs() + 1e-30
+    err = (got[0].double().flatten(0, 1) - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    # A position more does not fit.
+    cache.attend(q, table, _i32([n - K]), status=status)
+    assert int(status) == sb.SV_FLAG_BAD_LENGTH
+
+
+def test_the_largest_batch():
+    """16,384 single tokens, 256 heads that share nothing."""
+    B, heads, D = 16384, 256, 64
+    g = torch.Generator(device=DEV).manual_seed(16)
+    cache = BlockCache(DEV, 2, heads, D, 32)
+    cache.pool.random_(0, 256, generator=g)
+    cache.pool[..., 32 * D:].random_(122, 129, generator=g)
+    table = torch.tensor([[0, 1], [1, 0]], device=DEV).repeat(B // 2, 1).int()
+    ctx = torch.arange(B, device=DEV, dtype=torch.int32) % 61 - 1       # -1..59, in turn
+    q = torch.randn(61 * 2, 1, heads, D, generator=g, device=DEV).bfloat16()
+    q = q.repeat(B // 122 + 1, 1, 1, 1)[:B].contiguous()
+    got = cache.attend(q, table, ctx)
+    period = 122
+    _check_on_gpu(cache, q[:period], got[:period], table, ctx, torch.zeros(period, dtype=torch.int32))
+    whole = B // period * period
+    assert torch.equal(got[:whole].view(-1, period, heads * D),
+                       got[:period].view(1, period, heads * D).expand(B // period, -1, -1))
+    assert torch.equal(got[whole:], got[:B - whole])
+    none = cache.attend(q[:0], table[:0], ctx[:0])
+    assert none.shape == (0, 1, heads, D)
+
+
+def test_windows_beyond_32_bits_are_refused():
+    c = BlockCache(DEV, 4, 2, 64, 32)
+    q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16, device=DEV)
+    for window in (2**31, 2**32, 2**32 + 5, -2**32):
+        with pytest.raises(ValueError):
+            c.attend(q, _i32([[0]]), _i32([0]), window=window)
+
+
+def test_scales_near_the_largest():
+    """A scale whose product with log2(e) is no longer finite: equal scores
+    still share the weight, a larger one takes it all."""
+    c = BlockCache(DEV, 1, 1, 64, 32)
+    k, v = (torch.zeros(1, 4, 1, 64, device=DEV) for _ in range(2))
+    k[0, 2, 0, 0] = 1.0
+    v[0, :, 0, 0] = torch.tensor([1.0, 2.0, 4.0, 3.0], device=DEV)
+    table = _i32([[0]])
+    c.write(k, v, table, _i32([0]))
+    q = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16, device=DEV)
+    q[0, 3, 0, 0] = 2.0 ** -100
+    got = c.attend(q, table, _i32([0]), scale=3.0e38)[0, :, 0, 0].tolist()
+    assert got[0] == 1.0 and got[1] == 1.5 and abs(got[2] - 7 / 3) <= 2.0 ** -7 * 7 / 3 and got[3] == 4.0
