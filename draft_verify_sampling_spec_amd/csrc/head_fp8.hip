@@ -386,13 +386,238 @@ void launch_logits(const LogitArgs& a, hipStream_t s) {
                        band);
 }
 
+// bf16 logits of many rows and columns, 8-bit products: tiles of 256 x 256 by
+// four wavefronts, one a SIMD, of 128 x 128 each, so that a fragment read from
+// LDS serves four products (with eight wavefronts of 128 x 64 LDS is as busy as
+// the matrix cores). The accumulators are 256 registers, and the fragments are
+// held twice:
+//  - A stage (128 channels) has two phases, one half of its channels each. While
+//    a phase's 16 products run, the next phase's fragments are read; in the
+//    second the place in LDS that has been read is filled with the stage after
+//    the next. Products, reads and loads alternate in the order written here.
+//  - One barrier a stage, between its phases: every wave has read the stage
+//    whole, and the next one has arrived.
+// A workgroup goes through its tiles without a break: the next tile's first
+// stages are under way while one ends, and its outputs go straight from the
+// registers.
+// 2,560 rows x 151,936 columns x 2,560 channels: 930 us (logits_kernel's 256 x
+// 256 tiles: 1,005), 8,192 of each: 404 (450). Products alone take 67 % of the
+// loop's time at 1.9 GHz; 140 of the 930 us are the outputs' 778 MB, which all
+// workgroups write at the same time (788 without them; not waiting for a tile's
+// stores before the next one's second stage measured 921).
+struct Large {
+    static constexpr int T = 256, kWaves = 4, M = 4;        // tile, wavefronts, 32 x 32 tiles of a wave
+    static constexpr int kLoads = 2 * T / 8 / kWaves, kStageBytes = 2 * T * kBlock;
+};
+
+__global__ __launch_bounds__(256) void logits_large_kernel(LogitArgs a, int v_tiles, int band, int tiles) {
+    using C = Large;
+    __shared__ __attribute__((aligned(128))) unsigned char ring[2 * C::kStageBytes];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int vrow = (wave & 1) * 128, rrow = (wave >> 1) * 128;
+    const unsigned pitch = (unsigned)a.blocks * kBlock;
+
+    // Places as in logits_kernel; of the padded ones there may be none.
+    const int r_tiles = (a.R + C::T - 1) / C::T, v_per = (v_tiles + 7) / 8;
+    struct Place {
+        int v0, r0;
+    };
+    auto place = [&](int id) {
+        const int xcd = id & 7, at = id >> 3;
+        const int b0 = at / (v_per * band) * band, in_band = min(band, r_tiles - b0), rest = at - b0 * v_per;
+        return Place{(rest / in_band * 8 + xcd) * C::T, (b0 + rest % in_band) * C::T};
+    };
+    auto valid = [&](int id) {                              // the first from id on that is one
+        while (id < tiles && place(id).v0 >= a.V) id += gridDim.x;
+        return id;
+    };
+    int id = valid(blockIdx.x);
+    if (id >= tiles) return;
+
+    // What a tile reads. Rows past an operand read as zeros; of no tile none is read.
+    struct Source {
+        const uint8_t *w, *h;
+        unsigned wn, hn;
+    };
+    auto source = [&](const Place& p, bool some) {
+        return Source{a.w + (long long)p.v0 * pitch, a.h + (long long)p.r0 * pitch,
+                      some ? (unsigned)min(C::T, a.V - p.v0) * pitch : 0u,
+                      some ? (unsigned)min(C::T, a.R - p.r0) * pitch : 0u};
+    };
+    const unsigned lane_off = (lane >> 3) * pitch + (((lane & 7) ^ (lane >> 3)) * 16);
+    // Load n of a wave: rows 8 (n kWaves + wave) .. + 7 of the stage, the head's first.
+    auto fetch = [&](const Source& s, int n, int k, int slot) {
+        const int row = 8 * (n * C::kWaves + wave);
+        const bool head = n * C::kWaves * 8 < C::T;
+        const unsigned off = lane_off + (unsigned)(head ? row : row - C::T) * pitch + k * kBlock;
+        svdma::load16(head ? svdma::rsrc(s.w, s.wn) : svdma::rsrc(s.h, s.hn), off,
+                      ring + slot * C::kStageBytes + row * kBlock);
+    };
+    // Where a tile's scales start.
+    struct Scales {
+        unsigned w, h[C::M];
+    };
+    auto scales_of = [&](const Place& p) {
+        Scales s;
+        s.w = (unsigned)(min(p.v0 + vrow, a.V - 1) / kBlock * a.blocks);
+        #pragma unroll
+        for (int j = 0; j < C::M; ++j) s.h[j] = (unsigned)(min(p.r0 + rrow + 32 * j + (lane & 31), a.R - 1) * a.blocks);
+        return s;
+    };
+    Scales at;                                              // of the next stage
+    unsigned sw, sh[C::M];
+    auto load_scales = [&]() {
+        sw = a.ws[at.w];
+        #pragma unroll
+        for (int j = 0; j < C::M; ++j) sh[j] = a.hs[at.h[j]];
+    };
+
+    i32x8 wf[2][C::M], hf[2][C::M];
+    const unsigned lds_row = (lane & 31) * kBlock;
+    auto read = [&](int slot, int half, int n) {            // fragment n: rows', then columns'
+        const int c0 = 4 * half + 2 * (lane >> 5);
+        const int p0 = (c0 ^ (lane & 7)) * 16, p1 = ((c0 + 1) ^ (lane & 7)) * 16;
+        const unsigned char* row = ring + slot * C::kStageBytes + lds_row +
+                                   (n < C::M ? C::T + rrow + 32 * n : vrow + 32 * (n - C::M)) * kBlock;
+        const i32x8 f = __builtin_bit_cast(i32x8, __builtin_shufflevector(
+            *reinterpret_cast<const u32x4*>(row + p0), *reinterpret_cast<const u32x4*>(row + p1),
+            0, 1, 2, 3, 4, 5, 6, 7));
+        if (n < C::M) hf[half][n] = f;
+        else wf[half][n - C::M] = f;
+    };
+    f32x16 acc[C::M][C::M];
+    unsigned sw_now, sh_now[C::M];
+    // Waits for them here rather than behind a tile's stores.
+    auto use_scales = [&]() {
+        sw_now = sw;
+        asm volatile("" : "+v"(sw_now));
+        #pragma unroll
+        for (int j = 0; j < C::M; ++j) {
+            sh_now[j] = sh[j];
+            asm volatile("" : "+v"(sh_now[j]));
+        }
+    };
+    auto product = [&](int half, int n) {
+        const int i = n / C::M, j = n % C::M;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            wf[half][i], hf[half][j], acc[i][j], 0, 0, 0, (int)sw_now, 0, (int)sh_now[j]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    Place now = place(id);
+    Source from = source(now, true);
+    at = scales_of(now);
+    load_scales();
+    #pragma unroll
+    for (int n = 0; n < C::kLoads; ++n) fetch(from, n, 0, 0);
+    #pragma unroll
+    for (int n = 0; n < C::kLoads; ++n) fetch(from, n, 1, 1);
+    svdma::wait_vm<C::kLoads>();
+    svdma::ring_barrier();
+    #pragma unroll
+    for (int n = 0; n < 2 * C::M; ++n) read(0, 0, n);
+    use_scales();
+    int slot = 0;
+    for (;;) {
+        const int next = valid(id + gridDim.x);
+        const bool some = next < tiles;
+        const Place then = some ? place(next) : now;
+        const Source then_from = source(then, some);
+        const Scales then_at = scales_of(then);
+        #pragma unroll
+        for (int i = 0; i < C::M; ++i) {
+            #pragma unroll
+            for (int j = 0; j < C::M; ++j) acc[i][j] = f32x16{};
+        }
+        int k = 0;
+        do {
+            __builtin_amdgcn_sched_barrier(0);
+            #pragma unroll
+            for (int n = 0; n < C::M * C::M; ++n) {
+                product(0, n);
+                if (n < 2 * C::M) read(slot, 1, n);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // A branch here would make a second loop of the last stage, and copies
+            // of the accumulators between the two.
+            const bool last = k + 1 == a.blocks;
+            at.w = last ? then_at.w : at.w + 1;
+            #pragma unroll
+            for (int j = 0; j < C::M; ++j) at.h[j] = last ? then_at.h[j] : at.h[j] + 1;
+            load_scales();                                  // of the next stage
+            const bool wrap = k + 2 >= a.blocks;
+            const Source s = wrap ? then_from : from;
+            const int ks = wrap ? k + 2 - a.blocks : k + 2;
+            __builtin_amdgcn_sched_barrier(0);
+            // All but the scales has arrived. (Loads complete in order, so the
+            // scales outstanding means at most them and no stage's loads.)
+            svdma::wait_vm<C::M + 1>();
+            svdma::ring_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            #pragma unroll
+            for (int n = 0; n < C::M * C::M; ++n) {
+                product(1, n);
+                if (n < 2 * C::M) read(slot ^ 1, 0, n);
+                fetch(s, n, ks, slot);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            use_scales();
+            slot ^= 1;
+        } while (++k < a.blocks);
+        // A lane holds row lane % 32 of every 32 x 32 tile and columns 8 g + 4
+        // (lane / 32) .. + 3: swapping halves gives it eight in a row.
+        const int col0 = vrow + 8 * (lane >> 5), cols = a.V - now.v0;
+        const __amdgpu_buffer_rsrc_t dst = svdma::rsrc(
+            static_cast<const uint16_t*>(a.out) + (long long)now.r0 * a.V + now.v0,
+            ((unsigned)min(C::T, a.R - now.r0) * (unsigned)a.V - (unsigned)now.v0) * 2);
+        #pragma unroll
+        for (int j = 0; j < C::M; ++j) {
+            const unsigned off = ((unsigned)(rrow + 32 * j + (lane & 31)) * (unsigned)a.V + (unsigned)col0) * 2;
+            #pragma unroll
+            for (int i = 0; i < C::M; ++i) {
+                // Read one by one: the compiler would take them all over into
+                // ordinary registers, in the loop over stages.
+                asm volatile("" : "+a"(acc[i][j]));
+                __builtin_amdgcn_sched_barrier(0);
+                #pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const f32x16& v = acc[i][j];
+                    const float lo[4] = {v[8 * m], v[8 * m + 1], v[8 * m + 2], v[8 * m + 3]};
+                    const float hi[4] = {v[8 * m + 4], v[8 * m + 5], v[8 * m + 6], v[8 * m + 7]};
+                    const uint2 x = pack4(lo, uint16_t{}), y = pack4(hi, uint16_t{});
+                    const auto p = __builtin_amdgcn_permlane32_swap(x.x, y.x, false, false);
+                    const auto q = __builtin_amdgcn_permlane32_swap(x.y, y.y, false, false);
+                    const int c = 32 * i + 16 * m;
+                    // Past the last row or column: past the end of the buffer, dropped.
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{p[0], q[0], p[1], q[1]}, dst,
+                                                           col0 + c < cols ? (int)(off + 2 * c) : -1, 0, 0);
+                }
+            }
+        }
+        if (!some) break;
+        id = next;
+        now = then;
+        from = then_from;
+    }
+    svdma::wait_vm<0>();            // no load into LDS outlives the workgroup
+}
+
+void launch_large(const LogitArgs& a, hipStream_t s) {
+    const int v_tiles = (a.V + Large::T - 1) / Large::T, r_tiles = (a.R + Large::T - 1) / Large::T;
+    const int bands = (r_tiles + 7) / 8, band = (r_tiles + bands - 1) / bands;
+    const int tiles = (v_tiles + 7) / 8 * 8 * r_tiles;
+    hipLaunchKernelGGL(logits_large_kernel, dim3((unsigned)(tiles < 256 ? tiles : 256)), dim3(256), 0, s, a,
+                       v_tiles, band, tiles);
+}
+
 // Tiles by the number of rows and columns. Up to 64 rows the head's bytes
 // decide and the tile is as narrow as its rows. Above, the tile whose rounds of
 // workgroups take least: a round of 256 x 256 tiles (one workgroup per CU) as
-// the unit, one of 128 x 128 tiles (two) measured 0.62 of it and one of 64 x 64
-// tiles (three) 0.375, for an eighth more and twice the time per product. (20,000
-// columns x 5,120 channels, bf16: 300 rows take 62, 47, 71 us with them, 700
-// rows 68, 83, 136; 2,560 columns x 4,096, 1,024 rows: 50, 31, 27.)
+// the unit, one of 128 x 128 tiles (two) measured 0.62 to 0.7 of it and one of 64
+// x 64 tiles (three) 0.375 to 0.4. (20,000 columns x 5,120 channels, bf16: 300
+// rows take 53, 44, 71 us with them, 700 rows 63, 81, 136; 151,936 columns x
+// 2,560, 160 rows 126, 139, -; 2,560 columns x 4,096, 1,024 rows 44, 30, 27.)
 template <bool kF8, typename O>
 void launch_rows(const LogitArgs& a, hipStream_t s) {
     if (a.R <= 32) return launch_logits<Cfg<64, 32, 2, 1, 3, kF8, O>>(a, s);
@@ -406,7 +631,11 @@ void launch_rows(const LogitArgs& a, hipStream_t s) {
         return (double)(((a.V + tile - 1) / tile * ((a.R + tile - 1) / tile) + held - 1) / held);
     };
     const double large = rounds(256, 256), middle = 0.62 * rounds(128, 512), small = 0.375 * rounds(64, 768);
-    if (large <= middle && large <= small) launch_logits<Cfg<256, 256, 2, 4, 2, kF8, O>>(a, s);
+    if (large <= middle && large <= small) {
+        // Its outputs are 16-byte pieces, its ring takes two stages ahead.
+        if (kF8 && a.blocks > 1 && a.V % 8 == 0 && aligned(a.out, 16)) launch_large(a, s);
+        else launch_logits<Cfg<256, 256, 2, 4, 2, kF8, O>>(a, s);
+    }
     else if (middle <= small) launch_logits<Cfg<128, 128, 2, 2, 2, kF8, O>>(a, s);
     else launch_logits<Cfg<64, 64, 2, 2, 3, kF8, O>>(a, s);
 }

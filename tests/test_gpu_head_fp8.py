@@ -261,3 +261,33 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+@pytest.mark.parametrize("R,H,V,offset", [
+    (500, 256, 32000, 0), (512, 384, 31992, 0), (520, 640, 64000, 0),     # whole 16-byte pieces
+    (500, 136, 31999, 0), (500, 256, 32000, 1),                           # odd rows, an odd start
+    (500, 128, 32000, 0),                                                 # one block of channels
+    (700, 264, 60008, 0),                                                 # several tiles a workgroup
+    (2100, 256, 20016, 0),                                                # two bands of rows
+])
+def test_logits_in_large_tiles(R, H, V, offset):
+    """bf16 logits where 256 x 256 tiles are taken, every one against fp64
+    products; what lies around them keeps its values."""
+    _log(f"[logits] large R={R} H={H} V={V} offset={offset}")
+    g = torch.Generator(device=DEV).manual_seed(R + V)
+    h = torch.randn(R, H, generator=g, device=DEV)
+    w = torch.randn(V, H, generator=g, device=DEV) * (3.0 / H ** 0.5)
+    hc, hs = head_quantize(h, 1)
+    wc, ws = head_quantize(w, 128)
+    around = torch.full((offset + R * V + 64,), 77.0, dtype=torch.bfloat16, device=DEV)
+    out = around[offset:offset + R * V].view(R, V)
+    head_logits(hc, hs, wc, ws, out=out)
+    a = torch.tensor(lb.head_values(hc.double().cpu().numpy(), _scales(hs), 1)).to(DEV)
+    b = torch.tensor(lb.head_values(wc.double().cpu().numpy(), _scales(ws), 128)).to(DEV).t().contiguous()
+    ref, S = a @ b, a.abs() @ b.abs()
+    tol = (4 * math.sqrt(a.shape[1]) * 2.0 ** -24 + 2.0 ** -15) * S + 1e-30 \
+        + 2.0 ** -8 * (1 + 2.0 ** -7) * ref.abs()
+    err = (out.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    assert bool((around[:offset] == 77.0).all()) and bool((around[offset + R * V:] == 77.0).all())
+    assert torch.equal(head_logits(hc, hs, wc, ws, out=torch.empty_like(out)), out) or offset
