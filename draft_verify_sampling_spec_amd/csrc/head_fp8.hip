@@ -146,8 +146,9 @@ struct LogitArgs {
 };
 
 // The product: workgroups hold tiles of TV vocabulary columns x TR rows, the
-// operands' codes streamed through an LDS ring of kStages blocks of 128
-// channels by buffer-to-LDS loads. A row's 128 bytes are eight chunks of 16;
+// operands' codes streamed through an LDS ring of two blocks of 128 channels by
+// buffer-to-LDS loads (with three blocks fewer workgroups fit a CU: one row of
+// 151,936 x 2,560 took 78 us against 68, 48 rows 100 against 92). A row's 128 bytes are eight chunks of 16;
 // chunk c of row i lies at position c ^ (i & 7), so that the eight lanes that
 // read one chunk column at a time touch all banks (the loads choose their
 // global chunk accordingly; LDS itself is filled linearly).
@@ -158,16 +159,16 @@ struct LogitArgs {
 // keep a sum of products only to about 2^-17 of its terms (relative error
 // 1.4e-5 of a row's norm, measured at 128, 2,560 and 10,240 channels): under a
 // two-hundredth of a bf16 rounding, but two hundred fp32 ones.
-template <int TV_, int TR_, int WV_, int WR_, int kStages_, bool kF8_, typename O_>
+template <int TV_, int TR_, int WV_, int WR_, bool kF8_, typename O_>
 struct Cfg {
-    static constexpr int TV = TV_, TR = TR_, WV = WV_, WR = WR_, kStages = kStages_;
+    static constexpr int TV = TV_, TR = TR_, WV = WV_, WR = WR_;
     static constexpr bool kF8 = kF8_;
     using O = O_;
     static constexpr int kWaves = WV * WR, kThreads = 64 * kWaves;
     static constexpr int MV = TV / WV / 32, MR = TR / WR / 32;    // 32 x 32 tiles of a wave
     static constexpr int kLoads = (TV + TR) / 8 / kWaves;         // buffer loads per wave and stage
     static constexpr int kStageBytes = (TV + TR) * kBlock;
-    static constexpr int kRing = kStages * kStageBytes;
+    static constexpr int kRing = 2 * kStageBytes;
     static constexpr int kRowBytes = TV * (int)sizeof(O);
     // Rows that the ring holds of the finished tile.
     static constexpr int kPass = kRing / kRowBytes < TR ? kRing / kRowBytes / 64 * 64 : TR;
@@ -220,7 +221,7 @@ __global__ __launch_bounds__(C::kThreads) void logits_kernel(LogitArgs a, int v_
     // head's rows first. Rows past the operand read as zeros.
     const unsigned lane_off = (lane >> 3) * pitch + (((lane & 7) ^ (lane >> 3)) * 16);
     auto fetch = [&](int k) {
-        unsigned char* base = ring + (k % C::kStages) * C::kStageBytes;
+        unsigned char* base = ring + (k & 1) * C::kStageBytes;
         #pragma unroll
         for (int i = 0; i < C::kLoads; ++i) {
             const int row = 8 * (i * C::kWaves + wave);
@@ -243,22 +244,13 @@ __global__ __launch_bounds__(C::kThreads) void logits_kernel(LogitArgs a, int v_
     unsigned sw = wsp[0], sh[C::MR];
     #pragma unroll
     for (int j = 0; j < C::MR; ++j) sh[j] = hsp[j][0];
-    #pragma unroll
-    for (int s = 0; s < C::kStages - 1; ++s) {
-        if (s < a.blocks) fetch(s);
-    }
+    fetch(0);
     const unsigned lds_row = (lane & 31) * kBlock;
     for (int k = 0; k < a.blocks; ++k) {
-        // Stage k has arrived when at most the loads of the stages after it
-        // are outstanding (the scales' loads only make this stricter).
-        if (k + C::kStages - 2 < a.blocks) {
-            svdma::wait_vm<(C::kStages - 2) * C::kLoads>();
-        } else {
-            svdma::wait_vm<0>();
-        }
+        svdma::wait_vm<0>();          // stage k has arrived
         svdma::ring_barrier();
         // Everyone has read stage k - 1: its place is free.
-        if (k + C::kStages - 1 < a.blocks) fetch(k + C::kStages - 1);
+        if (k + 1 < a.blocks) fetch(k + 1);
         const unsigned sw_now = sw;
         unsigned sh_now[C::MR];
         #pragma unroll
@@ -268,9 +260,9 @@ __global__ __launch_bounds__(C::kThreads) void logits_kernel(LogitArgs a, int v_
             #pragma unroll
             for (int j = 0; j < C::MR; ++j) sh[j] = hsp[j][k + 1];
         }
-        const unsigned char* wbase = ring + (k % C::kStages) * C::kStageBytes + vrow * kBlock + lds_row;
+        const unsigned char* wbase = ring + (k & 1) * C::kStageBytes + vrow * kBlock + lds_row;
         const unsigned char* hbase =
-            ring + (k % C::kStages) * C::kStageBytes + (C::TV + rrow) * kBlock + lds_row;
+            ring + (k & 1) * C::kStageBytes + (C::TV + rrow) * kBlock + lds_row;
         #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int c0 = 4 * half + 2 * (lane >> 5);
@@ -620,12 +612,12 @@ void launch_large(const LogitArgs& a, hipStream_t s) {
 // 2,560, 160 rows 126, 139, -; 2,560 columns x 4,096, 1,024 rows 44, 30, 27.)
 template <bool kF8, typename O>
 void launch_rows(const LogitArgs& a, hipStream_t s) {
-    if (a.R <= 32) return launch_logits<Cfg<64, 32, 2, 1, 3, kF8, O>>(a, s);
+    if (a.R <= 32) return launch_logits<Cfg<64, 32, 2, 1, kF8, O>>(a, s);
     if (a.R <= 64) {
-        // Twice the columns once every resident workgroup has some: 105 against
-        // 100 us for 48 rows of fp32 logits, but 30 against 31 at 20,000 columns.
-        if (a.V >= 128 * 512) return launch_logits<Cfg<128, 64, 4, 2, 3, kF8, O>>(a, s);
-        return launch_logits<Cfg<64, 64, 2, 2, 3, kF8, O>>(a, s);
+        // Twice the columns once every CU has several such tiles (48 rows of fp32
+        // logits, 151,936 columns: 92 against 97 us; 20,000 x 5,120: 29 against 27).
+        if (a.V >= 128 * 512) return launch_logits<Cfg<128, 64, 4, 1, kF8, O>>(a, s);
+        return launch_logits<Cfg<64, 64, 2, 2, kF8, O>>(a, s);
     }
     auto rounds = [&](long long tile, long long held) {
         return (double)(((a.V + tile - 1) / tile * ((a.R + tile - 1) / tile) + held - 1) / held);
@@ -634,10 +626,10 @@ void launch_rows(const LogitArgs& a, hipStream_t s) {
     if (large <= middle && large <= small) {
         // Its outputs are 16-byte pieces, its ring takes two stages ahead.
         if (kF8 && a.blocks > 1 && a.V % 8 == 0 && aligned(a.out, 16)) launch_large(a, s);
-        else launch_logits<Cfg<256, 256, 2, 4, 2, kF8, O>>(a, s);
+        else launch_logits<Cfg<256, 256, 2, 4, kF8, O>>(a, s);
     }
-    else if (middle <= small) launch_logits<Cfg<128, 128, 2, 2, 2, kF8, O>>(a, s);
-    else launch_logits<Cfg<64, 64, 2, 2, 3, kF8, O>>(a, s);
+    else if (middle <= small) launch_logits<Cfg<128, 128, 2, 2, kF8, O>>(a, s);
+    else launch_logits<Cfg<64, 64, 2, 2, kF8, O>>(a, s);
 }
 
 }  // namespace
