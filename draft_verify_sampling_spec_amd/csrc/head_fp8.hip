@@ -606,10 +606,11 @@ void launch_large(const LogitArgs& a, hipStream_t s) {
 // Tiles by the number of rows and columns. Up to 64 rows the head's bytes
 // decide and the tile is as narrow as its rows. Above, the tile whose rounds of
 // workgroups take least: a round of 256 x 256 tiles (one workgroup per CU) as
-// the unit, one of 128 x 128 tiles (two) measured 0.62 to 0.7 of it and one of 64
-// x 64 tiles (three) 0.375 to 0.4. (20,000 columns x 5,120 channels, bf16: 300
+// the unit, one of 128 x 128 tiles (two) measured 0.62 to 0.7 of it and three of
+// 64 x 64 tiles per CU 0.375 to 0.4. (20,000 columns x 5,120 channels, bf16: 300
 // rows take 53, 44, 71 us with them, 700 rows 63, 81, 136; 151,936 columns x
-// 2,560, 160 rows 126, 139, -; 2,560 columns x 4,096, 1,024 rows 44, 30, 27.)
+// 2,560, 160 rows 126, 139, -; 2,560 columns x 4,096, 1,024 rows 44, 31, 28. The
+// rule's choice was the least, or within 4 % of it, at 11 sizes in either type.)
 template <bool kF8, typename O>
 void launch_rows(const LogitArgs& a, hipStream_t s) {
     if (a.R <= 32) return launch_logits<Cfg<64, 32, 2, 1, kF8, O>>(a, s);
@@ -624,12 +625,14 @@ void launch_rows(const LogitArgs& a, hipStream_t s) {
     };
     const double large = rounds(256, 256), middle = 0.62 * rounds(128, 512), small = 0.375 * rounds(64, 768);
     if (large <= middle && large <= small) {
-        // Its outputs are 16-byte pieces, its ring takes two stages ahead.
+        // Its outputs are 16-byte pieces, and it starts with two stages.
         if (kF8 && a.blocks > 1 && a.V % 8 == 0 && aligned(a.out, 16)) launch_large(a, s);
         else launch_logits<Cfg<256, 256, 2, 4, kF8, O>>(a, s);
+    } else if (middle <= small) {
+        launch_logits<Cfg<128, 128, 2, 2, kF8, O>>(a, s);
+    } else {
+        launch_logits<Cfg<64, 64, 2, 2, kF8, O>>(a, s);
     }
-    else if (middle <= small) launch_logits<Cfg<128, 128, 2, 2, kF8, O>>(a, s);
-    else launch_logits<Cfg<64, 64, 2, 2, kF8, O>>(a, s);
 }
 
 }  // namespace
