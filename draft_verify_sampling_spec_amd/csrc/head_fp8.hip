@@ -615,8 +615,9 @@ template <bool kF8, typename O>
 void launch_rows(const LogitArgs& a, hipStream_t s) {
     if (a.R <= 32) return launch_logits<Cfg<64, 32, 2, 1, kF8, O>>(a, s);
     if (a.R <= 64) {
-        // Twice the columns once every CU has several such tiles (48 rows of fp32
-        // logits, 151,936 columns: 92 against 97 us; 20,000 x 5,120: 29 against 27).
+        // Twice the columns once every CU has two such tiles (48 rows of fp32
+        // logits under 151,936 columns: 97 against 104 us, 100,000: 55 and 54,
+        // 65,536: 30 and 30, 40,000: 26 against 23).
         if (a.V >= 128 * 512) return launch_logits<Cfg<128, 64, 4, 1, kF8, O>>(a, s);
         return launch_logits<Cfg<64, 64, 2, 2, kF8, O>>(a, s);
     }
