@@ -291,3 +291,29 @@ def test_logits_in_large_tiles(R, H, V, offset):
     assert bool((err <= tol).all()), float((err / tol).max())
     assert bool((around[:offset] == 77.0).all()) and bool((around[offset + R * V:] == 77.0).all())
     assert torch.equal(head_logits(hc, hs, wc, ws, out=torch.empty_like(out)), out) or offset
+
+
+def test_large_tiles_on_two_streams_and_in_a_replayed_graph():
+    g = torch.Generator(device=DEV).manual_seed(13)
+    h = [head_quantize(torch.randn(600, 384, generator=g, device=DEV).bfloat16()) for _ in range(2)]
+    wq = head_quantize(torch.randn(60000, 384, generator=g, device=DEV).bfloat16(), 128)
+    want = [head_logits(*x, *wq, dtype=torch.bfloat16) for x in h]
+    out = [torch.zeros_like(x) for x in want]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for x, o, s in zip(h, out, streams):
+            head_logits(*x, *wq, out=o, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, x) for o, x in zip(out, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for x, o in zip(h, out):
+            head_logits(*x, *wq, out=o)
+    for _ in range(4):
+        for o in out:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, x) for o, x in zip(out, want))
+        assert torch.equal(head_logits(*h[0], *wq, dtype=torch.bfloat16), want[0])
