@@ -150,12 +150,12 @@ struct LogitArgs {
 
 // The product, bound by the head's bytes up to about 64 rows (48 rows of fp32
 // logits under 151,936 x 2,560: 93 us, 4.5 TB/s) and by LDS and the matrix cores
-// above: workgroups hold tiles of TV vocabulary columns x TR rows, the
-// operands' codes streamed through an LDS ring of two blocks of 128 channels by
-// buffer-to-LDS loads (with three blocks fewer workgroups fit a CU: one row of
-// 151,936 x 2,560 took 78 us against 68, 48 rows 100 against 92). A row's 128 bytes are eight chunks of 16;
-// chunk c of row i lies at position c ^ (i & 7), so that the eight lanes that
-// read one chunk column at a time touch all banks (the loads choose their
+// above: workgroups hold tiles of TV vocabulary columns x TR rows, the operands'
+// codes streamed through an LDS ring of two blocks of 128 channels by
+// buffer-to-LDS loads (with three blocks fewer workgroups fit a CU: one row took
+// 78 us against 68, 48 rows 100 against 92). A row's 128 bytes are eight chunks
+// of 16; chunk c of row i lies at position c ^ (i & 7), so that the eight lanes
+// that read one chunk column at a time touch all banks (the loads choose their
 // global chunk accordingly; LDS itself is filled linearly).
 //
 // kF8: 8-bit matrix instructions with both scales as their operands, for bf16
