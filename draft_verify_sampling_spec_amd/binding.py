@@ -735,6 +735,8 @@ class BlockCache:
         self._pool_ptr = _need(pool, "pool", torch.uint8, shape, self._index)
         self.pool = pool
         self._workspace_bytes = {}          # by attention shape
+        # For calls whose plan has no parts, which leave their 256 bytes alone.
+        self._no_parts = torch.empty(256, dtype=torch.uint8, device=device)
 
     def _table(self, page_table, B):
         shape = page_table.shape
@@ -846,7 +848,8 @@ class BlockCache:
             self._workspace_bytes[key] = nbytes
         if out is None:
             out = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        workspace = self._no_parts if nbytes == 256 else torch.empty(
+            nbytes, dtype=torch.uint8, device=self.device)
         rc = load().spec_verify_attention(
             queries.data_ptr(), stride, self._pool_ptr, table,
             _need(ctx_lens, "ctx_lens", torch.int32, (B,), index),
@@ -881,9 +884,10 @@ def head_quantize(x: torch.Tensor, block_rows: int = 1, out=None, stream=None):
     rows, H = x.shape
     blocks = -(-H // 128)
     codes, scales = (rows, blocks * 128), (-(-rows // block_rows), blocks)
-    if out is None:
-        out = (torch.empty(codes, dtype=torch.float8_e4m3fn, device=x.device),
-               torch.empty(scales, dtype=torch.float8_e8m0fnu, device=x.device))
+    if out is None:                     # empty_strided costs the host less than empty
+        device = x.device
+        out = (torch.empty_strided(codes, (blocks * 128, 1), dtype=torch.float8_e4m3fn, device=device),
+               torch.empty_strided(scales, (blocks, 1), dtype=torch.float8_e8m0fnu, device=device))
     rc = load().spec_head_quantize(
         x.data_ptr(), code, rows, H, block_rows,
         _need(out[0], "out codes", torch.float8_e4m3fn, codes, index),
@@ -906,11 +910,12 @@ def head_logits(h_codes: torch.Tensor, h_scales: torch.Tensor, w_codes: torch.Te
     if _current_device() != index:
         with torch.cuda.device(index):
             return head_logits(h_codes, h_scales, w_codes, w_scales, dtype, out)
-    if h_codes.dim() != 2 or w_codes.dim() != 2 or h_codes.shape[1] != w_codes.shape[1] \
-            or h_codes.shape[1] % 128 != 0 or h_codes.shape[1] == 0:
+    h_shape, w_shape = h_codes.shape, w_codes.shape
+    if len(h_shape) != 2 or len(w_shape) != 2 or h_shape[1] != w_shape[1] \
+            or h_shape[1] % 128 != 0 or h_shape[1] == 0:
         raise ValueError("h_codes [R, Hp] and w_codes [V, Hp] must share Hp, a multiple of 128")
-    R, H = h_codes.shape
-    V = w_codes.shape[0]
+    R, H = h_shape
+    V = w_shape[0]
     e4m3, e8m0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
     if out is not None:
         dtype = out.dtype
@@ -918,11 +923,11 @@ def head_logits(h_codes: torch.Tensor, h_scales: torch.Tensor, w_codes: torch.Te
     if code is None:
         raise ValueError(f"logits are float32 or bfloat16, not {dtype}")
     if out is None:
-        out = torch.empty((R, V), dtype=dtype, device=h_codes.device)
+        out = torch.empty_strided((R, V), (V, 1), dtype=dtype, device=h_codes.device)
     rc = load().spec_head_logits(
-        _need(h_codes, "h_codes", e4m3, (R, H), index),
+        _need(h_codes, "h_codes", e4m3, h_shape, index),
         _need(h_scales, "h_scales", e8m0, (R, H // 128), index),
-        _need(w_codes, "w_codes", e4m3, (V, H), index),
+        _need(w_codes, "w_codes", e4m3, w_shape, index),
         _need(w_scales, "w_scales", e8m0, (-(-V // 128), H // 128), index), R, H, V, code,
         _need(out, "out", dtype, (R, V), index), _raw_stream(index))
     if rc != SV_OK:

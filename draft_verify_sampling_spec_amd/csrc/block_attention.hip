@@ -40,7 +40,7 @@ typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
 
-constexpr int kWaves = 4;
+constexpr int kFew = 4, kMany = 8;      // wavefronts of a workgroup (see plan_of)
 constexpr float kNegInf = -INFINITY;
 
 // How the work is cut. A unit is a request's kv head and block of 16 kMT
@@ -185,7 +185,7 @@ struct State {
     int pos[kAct];       // the row's position; -1 past the block
 };
 
-template <int D, int kMT>
+template <int D, int kMT, int kWaves>
 struct Lds {
     static constexpr int kPieces = kMT * Tile<D>::kPlanes * (D == 64 ? 4 : 8) / 4;  // float4 per lane and component
     union {
@@ -200,9 +200,9 @@ struct Lds {
 };
 
 // One tile. kMasked: some row does not see some token of it.
-template <int D, int kMT, int kAct, bool kMasked>
+template <int D, int kMT, int kWaves, int kAct, bool kMasked>
 __device__ __forceinline__ void tile_step(State<D, kAct>& st, const Frag<D>& f,
-                                          const Lds<D, kMT>& sh, const AttendArgs& a, int lane,
+                                          const Lds<D, kMT, kWaves>& sh, const AttendArgs& a, int lane,
                                           int tok0, int last, const uint8_t* tile) {
     using L = Tile<D>;
     using S = State<D, kAct>;
@@ -369,7 +369,7 @@ __device__ __forceinline__ void tile_step(State<D, kAct>& st, const Frag<D>& f,
 // flight while one is worked on. (Two tiles ahead, or a ring in LDS filled by
 // buffer-to-LDS loads, measured slower: 174-186 against 153 us for 128
 // requests over 1,024..8,192 tokens.)
-template <int D, int kMT>
+template <int D, int kMT, int kWaves>
 struct Stream {
     using L = Tile<D>;
     Frag<D> f[2];
@@ -418,23 +418,23 @@ struct Stream {
         return count > 0 ? fetch<0>(a, wk, 0, lane) : a.cache;
     }
     template <int kAct>
-    __device__ __forceinline__ void run(State<D, kAct>& st, const Lds<D, kMT>& sh,
+    __device__ __forceinline__ void run(State<D, kAct>& st, const Lds<D, kMT, kWaves>& sh,
                                         const AttendArgs& a, const Work& wk, const Block& blk,
                                         const uint8_t* tile, int lane) {
         int n = 0;
         for (; wave + n * kWaves < edges; ++n) {
             const uint8_t* next = tile;
             if (n + 1 < count) next = fetch<1>(a, wk, n + 1, lane);
-            tile_step<D, kMT, kAct, true>(st, f[0], sh, a, lane, tile_of(n) * kTile, blk.ctx + blk.len - 1, tile);
+            tile_step<D, kMT, kWaves, kAct, true>(st, f[0], sh, a, lane, tile_of(n) * kTile, blk.ctx + blk.len - 1, tile);
             f[0] = f[1];
             tile = next;
         }
         while (n < count) {
             if (n + 1 < count) fetch<1>(a, wk, n + 1, lane);
-            tile_step<D, kMT, kAct, false>(st, f[0], sh, a, lane, 0, 0, nullptr);
+            tile_step<D, kMT, kWaves, kAct, false>(st, f[0], sh, a, lane, 0, 0, nullptr);
             if (n + 1 < count) {
                 if (n + 2 < count) fetch<0>(a, wk, n + 2, lane);
-                tile_step<D, kMT, kAct, false>(st, f[1], sh, a, lane, 0, 0, nullptr);
+                tile_step<D, kMT, kWaves, kAct, false>(st, f[1], sh, a, lane, 0, 0, nullptr);
             }
             n += 2;
         }
@@ -476,9 +476,9 @@ constexpr int occupancy() {
 
 // One run of tiles, from the queries to the output or a partial result, for a
 // row block of which kAct row tiles hold rows.
-template <int D, int kMT, int kAct>
+template <int D, int kMT, int kWaves, int kAct>
 __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any, const Block& its,
-                                           Lds<D, kMT>& sh, int lane, int wave) {
+                                           Lds<D, kMT, kWaves>& sh, int lane, int wave) {
     // The same for the whole wavefront, and to be kept in scalar registers.
     const Work wk{scalar(any.b), scalar(any.h), scalar(any.rb), scalar(any.t0), scalar(any.t1), scalar(any.slot)};
     const Block blk = scalar(its);
@@ -506,7 +506,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any,
             if (a.negate) own[k] ^= u32x4{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
         }
     }
-    Stream<D, kMT> stream;
+    Stream<D, kMT, kWaves> stream;
     const uint8_t* tile = stream.start(a, wk, blk, lane, wave);
     S st;
     #pragma unroll
@@ -575,14 +575,15 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any,
         svdma::ring_barrier();
         const int k = wave & 1, m = 4 * quad + 2 * round + k;     // the lane's pieces of channels
         #pragma unroll
-        for (int j = 0; j < (kPieces + 1) / 2; ++j) {
-            const int i = 2 * j + (wave >> 1);
+        for (int j = 0; j < (kPieces + kWaves / 2 - 1) / (kWaves / 2); ++j) {
+            const int i = kWaves / 2 * j + (wave >> 1);
             if (i >= kPieces) continue;
             const int mt = i / (kPieces / kAct), p = i / (kChans / 4) % kPlanes, c = i % (kChans / 4) * 4;
             const int in = mt * 16 + x, row = wk.rb * (16 * kMT) + in;
             if (row >= rows) continue;
-            const f32x4 v = (sh.o[0][k][i][lane] + sh.o[1][k][i][lane]) +
-                            (sh.o[2][k][i][lane] + sh.o[3][k][i][lane]);
+            f32x4 v = sh.o[0][k][i][lane] + sh.o[1][k][i][lane];
+            #pragma unroll
+            for (int w = 2; w < kWaves; w += 2) v += sh.o[w][k][i][lane] + sh.o[w + 1][k][i][lane];
             const int ch = p * 128 + m * kChans + c;
             // mt is the same for the whole wave but no constant.
             float sum = total[0], ref = top[0];
@@ -611,15 +612,15 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any,
 __device__ __forceinline__ Block plain_block(const AttendArgs& a, int b) {
     return block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, nullptr, false);
 }
-template <int D, int kMT>
-__global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(AttendArgs a) {
-    __shared__ Lds<D, kMT> sh;
+template <int D, int kMT, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_kernel(AttendArgs a) {
+    __shared__ Lds<D, kMT, kWaves> sh;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = scalar(tid >> 6);
     const int heads = a.pages.heads, g = blockIdx.x;
 
     if (g == 0) {                     // report bad budgets and lengths, once per call
-        for (int b = tid; b < a.B; b += 256) {
+        for (int b = tid; b < a.B; b += 64 * kWaves) {
             block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, a.status, true);
         }
     }
@@ -629,13 +630,13 @@ __global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(Atte
     unsigned long long at = 0, lo = 0, hi = 0, share = 1;
     bool aligned = false;
     Block blk{0, 0};
-    if (a.direct) {
+    if (kWaves != kFew || a.direct) {
         rb = scalar(g % a.row_blocks);
         h = scalar(g / a.row_blocks % heads);
         const int mine = scalar(g / a.row_blocks / heads);
         blk = scalar(plain_block(a, mine));
         if (rb < Share<kMT>(a, blk).blocks) b = mine;
-    } else {
+    } else if constexpr (kWaves == kFew) {
         const int per = (a.B + 255) / 256;
         const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
         if (tid == 0) sh.found = -1;
@@ -767,10 +768,10 @@ __global__ __launch_bounds__(256, (occupancy<D, kMT>())) void attend_kernel(Atte
         if (i0 < i1) {
             const Work wk{b, h, rb, s.span.first + scalar(i0), s.span.first + scalar(i1), slot};
             const int act = scalar(s.act(rb));
-            if (kMT >= 4 && act == 4) attend_run<D, kMT, (kMT < 4 ? 1 : 4)>(a, wk, blk, sh, lane, wave);
-            else if (kMT >= 3 && act == 3) attend_run<D, kMT, (kMT < 3 ? 1 : 3)>(a, wk, blk, sh, lane, wave);
-            else if (kMT >= 2 && act == 2) attend_run<D, kMT, (kMT < 2 ? 1 : 2)>(a, wk, blk, sh, lane, wave);
-            else attend_run<D, kMT, 1>(a, wk, blk, sh, lane, wave);
+            if (kMT >= 4 && act == 4) attend_run<D, kMT, kWaves, (kMT < 4 ? 1 : 4)>(a, wk, blk, sh, lane, wave);
+            else if (kMT >= 3 && act == 3) attend_run<D, kMT, kWaves, (kMT < 3 ? 1 : 3)>(a, wk, blk, sh, lane, wave);
+            else if (kMT >= 2 && act == 2) attend_run<D, kMT, kWaves, (kMT < 2 ? 1 : 2)>(a, wk, blk, sh, lane, wave);
+            else attend_run<D, kMT, kWaves, 1>(a, wk, blk, sh, lane, wave);
         }
         if (a.direct || aligned) break;
         // On to the next unit: heads, row blocks, requests.
@@ -822,7 +823,7 @@ template <int D, int kMT>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     constexpr int kSide = 256 / D, kLanes = 64 / kSide;     // parts side by side, lanes of each
     constexpr int kDeep = 8;
-    __shared__ Joined sh[kWaves][64];
+    __shared__ Joined sh[kFew][64];
     const int lane = threadIdx.x & 63, wave = scalar((int)threadIdx.x >> 6);
     const int side = lane / kLanes, ch = lane % kLanes * 4;
     const int g = blockIdx.x / kMT, in0 = blockIdx.x % kMT * 16;
@@ -835,8 +836,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
         const int rb = both[slot].x % a.row_blocks, h = both[slot].x / a.row_blocks % a.pages.heads;
         const int b = both[slot].x / a.row_blocks / a.pages.heads;
         const int rows = plain_block(a, b).len * a.group - rb * (16 * kMT);
-        const int by = many ? kWaves * kSide : kSide;
-        for (int i = many ? s0 : s0 * kWaves + wave; i < 16 && in0 + i < rows; i += many ? 16 : min(n, 4) * kWaves) {
+        const int by = many ? kFew * kSide : kSide;
+        for (int i = many ? s0 : s0 * kFew + wave; i < 16 && in0 + i < rows; i += many ? 16 : min(n, 4) * kFew) {
             const int in = in0 + i;
             Joined j{kNegInf, 0.0f, {0, 0, 0, 0}};
             for (int s = (many ? wave * kSide : 0) + side; s < n; s += kDeep * by) {
@@ -866,7 +867,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
                 __syncthreads();
                 j = sh[0][lane];
                 #pragma unroll
-                for (int w = 1; w < kWaves; ++w) j.add(sh[w][lane].ref, sh[w][lane].sum, sh[w][lane].acc);
+                for (int w = 1; w < kFew; ++w) j.add(sh[w][lane].ref, sh[w][lane].sum, sh[w][lane].acc);
             }
             if (side == 0 && (!many || wave == 0)) {
                 const int row = rb * (16 * kMT) + in;
@@ -887,6 +888,7 @@ struct Plan {
     int groups;         // workgroups resident at once (and no more than there is work for)
     int grid, slots;
     bool direct;
+    int waves;          // of a workgroup
 };
 
 template <int D>
@@ -910,6 +912,12 @@ Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_p
     p.groups = (int)std::min<long long>(held, most);
     p.direct = tiles <= kDirectTiles || (units >= held && tiles <= 2 * kDirectTiles) ||
                units >= (long long)kDirectUnits * held;
+    // Twice the wavefronts on a unit's tiles where a CU has no more than one unit
+    // of one row tile: what is left is latency. (8 requests of up to 577 tokens, 8
+    // kv heads of 128: 7.0 against 7.6 us, of 900 tokens 8.2 against 9.4, of 256
+    // channels 11.3 against 14.4; 32 requests 9.4 against 10.8, but 64, two units
+    // a CU, 15.9 against 15.2.)
+    p.waves = p.direct && p.mt == 1 && units <= 256 ? kMany : kFew;
     p.grid = (int)(p.direct ? units : p.groups + std::min<long long>(units, held));
     p.slots = p.direct ? 0 : std::max(2 * p.groups, p.grid);
     return p;
@@ -927,7 +935,13 @@ bool shape_ok(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_
 
 template <int D, int kMT>
 void launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
-    hipLaunchKernelGGL((attend_kernel<D, kMT>), dim3((unsigned)p.grid), dim3(256), 0, s, a);
+    if constexpr (kMT == 1) {
+        if (p.waves == kMany) {
+            hipLaunchKernelGGL((attend_kernel<D, kMT, kMany>), dim3((unsigned)p.grid), dim3(64 * kMany), 0, s, a);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((attend_kernel<D, kMT, kFew>), dim3((unsigned)p.grid), dim3(64 * kFew), 0, s, a);
     if (!p.direct) {
         const unsigned blocks = (unsigned)(p.grid * kMT);
         hipLaunchKernelGGL((attend_join_kernel<D, kMT>), dim3(blocks), dim3(256), 0, s, a);

@@ -463,3 +463,20 @@ def test_scales_near_the_largest():
     q[0, 3, 0, 0] = 2.0 ** -100
     got = c.attend(q, table, _i32([0]), scale=3.0e38)[0, :, 0, 0].tolist()
     assert got[0] == 1.0 and got[1] == 1.5 and abs(got[2] - 7 / 3) <= 2.0 ** -7 * 7 / 3 and got[3] == 4.0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,K,Hq,Hkv,ctx,window", [
+    (1, 0, 16, 1, [900], 0), (4, 0, 8, 8, [0, 990, -1, 31], 0), (32, 1, 16, 8, None, 0),
+    (33, 1, 16, 8, None, 0),                    # past 256 units: fewer wavefronts
+    (5, 3, 8, 2, [700, 1, 32, 512, 63], 65),
+])
+def test_few_short_units(B, K, Hq, Hkv, ctx, window, D):
+    """Short contexts of few units, whose workgroups have twice the wavefronts:
+    more of them than tiles, tiles in two and more rounds, windows."""
+    rng = np.random.default_rng(B + D)
+    ctx = rng.integers(0, 600, B) if ctx is None else np.array(ctx)
+    c = Case(B, K, Hq, Hkv, D, 32, ctx, rng.integers(0, K + 1, B), window=window, seed=21)
+    got = c.run()
+    c.check(got)
+    assert torch.equal(c.run(), got)
