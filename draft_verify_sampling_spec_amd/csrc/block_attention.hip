@@ -199,11 +199,12 @@ struct Lds {
     int found;
 };
 
-// One tile. kMasked: some row does not see some token of it.
+// One tile. kMasked: some row does not see some token of it; positions outside
+// [first, last] no row sees.
 template <int D, int kMT, int kWaves, int kAct, bool kMasked>
 __device__ __forceinline__ void tile_step(State<D, kAct>& st, const Frag<D>& f,
                                           const Lds<D, kMT, kWaves>& sh, const AttendArgs& a, int lane,
-                                          int tok0, int last, const uint8_t* tile) {
+                                          int tok0, int first, int last, const uint8_t* tile) {
     using L = Tile<D>;
     using S = State<D, kAct>;
     // These accumulators leave no registers for steps that overlap (D = 256, of
@@ -304,14 +305,15 @@ __device__ __forceinline__ void tile_step(State<D, kAct>& st, const Frag<D>& f,
             const unsigned sc = f.vs[p][half];
             unsigned bits = (r == 3 ? sc >> 1 : sc << (23 - 8 * r)) & 0x7f800000u;
             if (kMasked) {
-                // What some row does not see must not reach it as 0 * NaN:
-                // tokens past the block hold anything and are cleared; NaN
-                // groups of tokens that other rows see are cleared here and
-                // put into those rows below.
+                // What some row does not see must not reach it as 0 * NaN or
+                // 0 * infinity: positions past the block and in front of every
+                // row's window hold anything and are cleared; NaN groups of
+                // tokens that other rows see are cleared here and put into
+                // those rows below.
                 const int j = tok0 + 16 * half + 4 * quad + r;
-                const bool nan = bits == 0x7f800000u;
-                poison |= nan && j <= last;
-                if (nan || j > last) {
+                const bool nan = bits == 0x7f800000u, some = j >= first && j <= last;
+                poison |= nan && some;
+                if (nan || !some) {
                     bits = 0x3f800000u;
                     w[i] = 0;
                 }
@@ -421,20 +423,21 @@ struct Stream {
     __device__ __forceinline__ void run(State<D, kAct>& st, const Lds<D, kMT, kWaves>& sh,
                                         const AttendArgs& a, const Work& wk, const Block& blk,
                                         const uint8_t* tile, int lane) {
+        const int lo = a.window > 0 ? max(0, blk.ctx - a.window + 1) : 0;
         int n = 0;
         for (; wave + n * kWaves < edges; ++n) {
             const uint8_t* next = tile;
             if (n + 1 < count) next = fetch<1>(a, wk, n + 1, lane);
-            tile_step<D, kMT, kWaves, kAct, true>(st, f[0], sh, a, lane, tile_of(n) * kTile, blk.ctx + blk.len - 1, tile);
+            tile_step<D, kMT, kWaves, kAct, true>(st, f[0], sh, a, lane, tile_of(n) * kTile, lo, blk.ctx + blk.len - 1, tile);
             f[0] = f[1];
             tile = next;
         }
         while (n < count) {
             if (n + 1 < count) fetch<1>(a, wk, n + 1, lane);
-            tile_step<D, kMT, kWaves, kAct, false>(st, f[0], sh, a, lane, 0, 0, nullptr);
+            tile_step<D, kMT, kWaves, kAct, false>(st, f[0], sh, a, lane, 0, 0, 0, nullptr);
             if (n + 1 < count) {
                 if (n + 2 < count) fetch<0>(a, wk, n + 2, lane);
-                tile_step<D, kMT, kWaves, kAct, false>(st, f[1], sh, a, lane, 0, 0, nullptr);
+                tile_step<D, kMT, kWaves, kAct, false>(st, f[1], sh, a, lane, 0, 0, 0, nullptr);
             }
             n += 2;
         }

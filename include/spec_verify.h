@@ -560,7 +560,8 @@ int spec_verify_cache_read(const void* cache, const int32_t* page_table, const i
  *   scale        finite; usually 1 / sqrt(head_dim). Scores scale log2(e) q . k
  *                past fp32's range give NaN.
  *   window       0, or the number of positions a row sees, its own included.
- *                Pages wholly before every row's window are not needed.
+ *                Pages wholly before every row's window are not needed, and
+ *                positions before it need never have been written.
  *   out          bf16 [B, K+1, q_heads, head_dim] (device, 16-byte aligned).
  *                Rows t > budgets[b] and empty slots keep their values. It may
  *                not overlap any other argument.
