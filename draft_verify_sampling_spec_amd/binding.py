@@ -709,8 +709,9 @@ class BlockCache:
     """A target layer's paged 4-bit key/value cache on one device: writing
     blocks (or prompts), reading tokens back, and the attention of drafted
     blocks over it. Holds the pool (torch-allocated unless given: uint8
-    [num_pages, kv_heads, page_size / 32, 34 head_dim]); the page table and
-    the lengths are the caller's.
+    [num_pages, kv_heads, page_size / 32, 34 head_dim]; ``pool`` may be replaced
+    by another of that shape between calls); the page table and the lengths are
+    the caller's.
 
     ``status`` (int32 [1] on the device, or None) collects SV_FLAG_* bits;
     nothing clears it. Calls are enqueued on ``stream`` (default: the current
@@ -729,14 +730,19 @@ class BlockCache:
         if spec_verify_cache_bytes(num_pages, kv_heads, head_dim, page_size) == 0:
             raise ValueError(f"bad cache geometry: {num_pages} pages of {page_size} tokens, "
                              f"{kv_heads} heads of {head_dim}")
-        shape = (self.num_pages, self.kv_heads, self.page_size // 32, 34 * self.head_dim)
-        if pool is None:
-            pool = torch.zeros(shape, dtype=torch.uint8, device=device)
-        self._pool_ptr = _need(pool, "pool", torch.uint8, shape, self._index)
-        self.pool = pool
+        self.pool = torch.zeros(self._pool_shape(), dtype=torch.uint8, device=device) \
+            if pool is None else pool
+        self._pool_ptr()
         self._workspace_bytes = {}          # by attention shape
         # For calls whose plan has no parts, which leave their 256 bytes alone.
         self._no_parts = torch.empty(256, dtype=torch.uint8, device=device)
+
+    def _pool_shape(self):
+        return self.num_pages, self.kv_heads, self.page_size // 32, 34 * self.head_dim
+
+    def _pool_ptr(self):
+        # At every call: ``pool`` may be another tensor, or have other storage, by then.
+        return _need(self.pool, "pool", torch.uint8, self._pool_shape(), self._index)
 
     def _table(self, page_table, B):
         shape = page_table.shape
@@ -770,7 +776,7 @@ class BlockCache:
             _need(ctx_lens, "ctx_lens", torch.int32, (B,), index),
             None if budgets is None else _need(budgets, "budgets", torch.int32, (B,), index),
             B, T, self.kv_heads, self.head_dim, self.page_size, width, self.num_pages,
-            self._pool_ptr,
+            self._pool_ptr(),
             None if status is None else _need(status, "status", torch.int32, (1,), index),
             _raw_stream(index))
         if rc != SV_OK:
@@ -800,7 +806,7 @@ class BlockCache:
         if out is None:
             out = tuple(torch.zeros(shape, dtype=dtype, device=self.device) for _ in range(2))
         rc = load().spec_verify_cache_read(
-            self._pool_ptr, table,
+            self._pool_ptr(), table,
             None if starts is None else _need(starts, "starts", torch.int32, (B,), index),
             _need(lens, "lens", torch.int32, (B,), index), B, T, self.kv_heads, self.head_dim,
             self.page_size, width, self.num_pages, code,
@@ -851,7 +857,7 @@ class BlockCache:
         workspace = self._no_parts if nbytes == 256 else torch.empty(
             nbytes, dtype=torch.uint8, device=self.device)
         rc = load().spec_verify_attention(
-            queries.data_ptr(), stride, self._pool_ptr, table,
+            queries.data_ptr(), stride, self._pool_ptr(), table,
             _need(ctx_lens, "ctx_lens", torch.int32, (B,), index),
             None if budgets is None else _need(budgets, "budgets", torch.int32, (B,), index),
             B, T - 1, heads, self.kv_heads, dim, self.page_size, width, self.num_pages,

@@ -50,3 +50,36 @@ def test_bytes_before_every_window_are_not_read(D, K, Hq, Hkv, window, ctx):
         got = c.run()
         assert torch.equal(got, clean), byte
         assert int(c.status) == 0
+
+
+def test_calls_use_the_pool_that_the_cache_holds_now():
+    """A pool replaced, or given other storage, between calls; one of another
+    shape, type or place is refused."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    shape = (4, 2, 1, 34 * 64)
+    first, second = (torch.zeros(shape, dtype=torch.uint8, device=DEV) for _ in range(2))
+    c = BlockCache(DEV, 4, 2, 64, 32, pool=first)
+    k, v = (torch.randn(1, 40, 2, 64, generator=g, device=DEV).bfloat16() for _ in range(2))
+    q = torch.randn(1, 3, 4, 64, generator=g, device=DEV).bfloat16()
+    table, zero, n = _i32([[3, 1]]), _i32([0]), _i32([40])
+    c.write(k, v, table, zero)
+    values = c.read(table, None, n, 40)
+    out = c.attend(q, table, _i32([37]))
+    assert first.any() and out.any()
+    c.pool = second
+    assert not any(x.any() for x in c.read(table, None, n, 40))
+    assert not c.attend(q, table, _i32([37])).any()
+    kept = first.clone()
+    c.write(k, v, table, zero)
+    assert torch.equal(second, kept) and torch.equal(first, kept)
+    third = kept.clone()
+    second.zero_()
+    second.set_(third)                                     # the same tensor, other storage
+    assert all(torch.equal(x, y) for x, y in zip(c.read(table, None, n, 40), values))
+    assert torch.equal(c.attend(q, table, _i32([37])), out)
+    for bad in (kept[:3], kept.to(torch.int8), kept.cpu(), kept.transpose(0, 1)):
+        c.pool = bad
+        for call in (lambda: c.write(k, v, table, zero), lambda: c.read(table, None, n, 40),
+                     lambda: c.attend(q, table, _i32([37]))):
+            with pytest.raises(ValueError):
+                call()
