@@ -668,8 +668,10 @@ def spec_head_logits(h_codes, h_scales, w_codes, w_scales, R, H, V, dtype, out, 
 # belong to that stream, so that one freed when the call returns is not handed
 # out again before the stream is done with it.
 
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# A torch build without GPU support has no such accessors and still imports this.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _need(t, name, dtype, shape, index):
