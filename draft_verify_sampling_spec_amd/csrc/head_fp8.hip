@@ -542,14 +542,16 @@ __global__ __launch_bounds__(256) void logits_large_kernel(LogitArgs a, int v_ti
             at.w = last ? then_at.w : at.w + 1;
             #pragma unroll
             for (int j = 0; j < C::M; ++j) at.h[j] = last ? then_at.h[j] : at.h[j] + 1;
-            load_scales();                                  // of the next stage
             const bool wrap = k + 2 >= a.blocks;
             const Source s = wrap ? then_from : from;
             const int ks = wrap ? k + 2 - a.blocks : k + 2;
             __builtin_amdgcn_sched_barrier(0);
-            // All but the scales has arrived. (Loads complete in order, so the
-            // scales outstanding means at most them and no stage's loads.)
-            svdma::wait_vm<C::M + 1>();
+            // The next stage has arrived: its loads were issued a phase ago, and
+            // nothing since. (A count that left the scales' loads outstanding
+            // would rest on how many of them the compiler makes.)
+            svdma::wait_vm<0>();
+            __builtin_amdgcn_sched_barrier(0);
+            load_scales();                                  // of the next stage
             svdma::ring_barrier();
             __builtin_amdgcn_sched_barrier(0);
             #pragma unroll
