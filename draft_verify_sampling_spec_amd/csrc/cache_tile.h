@@ -122,28 +122,28 @@ __device__ __forceinline__ void flag(int32_t* status, unsigned bits) {
 
 // A request's block: its context length (negative: an empty slot) and its
 // tokens (budget + 1, the budget clamped into [0, width - 1]; NULL budgets:
-// width). len = 0: nothing to do. A block that does not fit the request's
-// page table row is flagged and skipped.
+// width). len = 0 (and ctx = 0, so that nothing derived from it overflows):
+// nothing to do. A block that does not fit the request's page table row is
+// flagged and skipped.
 struct Block {
     int ctx, len;
 };
 __device__ __forceinline__ Block block_of(const int32_t* ctx_lens, const int32_t* budgets, int b,
                                           int width, const Pages& pages, int32_t* status,
                                           bool report) {
-    Block k{ctx_lens[b], 0};
-    if (k.ctx < 0) return k;
+    const int ctx = ctx_lens[b];
+    if (ctx < 0) return Block{0, 0};
     int n = width;
     if (budgets) {
         const int kb = budgets[b];
         n = min(max(kb, 0), width - 1) + 1;
-        if (report && n != kb + 1) flag(status, SV_FLAG_BAD_BUDGET);
+        if (report && n - 1 != kb) flag(status, SV_FLAG_BAD_BUDGET);
     }
-    if ((long long)k.ctx + n > ((long long)pages.max_pages << pages.shift)) {
+    if ((long long)ctx + n > ((long long)pages.max_pages << pages.shift)) {
         if (report) flag(status, SV_FLAG_BAD_LENGTH);
-        return k;
+        return Block{0, 0};
     }
-    k.len = n;
-    return k;
+    return Block{ctx, n};
 }
 
 inline bool aligned(const void* p, uintptr_t n) {

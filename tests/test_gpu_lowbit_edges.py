@@ -83,3 +83,30 @@ def test_calls_use_the_pool_that_the_cache_holds_now():
                      lambda: c.attend(q, table, _i32([37]))):
             with pytest.raises(ValueError):
                 call()
+
+
+@pytest.mark.parametrize("K,Hq,ctx", [(3, 4, 90), (8, 16, 90), (4, 8, 5000)])
+def test_the_largest_and_smallest_numbers_of_a_request(K, Hq, ctx):
+    """Budgets and contexts at the ends of int32, beside a request that is in
+    order, under a window and without: flagged, and otherwise what the clamped
+    budgets and empty slots give."""
+    far = 2**31 - 1
+    for window in (0, 50, far):
+        c = ta.Case(3, K, Hq, 2, 64, 32, np.array([ctx, ctx - 7, ctx - 20]), np.full(3, K), window=window, seed=5)
+        for budgets, lens, clamped, held, flag in (
+                ([K, far, -far - 1], c.ctx, [K, K, 0], c.ctx, sb.SV_FLAG_BAD_BUDGET),
+                ([K, K, K], [ctx, far, -far - 1], [K, K, K], [ctx, -1, -1], sb.SV_FLAG_BAD_LENGTH)):
+            c.budgets, c.ctx = np.array(clamped), np.array(held)
+            want = c.run()
+            c.check(want)
+            c.budgets, c.ctx = np.array(budgets), np.array(lens)
+            got = c.run()
+            assert int(c.status) == flag
+            assert torch.equal(got, want)
+    cache = BlockCache(DEV, 3, 2, 64, 32)
+    k = torch.ones(3, 4, 2, 64, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cache.write(k, k, _i32([[0], [1], [2]]), _i32([0, 0, 0]), _i32([far, -far - 1, 3]), status=status)
+    assert int(status) == sb.SV_FLAG_BAD_BUDGET
+    one = cache.read(_i32([[0], [1], [2]]), None, _i32([4, 4, 4]), 4)[0]
+    assert bool((one[0] == 1).all()) and bool((one[1, 0] == 1).all()) and not one[1, 1:].any() and bool((one[2] == 1).all())
