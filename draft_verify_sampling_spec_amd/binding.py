@@ -12,6 +12,7 @@ the HIP runtime torch already loaded (one runtime per process).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -674,6 +675,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# A function of the shapes alone, for every layer and step: the last shapes' sizes.
+_attention_bytes = functools.lru_cache(maxsize=1024)(spec_verify_attention_workspace_bytes)
+
+
 def _need(t, name, dtype, shape, index):
     """The address of a contiguous tensor of exactly this type, shape and GPU."""
     if isinstance(t, torch.Tensor):
@@ -735,7 +740,6 @@ class BlockCache:
         self.pool = torch.zeros(self._pool_shape(), dtype=torch.uint8, device=device) \
             if pool is None else pool
         self._pool_ptr()
-        self._workspace_bytes = {}          # by attention shape
         # For calls whose plan has no parts, which leave their 256 bytes alone.
         self._no_parts = torch.empty(256, dtype=torch.uint8, device=device)
 
@@ -845,15 +849,11 @@ class BlockCache:
         B, T, heads, dim = shape
         stride = _token_stride(queries, "queries", index)
         table, width = self._table(page_table, B)
-        key = (B, T, heads, width, window)
-        nbytes = self._workspace_bytes.get(key)
-        if nbytes is None:
-            nbytes = spec_verify_attention_workspace_bytes(
-                max(B, 1), T - 1, heads, self.kv_heads, dim, self.page_size, width, window)
-            if nbytes == 0:
-                raise ValueError(f"bad attention shape: B={B} K={T - 1} q_heads={heads} kv_heads="
-                                 f"{self.kv_heads} window={window} max_pages={width}")
-            self._workspace_bytes[key] = nbytes
+        nbytes = _attention_bytes(max(B, 1), T - 1, heads, self.kv_heads, dim, self.page_size,
+                                  width, window)
+        if nbytes == 0:
+            raise ValueError(f"bad attention shape: B={B} K={T - 1} q_heads={heads} kv_heads="
+                             f"{self.kv_heads} window={window} max_pages={width}")
         if out is None:
             out = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
         workspace = self._no_parts if nbytes == 256 else torch.empty(

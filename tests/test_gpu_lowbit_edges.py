@@ -110,3 +110,18 @@ def test_the_largest_and_smallest_numbers_of_a_request(K, Hq, ctx):
     assert int(status) == sb.SV_FLAG_BAD_BUDGET
     one = cache.read(_i32([[0], [1], [2]]), None, _i32([4, 4, 4]), 4)[0]
     assert bool((one[0] == 1).all()) and bool((one[1, 0] == 1).all()) and not one[1, 1:].any() and bool((one[2] == 1).all())
+
+
+def test_many_shapes_leave_little_behind():
+    """A table width and batch per call, as a server has them: what is kept of
+    the shapes stays bounded, and the sizes stay those of the shapes."""
+    c = BlockCache(DEV, 1, 1, 64, 32)
+    q = torch.zeros(0, 2, 4, 64, dtype=torch.bfloat16, device=DEV)
+    for width in range(1, 1500):
+        c.attend(q, torch.zeros(0, width, dtype=torch.int32, device=DEV), _i32([]))
+    held = [len(x) for x in vars(c).values() if isinstance(x, (dict, list, set))]
+    assert max(held, default=0) <= 1024
+    for width in (1, 700, 1499, 1, 5000):
+        assert sb._attention_bytes(2, 3, 4, 1, 64, 32, width, 0) == \
+            sb.spec_verify_attention_workspace_bytes(2, 3, 4, 1, 64, 32, width, 0)
+    assert sb._attention_bytes.cache_info().currsize <= 1024
