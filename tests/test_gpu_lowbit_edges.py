@@ -125,3 +125,169 @@ def test_many_shapes_leave_little_behind():
         assert sb._attention_bytes(2, 3, 4, 1, 64, 32, width, 0) == \
             sb.spec_verify_attention_workspace_bytes(2, 3, 4, 1, 64, 32, width, 0)
     assert sb._attention_bytes.cache_info().currsize <= 1024
+
+
+# ---- three row tiles, and NaN groups and bad pages in every cut of the work -----------
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("K,Hq,Hkv,ctx", [
+    (8, 8, 2, [0, 1, 31, 32, 33, 95, -1, 300]),      # 36 rows
+    (10, 8, 2, [5, 64, 511]),                        # 44 rows
+    (15, 3, 1, [17, 800, 96]),                       # 48 rows
+])
+def test_three_row_tiles(D, K, Hq, Hkv, ctx):
+    """Blocks of up to 48 rows a head, short contexts; ragged budgets leave one,
+    two or three row tiles."""
+    _log(f"[attend] three row tiles D={D} K={K} Hq={Hq} Hkv={Hkv}")
+    rng = np.random.default_rng(K)
+    budgets = rng.integers(0, K + 1, len(ctx))
+    budgets[-1], budgets[0], budgets[1] = K, 0, K // 2
+    c = ta.Case(len(ctx), K, Hq, Hkv, D, 32, np.array(ctx), budgets, seed=K)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("B,K,Hq,Hkv,D,lo,hi,window", [
+    (64, 8, 32, 8, 128, 300, 9000, 0),         # shares of a line
+    (24, 8, 16, 4, 64, 300, 12000, 0),
+    (2, 8, 8, 2, 128, 30000, 60000, 0),        # few units, many parts each
+    (1, 10, 8, 2, 64, 40000, 40000, 0),
+    (16, 8, 32, 8, 128, 4000, 4100, 0),        # nearly equal units, few parts each
+    (16, 8, 32, 8, 128, 5000, 9000, 3000),
+])
+def test_three_row_tiles_split_over_workgroups(B, K, Hq, Hkv, D, lo, hi, window):
+    ta.test_every_way_the_work_is_cut(B, K, Hq, Hkv, D, lo, hi, window)
+
+
+# Shapes of one to four row tiles: (B, K, Hq, Hkv, D, contexts from .. to, window).
+CUTS = [
+    (6, 8, 8, 2, 128, 40, 700, 0),             # direct, three row tiles
+    (6, 8, 16, 2, 128, 40, 700, 0),            # direct, four, two row blocks
+    (6, 4, 16, 2, 64, 40, 700, 90),            # direct, three, a window
+    (5, 5, 8, 2, 256, 40, 700, 0),             # direct, two of 256 channels
+    (2, 0, 8, 2, 128, 9000, 20000, 0),         # many parts, one row tile
+    (2, 8, 8, 2, 128, 9000, 20000, 0),         # three
+    (2, 7, 16, 2, 128, 9000, 20000, 0),        # four
+    (2, 7, 16, 2, 64, 9000, 20000, 5000),
+    (2, 5, 8, 2, 256, 9000, 20000, 0),
+    (64, 8, 32, 8, 128, 300, 9000, 0),         # a line
+    (24, 7, 64, 8, 64, 300, 9000, 0),
+]
+
+
+class Big:
+    """A batch made on the GPU: random codes under sane scales."""
+
+    def __init__(self, B, K, Hq, Hkv, D, lo, hi, window, page=64):
+        g = torch.Generator(device=DEV).manual_seed(B + K + D)
+        self.ctx = torch.randint(lo, hi + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+        self.ctx[0], self.ctx[-1] = hi, lo
+        self.budgets = torch.randint(0, K + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+        self.budgets[0] = K
+        need = (self.ctx + self.budgets + page) // page
+        first = torch.cumsum(need, 0) - need
+        width, pages = int(need.max()), int(need.sum())
+        col = torch.arange(width, device=DEV)
+        order = torch.randperm(pages, generator=g, device=DEV)
+        self.table = torch.where(col < need[:, None], order[(first[:, None] + col).clamp_max(pages - 1)], -1).int()
+        self.cache = BlockCache(DEV, pages, Hkv, D, page)
+        self.cache.pool.random_(0, 256, generator=g)
+        self.cache.pool[..., 32 * D:].random_(122, 129, generator=g)
+        self.q = torch.randn(B, K + 1, Hq, D, generator=g, device=DEV).bfloat16()
+        self.K, self.Hq, self.Hkv, self.D, self.window, self.page = K, Hq, Hkv, D, window, page
+        self.status = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def run(self):
+        return self.cache.attend(self.q, self.table, self.ctx, self.budgets, window=self.window,
+                                 status=self.status)
+
+    def sees(self, b, pos):
+        """Which rows t of request b see a position."""
+        row = int(self.ctx[b]) + torch.arange(self.K + 1, device=DEV)
+        seen = (pos <= row) & (torch.arange(self.K + 1, device=DEV) <= self.budgets[b])
+        return seen & (pos > row - self.window) if self.window else seen
+
+
+@pytest.mark.parametrize("cut", CUTS)
+def test_nan_tokens_in_every_cut(cut):
+    """NaN groups of values and of keys of one kv head: in a tile that every row
+    sees whole, in the block itself (seen by its later rows only), at a window's
+    edge and in front of every window. They reach exactly the rows that see the
+    token; every other output keeps its bits."""
+    _log(f"[attend] NaN tokens {cut}")
+    x = Big(*cut)
+    clean = x.run()
+    assert not clean.isnan().any()
+    b, h, group = 0, x.Hkv - 1, x.Hq // x.Hkv
+    hi = int(x.ctx[b])
+    kc, vc, ks, vs = lb.tile_addresses(x.D)
+    where = [hi - 200 - 32 * (hi // 900), hi + x.K // 2, hi]
+    if x.window:
+        where = [hi - x.window // 2, hi + x.K // 2, hi - x.window + 1 + x.K // 2, hi - x.window]
+    for pos in where:
+        for side, at in (("value", vs), ("key", ks)):
+            grp = 1
+            i = int(x.table[b, pos // x.page]), h, pos % x.page // 32, int(at[pos % 32, grp])
+            kept = x.cache.pool[i].item()
+            x.cache.pool[i] = 255
+            got = x.run()
+            x.cache.pool[i] = kept
+            want = torch.zeros_like(clean, dtype=torch.bool)
+            ch = slice(32 * grp, 32 * grp + 32) if side == "value" else slice(None)
+            want[b, x.sees(b, pos), h * group:(h + 1) * group, ch] = True
+            assert torch.equal(got.isnan(), want), (pos, side)
+            assert torch.equal(torch.where(want, 0, got), torch.where(want, 0, clean)), (pos, side)
+    assert torch.equal(x.run(), clean) and int(x.status) == 0
+
+
+@pytest.mark.parametrize("cut", CUTS)
+def test_bad_pages_in_every_cut(cut):
+    """A page outside the pool is flagged; every other request keeps its bits.
+    Where rows have a window, the pages before it may be anything."""
+    _log(f"[attend] bad pages {cut}")
+    x = Big(*cut)
+    hi = int(x.ctx[0])
+    if x.window:
+        x.table[0, :(hi - x.window + 1) // x.page] = -7
+    clean = x.run()
+    assert int(x.status) == 0
+    for col in {max(0, hi - x.window // 2) // x.page if x.window else 0, hi // x.page}:
+        kept = int(x.table[0, col])
+        for bad in (-1, x.cache.num_pages, 2**31 - 1):
+            x.table[0, col] = bad
+            x.status.zero_()
+            got = x.run()
+            assert int(x.status) == sb.SV_FLAG_BAD_PAGE
+            assert torch.equal(got[1:], clean[1:])
+        x.table[0, col] = kept
+    x.status.zero_()
+    assert torch.equal(x.run(), clean) and int(x.status) == 0
+
+
+def test_rows_of_a_prompts_chunk_in_blocks():
+    """More rows than a call takes: a chunk of 80 tokens over a prefix is written
+    at once and attended in blocks of 33 rows, each from its own position."""
+    Hq, Hkv, D, page, n = 6, 2, 128, 64, 80
+    g = torch.Generator(device=DEV).manual_seed(6)
+    cache = BlockCache(DEV, 12, Hkv, D, page)
+    table = torch.randperm(12, generator=g, device=DEV)[:10].int().view(2, 5)
+    ctx, budgets = _i32([37, 200]), _i32([n - 1, 50])
+    prefix = torch.randn(2, 2, 200, Hkv, D, generator=g, device=DEV).bfloat16()
+    cache.write(prefix[0], prefix[1], table, _i32([0, 0]), ctx - 1)
+    k, v = (torch.randn(2, n, Hkv, D, generator=g, device=DEV).bfloat16() for _ in range(2))
+    q = torch.randn(2, n, Hq, D, generator=g, device=DEV).bfloat16()
+    cache.write(k, v, table, ctx, budgets)
+    out = torch.zeros_like(q)
+    most = sb.SV_MAX_K + 1
+    for at in range(0, n, most):
+        rows = q[:, at:at + most].contiguous()
+        left = budgets - at                                # a request whose rows have ended is skipped
+        start = torch.where(left < 0, -1, ctx + at)
+        out[:, at:at + most] = cache.attend(rows, table, start, left.clamp(0, rows.shape[1] - 1))
+    pool, tab = cache.pool.cpu().numpy(), table.cpu().numpy()
+    for b, (c, last) in enumerate(((37, n - 1), (200, 50))):
+        total = c + last + 1
+        keys, values = lb.read(pool, tab[b], 0, total, D, page)
+        ref, mag, reach = lb.attend(q[b, :last + 1].double().cpu().numpy(), keys, values, 0, c, D ** -0.5)
+        err = np.abs(out[b, :last + 1].double().cpu().numpy() - ref)
+        assert np.all(err <= ta._bound(ref, mag, reach, D, total))
+        assert not out[b, last + 1:].any()
