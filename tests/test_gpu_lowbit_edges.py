@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from draft_verify_sampling_spec_amd import BlockCache, binding as sb
+from draft_verify_sampling_spec_amd import BlockCache, binding as sb, head_logits, head_quantize
 from oracle import lowbit as lb
 from tests import test_gpu_attention as ta
 
@@ -291,3 +291,53 @@ def test_rows_of_a_prompts_chunk_in_blocks():
         err = np.abs(out[b, :last + 1].double().cpu().numpy() - ref)
         assert np.all(err <= ta._bound(ref, mag, reach, D, total))
         assert not out[b, last + 1:].any()
+
+
+# ---- the 8-bit head --------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,H,V", [(500, 256, 32000), (500, 384, 31999), (700, 264, 60008)])
+def test_a_nan_block_in_the_largest_tiles(R, H, V, dtype):
+    """256 x 256 tiles, from one workgroup to the next (bf16, V a multiple of 8)
+    and one by one: a NaN block reaches its row or its 128 columns only; every
+    other logit keeps its bits."""
+    _log(f"[logits] NaN block R={R} H={H} V={V} {dtype}")
+    g = torch.Generator(device=DEV).manual_seed(R + V)
+    hc, hs = head_quantize(torch.randn(R, H, generator=g, device=DEV), 1)
+    wc, ws = head_quantize(torch.randn(V, H, generator=g, device=DEV), 128)
+    clean = head_logits(hc, hs, wc, ws, dtype=dtype)
+    assert bool(clean.isfinite().all())
+    want = torch.zeros(R, V, dtype=torch.bool, device=DEV)
+    for row, blk in ((1, 0), (R - 1, hs.shape[1] - 1)):
+        hc.view(torch.uint8)[row, 128 * blk:128 * blk + 128] = 0x7f
+        hs.view(torch.uint8)[row, blk] = 255
+        want[row] = True
+    for col, blk in ((3, 1), ((V - 1) // 128, 0)):
+        wc.view(torch.uint8)[128 * col:128 * col + 128, 128 * blk:128 * blk + 128] = 0x7f
+        ws.view(torch.uint8)[col, blk] = 255
+        want[:, 128 * col:128 * col + 128] = True
+    got = head_logits(hc, hs, wc, ws, dtype=dtype)
+    assert torch.equal(got.isnan(), want)
+    assert torch.equal(got.masked_fill(want, 0), clean.masked_fill(want, 0))
+
+
+def test_states_of_more_than_one_launch():
+    """More than 2^31 / 16 blocks of 128 channels: rows on both sides of the
+    border between launches, the first and the last; all others are zeros."""
+    rows, H = 1 << 20, 16512
+    border = (1 << 27) // (H // 128)
+    assert rows * (H // 128) > 1 << 27 and border < rows
+    x = torch.zeros(rows, H, dtype=torch.bfloat16, device=DEV)
+    pick = torch.tensor([0, border - 1, border, border + 1, rows - 1], device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x[pick] = torch.randn(pick.numel(), H, generator=g, device=DEV).bfloat16()
+    codes, scales = head_quantize(x)
+    rc, rs = lb.quantise_head(x[pick].double().cpu().numpy(), 1)
+    assert np.array_equal(codes[pick].double().cpu().numpy(), rc)
+    assert np.array_equal(np.exp2(scales.view(torch.uint8)[pick].double().cpu().numpy() - 127.0), rs)
+    codes.view(torch.uint8)[pick] = 0
+    scales.view(torch.uint8)[pick] = 63                    # 2^-64, the scale of zeros
+    step = 1 << 16
+    for at in range(0, rows, step):
+        assert not codes.view(torch.uint8)[at:at + step].any()
+        assert bool((scales.view(torch.uint8)[at:at + step] == 63).all())
