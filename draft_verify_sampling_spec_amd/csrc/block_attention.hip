@@ -49,8 +49,15 @@ constexpr float kNegInf = -INFINITY;
 //  - direct: a workgroup per unit and nothing to join, where rows see at most
 //    kDirectTiles tiles, or twice that if every workgroup that is resident at
 //    once has a unit (searching and joining, about 8 us, would cost more: 64
-//    requests under a window of 1,024 tokens 41 against 34 us), or where each
-//    has kDirectUnits units (they even out by themselves).
+//    requests under a window of 1,024 tokens 41 against 34 us; measured there
+//    only), or kDirectTiles for each of kDirectUnits and more units that it has:
+//    then they even out by themselves, even if one request is as long as the
+//    page table allows and the others are short. (512 requests of 256..4,096
+//    tokens, 2 rows x 3 heads of 128: 228 us direct, 244 cut; heads of 64 195
+//    and 216; 18 rows of 256 channels, 128 requests of 2,016 tokens 175 and 173.
+//    But one request of 131,000 tokens among 127 of 1,000 takes 1,815 us direct
+//    and 195 cut, among 511 897 and 159: under page tables wider than that a
+//    batch of many even requests pays the cut's 2 to 11 %.)
 // Else the lengths, which are on the device, decide. Every workgroup adds up
 // the requests for itself and finds its place by a prefix sum. With `groups`
 // workgroups resident at once and share = (cost of all units) / groups:
@@ -914,7 +921,7 @@ Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_p
     const int held = D == 64 ? resident<64>(p.mt) : D == 128 ? resident<128>(p.mt) : resident<256>(p.mt);
     p.groups = (int)std::min<long long>(held, most);
     p.direct = tiles <= kDirectTiles || (units >= held && tiles <= 2 * kDirectTiles) ||
-               units >= (long long)kDirectUnits * held;
+               (units >= (long long)kDirectUnits * held && tiles * held <= kDirectTiles * units);
     // Twice the wavefronts on a unit's tiles where a CU has no more than one unit
     // of one row tile: what is left is latency. (8 requests of up to 577 tokens, 8
     // kv heads of 128: 7.0 against 7.6 us, of 900 tokens 8.2 against 9.4, of 256

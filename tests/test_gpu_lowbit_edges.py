@@ -341,3 +341,23 @@ def test_states_of_more_than_one_launch():
     for at in range(0, rows, step):
         assert not codes.view(torch.uint8)[at:at + step].any()
         assert bool((scales.view(torch.uint8)[at:at + step] == 63).all())
+
+
+@pytest.mark.parametrize("B,K,Hq,Hkv,D,long,short", [
+    (128, 5, 24, 8, 256, 131000, 1000), (300, 2, 32, 16, 64, 70000, 30), (520, 1, 16, 8, 128, 50000, 200)])
+def test_one_long_request_among_many_short_ones(B, K, Hq, Hkv, D, long, short):
+    """More units than the chip holds, one request far longer than the others."""
+    _log(f"[attend] skewed B={B} K={K} D={D} {long} among {short}")
+    x = Big(B, K, Hq, Hkv, D, short // 2, short, 0)
+    ctx = x.ctx.clone()
+    ctx[B // 3] = long
+    width = (long + K) // x.page + 1
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    table[:, :x.table.shape[1]] = x.table
+    table[B // 3] = torch.arange(width, device=DEV) % x.cache.num_pages       # pages in turn
+    got = x.cache.attend(x.q, table, ctx, x.budgets, status=x.status)
+    assert int(x.status) == 0
+    pick = [B // 3] + list(range(0, B, 7))                 # the long one first
+    q, rows, lens, left = x.q[pick], table[pick].contiguous(), ctx[pick], x.budgets[pick]
+    ta._check_on_gpu(x.cache, q, got[pick], rows, lens.tolist(), left.tolist())
+    assert torch.equal(x.cache.attend(x.q, table, ctx, x.budgets), got)
