@@ -7,7 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from draft_verify_sampling_spec_amd import BlockCache, binding as sb, head_logits, head_quantize
+from draft_verify_sampling_spec_amd import BlockCache, SpecVerify, binding as sb, head_logits
+from draft_verify_sampling_spec_amd import head_quantize
 from oracle import lowbit as lb
 from tests import test_gpu_attention as ta
 
@@ -361,3 +362,36 @@ def test_one_long_request_among_many_short_ones(B, K, Hq, Hkv, D, long, short):
     q, rows, lens, left = x.q[pick], table[pick].contiguous(), ctx[pick], x.budgets[pick]
     ta._check_on_gpu(x.cache, q, got[pick], rows, lens.tolist(), left.tolist())
     assert torch.equal(x.cache.attend(x.q, table, ctx, x.budgets), got)
+
+
+def test_an_empty_slot_stays_empty_over_steps():
+    """The loop of a serving step with a slot that holds no request: its page and
+    its length stay as they are, and the other requests' outputs are those of a
+    batch without it."""
+    B, K, Hq, Hkv, D, V, page = 3, 3, 4, 2, 64, 500, 32
+    g = torch.Generator(device=DEV).manual_seed(41)
+    head = head_quantize(torch.randn(V, Hq * D, generator=g, device=DEV), 128)
+    cache = BlockCache(DEV, 6, Hkv, D, page)
+    cache.pool[4:] = 77                                    # the empty slot's pages
+    table = _i32([[0, 1], [4, 5], [2, 3]])
+    ctx_lens = _i32([9, -1, 0])
+    qkv = torch.randn(4, B, K + 1, (Hq + 2 * Hkv) * D, generator=g, device=DEV).bfloat16()
+    live = torch.tensor([0, 2], device=DEV)
+    verify = SpecVerify(DEV, B, K, V, torch.float32)
+    for step in range(4):
+        q, k, v = (x.unflatten(-1, (-1, D)) for x in qkv[step].split([Hq * D, Hkv * D, Hkv * D], -1))
+        budgets = _i32([K, 2, step])
+        cache.write(k, v, table, ctx_lens, budgets)
+        o = cache.attend(q, table, ctx_lens, budgets)
+        logits = head_logits(*head_quantize(o.view(B * (K + 1), -1)), *head).view(B, K + 1, V)
+        drafted = logits[:, :K].argmax(-1).int()
+        drafted[:, 1] = 3
+        _, n_accepted, _, _ = verify.run(logits, None, drafted, budgets, 0.0, 1, want_probs=False)
+        assert torch.equal(o[live], cache.attend(q[live], table[live], ctx_lens[live], budgets[live]))
+        before = ctx_lens
+        ctx_lens = torch.where(ctx_lens < 0, ctx_lens, ctx_lens + n_accepted + 1)
+        assert int(ctx_lens[1]) == -1 and bool((ctx_lens[live] > before[live]).all())
+        assert ctx_lens.dtype == torch.int32
+    assert bool((cache.pool[4:] == 77).all()) and cache.pool[:4].any()
+    assert verify.status() == 0
+    verify.close()
