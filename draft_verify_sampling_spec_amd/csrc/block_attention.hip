@@ -4,11 +4,13 @@
 // The mathematics: row (t, h) of request b, t <= k_b, stands at position
 // p = ctx_b + t and sees the positions j of [max(0, p - window + 1), p]:
 //   o = sum_j 2^(z_j - m) v_j / sum_j 2^(z_j - m),  z_j = scale log2(e) q . k_j,
-// with the running maximum m and the sums held in fp32 over one pass. Keys
-// and values are decoded to bf16 (exact); products accumulate in fp32 on the
-// matrix cores. The probabilities 2^(z - m), in [0, 1], are rounded to bf16
-// for the value product (at most 2^-8 relative each, the size of the output's
-// own rounding); their sum is taken before that rounding.
+// over one pass, the reference m and the sums held in fp32. m is a maximum that
+// lags behind: it follows the running one when a term would exceed 2^8, so the
+// weights 2^(z - m) lie in [0, 2^8]. Keys and values are decoded to bf16 (exact);
+// products accumulate in fp32 on the matrix cores. The weights are rounded to
+// bf16 for the value product (at most 2^-8 relative each, the size of the
+// output's own rounding: with it outputs are 2.3e-3 of their norm off, without
+// it 1.7e-3); their sum is taken before that rounding.
 //
 // Layout: a wavefront takes tiles of 32 tokens of one kv head and all query
 // rows that share it (up to 16 kMT rows of (t, head in the group), in
@@ -21,10 +23,13 @@
 //
 // What bounds it is the latency of a tile's loads and the work on the tile
 // before, two wavefronts a SIMD: about 1.5 us a tile and wavefront, 6 TB/s with
-// all of them in the loop. 128 blocks of 3..9 rows x 4 heads over 1,024..8,192
-// tokens (8 kv heads of 128): 157 us, 4.1 TB/s, the join's 13 in it; single
-// tokens over the same contexts 129; one block of 5 over 131,071 tokens 41; 64
-// blocks under a window of 1,024 (8 kv heads of 256) 34.
+// all of them in the loop, 54 % of a wavefront's time spent waiting. 128 blocks of
+// 3..9 rows x 4 heads over 1,024..8,192 tokens (8 kv heads of 128): 155 us, 4.2
+// TB/s, the join's 13 in it, and 197 with 9 rows each; single tokens over the same
+// contexts 129; one block of 5 over 131,071 tokens 41; 64 blocks under a window of
+// 1,024 (8 kv heads of 256) 33. 64 blocks over 2,000..4,000 tokens, 8 kv heads:
+// 64 rows of 128 channels 101 us, 2.0 TB/s (that kernel spills 66 registers, six
+// reloads in its loop over pairs of tiles), 48 rows of 64 channels 50, 2.1 TB/s.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -374,18 +379,21 @@ __device__ __forceinline__ void tile_step(State<D, kAct>& st, const Frag<D>& f,
 
 // This wavefront's share of a run: of the run's tiles, those that some row
 // does not see whole first (the block's own, the windows' edges), then the
-// others, every kWaves-th by number n = 0, 1, ... The next tile's bytes are in
-// flight while one is worked on. (Two tiles ahead, or a ring in LDS filled by
-// buffer-to-LDS loads, measured slower: 174-186 against 153 us for 128
-// requests over 1,024..8,192 tokens.)
+// others, every kWaves-th by number n = 0, 1, ... The next tile's bytes are asked
+// for before one is worked on. Of the whole tiles only every other one's stay in
+// flight meanwhile: the second load of a pair is conditional, and where its two
+// paths meet the compiler waits for all of it but the last piece. (Two tiles
+// ahead, or a ring in LDS filled by buffer-to-LDS loads, measured slower: 174-186
+// against 153 us for 128 requests over 1,024..8,192 tokens.)
 template <int D, int kMT, int kWaves>
 struct Stream {
     using L = Tile<D>;
     Frag<D> f[2];
     int wave, first, low, u0, u1, edges, count;     // tiles [u0, u1) are seen whole by every row
-    // Page numbers of the next 64 tiles, one a lane. They come in one load: a
-    // lookup per tile would wait for every load before it, the tiles in flight
-    // among them.
+    // Page numbers of the next 64 tiles, one a lane. They come in one load: 157 us
+    // for 128 requests over 1,024..8,192 tokens, 192 with a lookup per tile. (As
+    // that load is conditional, taking a number out of the register still waits
+    // for the loads before it.)
     int pages;
     bool bad;               // a page was outside the pool
 

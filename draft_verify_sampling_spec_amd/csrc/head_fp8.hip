@@ -154,16 +154,22 @@ struct LogitArgs {
 // codes streamed through an LDS ring of two blocks of 128 channels by
 // buffer-to-LDS loads (with three blocks fewer workgroups fit a CU: one row took
 // 78 us against 68, 48 rows 100 against 92). A row's 128 bytes are eight chunks
-// of 16; chunk c of row i lies at position c ^ (i & 7), so that the eight lanes
-// that read one chunk column at a time touch all banks (the loads choose their
-// global chunk accordingly; LDS itself is filled linearly).
+// of 16; chunk c of row i lies at position c ^ (i & 7), so that eight rows at one
+// chunk column use eight positions (the loads choose their global chunk
+// accordingly; LDS itself is filled linearly). Rows are half a sweep of the banks
+// apart, so even rows meet in one half and odd ones in the other, and a fragment's
+// read takes twice the cycles it could: SQ_LDS_BANK_CONFLICT is half of
+// SQ_LDS_IDX_ACTIVE, 3.8 and 4.0 cycles an LDS instruction for 48 and 2,560 rows
+// under 151,936 x 2,560. (head_stats.hip's c ^ ((i / 2) % 8) has next to none.)
 //
 // kF8: 8-bit matrix instructions with both scales as their operands, for bf16
 // logits. Otherwise the codes are decoded to bf16 (exact, scales included) in
 // registers and multiplied in bf16, for fp32 logits: the 8-bit instructions
 // keep a sum of products only to about 2^-17 of its terms (relative error
 // 1.4e-5 of a row's norm, measured at 128, 2,560 and 10,240 channels): under a
-// two-hundredth of a bf16 rounding, but two hundred fp32 ones.
+// two-hundredth of a bf16 rounding, but two hundred fp32 ones. 2,560 rows of fp32
+// logits under 151,936 x 2,560 take 1,730 us (a large bf16 product's rate: 1,414);
+// every wavefront decodes what it reads.
 template <int TV_, int TR_, int WV_, int WR_, bool kF8_, typename O_>
 struct Cfg {
     static constexpr int TV = TV_, TR = TR_, WV = WV_, WR = WR_;
@@ -386,7 +392,7 @@ void launch_logits(const LogitArgs& a, hipStream_t s) {
 // bf16 logits of many rows and columns, 8-bit products: tiles of 256 x 256 by
 // four wavefronts, one a SIMD, of 128 x 128 each, so that a fragment read from
 // LDS serves four products (with eight wavefronts of 128 x 64 LDS is as busy as
-// the matrix cores). The accumulators are 256 registers, and the fragments are
+// the matrix cores, conflicts included). The accumulators are 256 registers, and the fragments are
 // held twice:
 //  - A stage (128 channels) has two phases, one half of its channels each. While
 //    a phase's 16 products run, the next phase's fragments are read; in the
@@ -397,11 +403,12 @@ void launch_logits(const LogitArgs& a, hipStream_t s) {
 // A workgroup goes through its tiles without a break: the next tile's first
 // stages are under way while one ends, and its outputs go straight from the
 // registers.
-// 2,560 rows x 151,936 columns x 2,560 channels: 930 us (logits_kernel's 256 x
-// 256 tiles: 1,005), 8,192 of each: 404 (450). Products alone take 67 % of the
-// loop's time at 1.9 GHz; 140 of the 930 us are the outputs' 778 MB, which all
-// workgroups write at the same time (788 without them; not waiting for a tile's
-// stores before the next one's second stage measured 921).
+// 2,560 rows x 151,936 columns x 2,560 channels: 945..965 us (logits_kernel's 256
+// x 256 tiles: 1,005), 8,192 of each: 403 (450). Products alone take two thirds of
+// the loop's time at 1.9 GHz; 140 us are the outputs' 778 MB, which all workgroups
+// write at the same time (788 of 930 without them, with a stage's wait that cost 1
+// % less but counted on the number of loads that the compiler makes; with that
+// one, not waiting for a tile's stores before the next one's second stage 921).
 struct Large {
     static constexpr int T = 256, kWaves = 4, M = 4;        // tile, wavefronts, 32 x 32 tiles of a wave
     static constexpr int kLoads = 2 * T / 8 / kWaves, kStageBytes = 2 * T * kBlock;
@@ -613,8 +620,9 @@ void launch_large(const LogitArgs& a, hipStream_t s) {
 // Tiles by the number of rows and columns. Up to 64 rows the head's bytes
 // decide and the tile is as narrow as its rows. Above, the tile whose rounds of
 // workgroups take least: a round of 256 x 256 tiles (one workgroup per CU) as
-// the unit, one of 128 x 128 tiles (two) measured 0.62 to 0.7 of it and three of
-// 64 x 64 tiles per CU 0.375 to 0.4. (20,000 columns x 5,120 channels, bf16: 300
+// the unit, one of 128 x 128 tiles (two) measured 0.62 to 0.7 of it and one of 64
+// x 64 tiles, counted as three per CU, 0.375 to 0.4 (since the rings have two
+// stages five are resident; the rule was measured with what it counts). (20,000 columns x 5,120 channels, bf16: 300
 // rows take 53, 44, 71 us with them, 700 rows 63, 81, 136; 151,936 columns x
 // 2,560, 160 rows 126, 139, -; 2,560 columns x 4,096, 1,024 rows 44, 31, 28. The
 // rule's choice was the least, or within 4 % of it, at 11 sizes in either type.)

@@ -545,8 +545,11 @@ int spec_verify_cache_read(const void* cache, const int32_t* page_table, const i
  * [max(0, p - window + 1), p] (window 0: [0, p]); query head i reads kv head
  * i / (q_heads / kv_heads):
  *   out = sum_j softmax_j(scale q . k_j) v_j.
- * Products accumulate in fp32, the softmax's statistics are fp32. A NaN group
- * of a key or value reaches exactly the rows that see its token. K = 0 is the
+ * Products accumulate in fp32, the softmax's statistics are fp32. The weights,
+ * up to 2^8 under a reference that lags behind the maximum, are rounded to bf16
+ * for the product with the values, not for their sum (so equal values come back
+ * within that rounding); weighted sums past fp32's range give infinities or NaN.
+ * A NaN group of a key or value reaches exactly the rows that see its token. K = 0 is the
  * single-token form. Stream-ordered, no host sync, one launch, or two when the
  * contexts may be split over workgroups (a choice by the shapes alone; how they
  * are split is decided on the device by all requests' lengths and budgets, so
@@ -557,8 +560,10 @@ int spec_verify_cache_read(const void* cache, const int32_t* page_table, const i
  *   B, K         requests (0..SV_MAX_BATCH; 0 is a no-op), drafted tokens
  *                (0..SV_MAX_K).
  *   q_heads      a multiple of kv_heads, up to SV_MAX_HEADS.
- *   scale        finite; usually 1 / sqrt(head_dim). Scores scale log2(e) q . k
- *                past fp32's range give NaN.
+ *   scale        finite; usually 1 / sqrt(head_dim). |scale| log2(e) is held
+ *                within fp32's normal numbers. A score scale log2(e) q . k above
+ *                fp32's range gives NaN; positions whose score is below it have
+ *                no weight (NaN where a row sees no other).
  *   window       0, or the number of positions a row sees, its own included.
  *                Pages wholly before every row's window are not needed, and
  *                positions before it need never have been written.
