@@ -395,3 +395,41 @@ def test_an_empty_slot_stays_empty_over_steps():
     assert bool((cache.pool[4:] == 77).all()) and cache.pool[:4].any()
     assert verify.status() == 0
     verify.close()
+
+
+@pytest.mark.parametrize("B,K,Hq,Hkv,D,width", [(16384, 0, 4, 2, 64, 600), (2000, 32, 16, 2, 128, 1200),
+                                                (3000, 5, 8, 4, 256, 800)])
+def test_many_short_requests_under_a_wide_page_table(B, K, Hq, Hkv, D, width):
+    """Tens of thousands of units that are cut on the device because the table
+    would allow long ones: empty slots among them, every request like the one a
+    period before it."""
+    _log(f"[attend] {B} short requests, table of {width} pages, K={K} D={D}")
+    period, page = 61, 64
+    g = torch.Generator(device=DEV).manual_seed(B)
+    cache = BlockCache(DEV, 4, Hkv, D, page)
+    cache.pool.random_(0, 256, generator=g)
+    cache.pool[..., 32 * D:].random_(122, 129, generator=g)
+    at = torch.arange(B, device=DEV) % period
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    table[:, :4] = torch.stack([(at + i) % 4 for i in range(4)], 1).int()
+    ctx = (at * 3 - 2).int()                               # -2 .. 178, in turn
+    budgets = (at % (K + 1)).int()
+    q = torch.randn(period, K + 1, Hq, D, generator=g, device=DEV).bfloat16()
+    q = q.repeat(B // period + 1, 1, 1, 1)[:B].contiguous()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    assert sb.spec_verify_attention_workspace_bytes(B, K, Hq, Hkv, D, page, width, 0) > 256
+    got = cache.attend(q, table, ctx, budgets, status=status)
+    assert int(status) == 0
+    for b0 in (0, B - period):
+        part = slice(b0, b0 + period)
+        ta._check_on_gpu(cache, q[part], got[part], table[part, :4].contiguous(), ctx[part].tolist(), budgets[part].tolist())
+    # Every other request against the same one of the first period: two results
+    # that are each off by test_gpu_attention's bound, in which the largest value
+    # bounds the weights' sum of |v| and the output, and with the largest sum of
+    # |q| every score's reach.
+    top = 6.0 * 2.0 ** (128 - 127)
+    reach = top * float(q[:period].float().abs().sum(-1).max()) * D ** -0.5
+    each = (2.0 ** -8 * (2 + 2.0 ** -7) + 2 * (D + 2) * 2.0 ** -24 * reach + 2.0 ** -20 * (1 + 256 / 4096)) * top
+    assert bool(((got.float() - got[:period][at].float()).abs() <= 2 * each).all())
+    live = torch.arange(K + 1, device=DEV) <= torch.where(ctx < 0, -1, budgets)[:, None]
+    assert bool((got.flatten(2).abs().amax(2) > 0).eq(live).all())
