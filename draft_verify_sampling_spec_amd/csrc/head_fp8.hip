@@ -392,8 +392,8 @@ void launch_logits(const LogitArgs& a, hipStream_t s) {
 // bf16 logits of many rows and columns, 8-bit products: tiles of 256 x 256 by
 // four wavefronts, one a SIMD, of 128 x 128 each, so that a fragment read from
 // LDS serves four products (with eight wavefronts of 128 x 64 LDS is as busy as
-// the matrix cores, conflicts included). The accumulators are 256 registers, and the fragments are
-// held twice:
+// the matrix cores, conflicts included). The accumulators are 256 registers, and
+// the fragments are held twice:
 //  - A stage (128 channels) has two phases, one half of its channels each. While
 //    a phase's 16 products run, the next phase's fragments are read; in the
 //    second the place in LDS that has been read is filled with the stage after
@@ -406,9 +406,9 @@ void launch_logits(const LogitArgs& a, hipStream_t s) {
 // 2,560 rows x 151,936 columns x 2,560 channels: 945..965 us (logits_kernel's 256
 // x 256 tiles: 1,005), 8,192 of each: 403 (450). Products alone take two thirds of
 // the loop's time at 1.9 GHz; 140 us are the outputs' 778 MB, which all workgroups
-// write at the same time (788 of 930 without them, with a stage's wait that cost 1
-// % less but counted on the number of loads that the compiler makes; with that
-// one, not waiting for a tile's stores before the next one's second stage 921).
+// write at the same time. (Measured with a wait for a stage that took 1 % less but
+// counted on how many loads the compiler makes: 930, without the outputs 788, and
+// 921 without waiting for a tile's stores before the next one's second stage.)
 struct Large {
     static constexpr int T = 256, kWaves = 4, M = 4;        // tile, wavefronts, 32 x 32 tiles of a wave
     static constexpr int kLoads = 2 * T / 8 / kWaves, kStageBytes = 2 * T * kBlock;
@@ -622,8 +622,8 @@ void launch_large(const LogitArgs& a, hipStream_t s) {
 // workgroups take least: a round of 256 x 256 tiles (one workgroup per CU) as
 // the unit, one of 128 x 128 tiles (two) measured 0.62 to 0.7 of it and one of 64
 // x 64 tiles, counted as three per CU, 0.375 to 0.4 (since the rings have two
-// stages five are resident; the rule was measured with what it counts). (20,000 columns x 5,120 channels, bf16: 300
-// rows take 53, 44, 71 us with them, 700 rows 63, 81, 136; 151,936 columns x
+// stages five are resident; the rule was measured with what it counts). (20,000
+// columns x 5,120 channels, bf16: 300 rows take 53, 44, 71 us with them, 700 rows 63, 81, 136; 151,936 columns x
 // 2,560, 160 rows 126, 139, -; 2,560 columns x 4,096, 1,024 rows 44, 31, 28. The
 // rule's choice was the least, or within 4 % of it, at 11 sizes in either type.)
 template <bool kF8, typename O>

@@ -549,9 +549,9 @@ int spec_verify_cache_read(const void* cache, const int32_t* page_table, const i
  * up to 2^8 under a reference that lags behind the maximum, are rounded to bf16
  * for the product with the values, not for their sum (so equal values come back
  * within that rounding); weighted sums past fp32's range give infinities or NaN.
- * A NaN group of a key or value reaches exactly the rows that see its token. K = 0 is the
- * single-token form. Stream-ordered, no host sync, one launch, or two when the
- * contexts may be split over workgroups (a choice by the shapes alone; how they
+ * A NaN group of a key or value reaches exactly the rows that see its token.
+ * K = 0 is the single-token form. Stream-ordered, no host sync, one launch, or
+ * two when the contexts may be split over workgroups (a choice by the shapes alone; how they
  * are split is decided on the device by all requests' lengths and budgets, so
  * the order of a request's sums may depend on what else is in the batch).
  *   queries      bf16 [B, K+1, q_heads, head_dim] (device, 16-byte aligned),
