@@ -38,6 +38,8 @@ SV_FLAG_BAD_TOKEN = 0x2
 SV_FLAG_SYNC_TIMEOUT = 0x4
 SV_FLAG_BAD_LENGTH = 0x8
 SV_FLAG_BAD_PAGE = 0x10
+SV_FLAG_NO_PAGES = 0x20
+SV_FLAG_BAD_PARENT = 0x40
 
 SV_MAX_BATCH = 16384
 SV_MAX_K = 32
@@ -69,6 +71,9 @@ EXPORTED = (
     "spec_verify_cache_bytes",
     "spec_verify_cache_write",
     "spec_verify_cache_read",
+    "spec_verify_pages_plan",
+    "spec_verify_pages_plan_workspace_bytes",
+    "spec_verify_cache_write_rotated",
     "spec_verify_attention",
     "spec_verify_attention_workspace_bytes",
     "spec_head_quantize",
@@ -136,6 +141,16 @@ def _declare(lib):
     lib.spec_verify_cache_read.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
                                            _vp, _vp, _vp, _vp]
     lib.spec_verify_cache_read.restype = _i
+    lib.spec_verify_pages_plan.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
+                                           _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.spec_verify_pages_plan.restype = _i
+    lib.spec_verify_pages_plan_workspace_bytes.argtypes = [_i, _i, _i]
+    lib.spec_verify_pages_plan_workspace_bytes.restype = ctypes.c_size_t
+    lib.spec_verify_cache_write_rotated.argtypes = [
+        _vp, _vp, _vp, _i, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _vp, _vp, ctypes.c_int64,
+        _vp, _i, _i, ctypes.c_float, _vp, _vp, _i, ctypes.c_float, _i, _i, _i, _i, _i, _vp, _vp, _vp,
+        _vp, _vp]
+    lib.spec_verify_cache_write_rotated.restype = _i
     lib.spec_verify_attention.argtypes = [_vp, ctypes.c_int64, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
                                           _i, _i, _i, _i, ctypes.c_float, _i, _vp, _vp, _vp,
                                           ctypes.c_size_t, _vp]
@@ -635,6 +650,31 @@ def spec_verify_cache_read(cache, page_table, starts, lens, B, T, kv_heads, head
                                          out_keys, out_values, out_status, stream)
 
 
+def spec_verify_pages_plan(page_table, page_refs, ctx_lens, budgets, parents, prefix_lens, B, T,
+                           page_size, max_pages, num_pages, window, sinks, out_starts, out_slots,
+                           out_positions, out_status, workspace, workspace_bytes, stream) -> int:
+    return load().spec_verify_pages_plan(page_table, page_refs, ctx_lens, budgets, parents,
+                                         prefix_lens, B, T, page_size, max_pages, num_pages, window,
+                                         sinks, out_starts, out_slots, out_positions, out_status,
+                                         workspace, workspace_bytes, stream)
+
+
+def spec_verify_pages_plan_workspace_bytes(B: int, max_pages: int, num_pages: int) -> int:
+    return int(load().spec_verify_pages_plan_workspace_bytes(int(B), int(max_pages),
+                                                             int(num_pages)))
+
+
+def spec_verify_cache_write_rotated(queries, keys, values, dtype, query_stride, key_stride,
+                                    value_stride, slots, positions, tokens, inv_freq, rot,
+                                    interleaved, factor, q_norm, k_norm, norm_dtype, eps, q_heads,
+                                    kv_heads, head_dim, page_size, num_pages, cache, out_queries,
+                                    out_keys, out_status, stream) -> int:
+    return load().spec_verify_cache_write_rotated(
+        queries, keys, values, dtype, query_stride, key_stride, value_stride, slots, positions,
+        tokens, inv_freq, rot, interleaved, factor, q_norm, k_norm, norm_dtype, eps, q_heads,
+        kv_heads, head_dim, page_size, num_pages, cache, out_queries, out_keys, out_status, stream)
+
+
 def spec_verify_attention(queries, query_stride, cache, page_table, ctx_lens, budgets, B, K,
                           q_heads, kv_heads, head_dim, page_size, max_pages, num_pages, scale,
                           window, out, out_status, workspace, workspace_bytes, stream) -> int:
@@ -788,6 +828,69 @@ class BlockCache:
         if rc != SV_OK:
             _check(rc, "spec_verify_cache_write")
 
+    def write_rotated(self, queries, keys, values, slots, positions, inv_freq=None, q_norm=None,
+                      k_norm=None, eps: float = 1e-6, interleaved: bool = False,
+                      factor: float = 1.0, out=None, out_keys=None, status=None, stream=None):
+        """Normalise (weights q_norm, k_norm [head_dim], float32 or bfloat16;
+        None: not) and rotate (inv_freq float32 [rot / 2], rot a multiple of 16;
+        None: not) the queries [B, T, q_heads, head_dim] and keys [B, T, kv_heads,
+        head_dim] of a step, float32 or bfloat16, at ``positions`` int32 [B, T];
+        returns the queries (bfloat16), and quantises keys and values into the
+        cache at ``slots`` int32 [B, T] (both from ``PageTables.plan``). Pairs are
+        the channels i and i + rot / 2, or with ``interleaved`` 2 i and 2 i + 1;
+        cosine and sine are multiplied by ``factor``. ``out_keys``, if given,
+        receives the rotated keys in bfloat16. Tokens with a negative slot are
+        skipped: ``out`` keeps its values there (a fresh one is zero)."""
+        index = self._index
+        if stream is not None:
+            with _other_stream(stream, index):
+                return self.write_rotated(queries, keys, values, slots, positions, inv_freq, q_norm,
+                                          k_norm, eps, interleaved, factor, out, out_keys, status)
+        if _current_device() != index:
+            with torch.cuda.device(index):
+                return self.write_rotated(queries, keys, values, slots, positions, inv_freq, q_norm,
+                                          k_norm, eps, interleaved, factor, out, out_keys, status)
+        shape, kv = queries.shape, keys.shape
+        if len(shape) != 4 or shape[3] != self.head_dim or shape[2] % self.kv_heads != 0 \
+                or kv != (shape[0], shape[1], self.kv_heads, self.head_dim) or values.shape != kv:
+            raise ValueError(f"queries must be [B, T, q_heads, {self.head_dim}] and keys and values "
+                             f"[B, T, {self.kv_heads}, {self.head_dim}]")
+        dtype = _DTYPES.get(queries.dtype)
+        if dtype is None or keys.dtype is not queries.dtype or values.dtype is not queries.dtype:
+            raise ValueError("queries, keys and values must share their type, float32 or bfloat16")
+        B, T, heads, dim = shape
+        rot = 0
+        if inv_freq is not None:
+            rot = 2 * inv_freq.numel()
+            if rot % 16 != 0 or rot > dim:
+                raise ValueError(f"inv_freq must have a multiple of 8 entries, at most {dim // 2}, "
+                                 f"got {inv_freq.numel()}")
+            inv_freq = _need(inv_freq, "inv_freq", torch.float32, (rot // 2,), index)
+        norms, norm_dtype = [None, None], 0
+        for i, w in enumerate((q_norm, k_norm)):
+            if w is not None:
+                code = _DTYPES.get(w.dtype)
+                if code is None or (norms[0] is not None and code != norm_dtype):
+                    raise ValueError("q_norm and k_norm must share their type, float32 or bfloat16")
+                norm_dtype = code
+                norms[i] = _need(w, "k_norm" if i else "q_norm", w.dtype, (dim,), index)
+        if out is None:
+            out = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+        rc = load().spec_verify_cache_write_rotated(
+            queries.data_ptr(), keys.data_ptr(), values.data_ptr(), dtype,
+            _token_stride(queries, "queries", index), _token_stride(keys, "keys", index),
+            _token_stride(values, "values", index), _need(slots, "slots", torch.int32, (B, T), index),
+            _need(positions, "positions", torch.int32, (B, T), index), B * T, inv_freq, rot,
+            1 if interleaved else 0, factor, norms[0], norms[1], norm_dtype, eps, heads,
+            self.kv_heads, dim, self.page_size, self.num_pages, self._pool_ptr(),
+            _need(out, "out", torch.bfloat16, shape, index),
+            None if out_keys is None else _need(out_keys, "out_keys", torch.bfloat16, kv, index),
+            None if status is None else _need(status, "status", torch.int32, (1,), index),
+            _raw_stream(index))
+        if rc != SV_OK:
+            _check(rc, "spec_verify_cache_write_rotated")
+        return out
+
     def read(self, page_table, starts, lens, length: int, dtype=torch.bfloat16, out=None,
              status=None, stream=None):
         """The keys and values [B, length, kv_heads, head_dim] of positions
@@ -870,6 +973,90 @@ class BlockCache:
         if rc != SV_OK:
             _check(rc, "spec_verify_attention")
         return out
+
+
+class PageTables:
+    """Which pages of a pool every slot of a batch holds: ``table`` (int32 [B,
+    max_pages], -1 where there is none) and ``refs`` (int32 [num_pages], how many
+    entries hold each page), both on the device and changed by ``plan`` only.
+    One object serves the caches of all layers, whose pools it numbers alike.
+    ``table`` and ``refs`` may be given to go on from a state of their own.
+
+    Calls are enqueued on ``stream`` (default: the current torch stream) and not
+    waited for; ``status`` as in ``BlockCache``."""
+
+    def __init__(self, device, B: int, max_pages: int, num_pages: int, page_size: int = 64,
+                 table: torch.Tensor | None = None, refs: torch.Tensor | None = None):
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("PageTables needs a GPU device")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.device, self._index = device, device.index
+        self.B, self.max_pages = int(B), int(max_pages)
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        self._bytes = spec_verify_pages_plan_workspace_bytes(max(self.B, 1), max_pages, num_pages)
+        if self._bytes == 0 or self.B < 0 or self.num_pages * self.page_size >= 1 << 31 \
+                or spec_verify_cache_bytes(num_pages, 1, 64, page_size) == 0 \
+                or self.max_pages * self.page_size > SV_MAX_CONTEXT:
+            raise ValueError(f"bad page tables: {B} rows of {max_pages} pages out of {num_pages} "
+                             f"of {page_size} tokens")
+        self.table = torch.full((self.B, self.max_pages), -1, dtype=torch.int32, device=device) \
+            if table is None else table
+        self.refs = torch.zeros(self.num_pages, dtype=torch.int32, device=device) \
+            if refs is None else refs
+        self._state()
+
+    def _state(self):
+        return (_need(self.table, "table", torch.int32, (self.B, self.max_pages), self._index),
+                _need(self.refs, "refs", torch.int32, (self.num_pages,), self._index))
+
+    def plan(self, ctx_lens, budgets=None, length: int = 1, window: int = 0, sinks: int = 0,
+             parents=None, prefix_lens=None, out=None, status=None, stream=None):
+        """One step: gives back the pages that a request no longer needs for
+        positions 0 .. ctx_lens[b] + budgets[b] (budgets None: length - 1; under a
+        ``window`` the first ``sinks`` positions and those of the window), takes
+        what is missing from the parent's row or from the free pages. Returns
+        (starts int32 [B]: ctx_lens, -1 where the request cannot run; slots int32
+        [B, length] and positions int32 [B, length] of its tokens, -1 behind its
+        budget)."""
+        index = self._index
+        if stream is not None:
+            with _other_stream(stream, index):
+                return self.plan(ctx_lens, budgets, length, window, sinks, parents, prefix_lens, out,
+                                 status)
+        if _current_device() != index:
+            with torch.cuda.device(index):
+                return self.plan(ctx_lens, budgets, length, window, sinks, parents, prefix_lens, out,
+                                 status)
+        B, T = self.B, int(length)
+        if not 1 <= T <= SV_MAX_CONTEXT or not 0 <= window <= 0x7fffffff or not 0 <= sinks <= 0x7fffffff:
+            raise ValueError(f"length must be 1..2^24, window and sinks 0..2^31 - 1, got {length}, "
+                             f"{window}, {sinks}")
+        if parents is not None and prefix_lens is None:
+            raise ValueError("parents need prefix_lens")
+        if out is None:
+            device = self.device
+            out = (torch.empty_strided((B,), (1,), dtype=torch.int32, device=device),
+                   torch.empty_strided((B, T), (T, 1), dtype=torch.int32, device=device),
+                   torch.empty_strided((B, T), (T, 1), dtype=torch.int32, device=device))
+        workspace = torch.empty_strided((self._bytes,), (1,), dtype=torch.uint8, device=self.device)
+        table, refs = self._state()
+        rows = (B,)
+        rc = load().spec_verify_pages_plan(
+            table, refs, _need(ctx_lens, "ctx_lens", torch.int32, rows, index),
+            None if budgets is None else _need(budgets, "budgets", torch.int32, rows, index),
+            None if parents is None else _need(parents, "parents", torch.int32, rows, index),
+            None if parents is None else _need(prefix_lens, "prefix_lens", torch.int32, rows, index),
+            B, T, self.page_size, self.max_pages, self.num_pages, window, sinks,
+            _need(out[0], "out starts", torch.int32, rows, index),
+            _need(out[1], "out slots", torch.int32, (B, T), index),
+            _need(out[2], "out positions", torch.int32, (B, T), index),
+            None if status is None else _need(status, "status", torch.int32, (1,), index),
+            workspace.data_ptr(), self._bytes, _raw_stream(index))
+        if rc != SV_OK:
+            _check(rc, "spec_verify_pages_plan")
+        return out[0], out[1], out[2]
 
 
 def head_quantize(x: torch.Tensor, block_rows: int = 1, out=None, stream=None):

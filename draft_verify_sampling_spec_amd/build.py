@@ -6,6 +6,8 @@ compiles ``csrc/spec_verify.hip`` (verification), ``csrc/budget_schedule.hip``
 statistics), ``csrc/verify_hidden.hip`` (verification from hidden states),
 ``csrc/markov_draft.hip`` (the drafter's low-rank Markov head),
 ``csrc/block_cache.hip`` (the paged 4-bit key/value cache),
+``csrc/page_tables.hip`` (its page tables from the requests' lengths),
+``csrc/rotate_write.hip`` (normalised and rotated heads on their way into it),
 ``csrc/block_attention.hip`` (attention of drafted blocks over it) and
 ``csrc/head_fp8.hip`` (the output head in 8-bit floating point) into
 ``libspec_verify.so`` next to this file.
@@ -25,6 +27,8 @@ SOURCES = [SRC, os.path.join(PKG_DIR, "csrc", "budget_schedule.hip"),
            os.path.join(PKG_DIR, "csrc", "verify_hidden.hip"),
            os.path.join(PKG_DIR, "csrc", "markov_draft.hip"),
            os.path.join(PKG_DIR, "csrc", "block_cache.hip"),
+           os.path.join(PKG_DIR, "csrc", "page_tables.hip"),
+           os.path.join(PKG_DIR, "csrc", "rotate_write.hip"),
            os.path.join(PKG_DIR, "csrc", "block_attention.hip"),
            os.path.join(PKG_DIR, "csrc", "head_fp8.hip")]
 INCLUDE = os.path.join(ROOT, "include")

@@ -93,6 +93,9 @@ enum sv_status {
                                    row (or an output); it was skipped */
 #define SV_FLAG_BAD_PAGE 0x10u  /* a page number that a call needed was outside
                                    the pool; its tokens were skipped */
+#define SV_FLAG_NO_PAGES 0x20u  /* too few free pages: some request got none */
+#define SV_FLAG_BAD_PARENT 0x40u /* a parent outside the batch, or one that has a
+                                   parent itself; treated as none */
 
 /* Library limits. */
 #define SV_MAX_BATCH 16384
@@ -518,6 +521,106 @@ int spec_verify_cache_write(const void* keys, const void* values, int dtype, int
                             const int32_t* ctx_lens, const int32_t* budgets, int B, int T,
                             int kv_heads, int head_dim, int page_size, int max_pages,
                             int num_pages, void* cache, int32_t* out_status, void* stream);
+
+/*
+ * spec_verify_pages_plan -- one step of the page tables: from the requests'
+ * lengths, which pages every request holds, and where its new tokens go. The
+ * caller keeps two arrays, which the call changes: the page table, and for every
+ * page of the pool the number of table entries that hold it (0: free).
+ * Page i of request b is needed if it holds a position of [0, ctx_lens[b] +
+ * budgets[b] + 1) that, with window > 0, is below `sinks` or at or behind
+ * ctx_lens[b] - window + 1 (what spec_verify_attention_sinks reads in this and
+ * later steps). Pages held and not needed are given back: an empty slot (a
+ * negative length) gives back all, and a slot is emptied by one call before
+ * another request takes it. Needed pages not held come from the parent's row, or
+ * are the lowest-numbered free ones, dealt out in the order of requests and of
+ * positions in each. A request whose new pages, with those of all requests
+ * before it, are more than there are free gets none of them
+ * (SV_FLAG_NO_PAGES). A function of the arguments alone. Stream-ordered, no
+ * host sync.
+ *   page_table   int32 [B, max_pages] (device), changed: entries in [0,
+ *                num_pages) are held; others are none and become -1 (those
+ *                >= num_pages with SV_FLAG_BAD_PAGE). At first: all -1.
+ *   page_refs    int32 [num_pages] (device), changed. At first: all 0. 0 or
+ *                less is free. num_pages * page_size is at most 2^31 - 1.
+ *   parents, prefix_lens  int32 [B] (device) or NULL: request b takes the
+ *                pages of its parent's first prefix_lens[b] tokens (whole
+ *                pages; a length of 0 or less: none) where it holds none
+ *                itself, as the parent's row was before the call. Negative:
+ *                no parent. A parent has none itself (SV_FLAG_BAD_PARENT).
+ *                Tokens in shared pages are not to be written again.
+ *   T            the block's width, 1..SV_MAX_CONTEXT; B 0..SV_MAX_BATCH.
+ *   out_starts   int32 [B] (device): ctx_lens[b] where the request's pages are
+ *                all there, else -1 (an empty slot, no pages, or a block that
+ *                does not fit its row, which then stays as it is, with
+ *                SV_FLAG_BAD_LENGTH). Serves as ctx_lens of the other calls.
+ *   out_slots    int32 [B, T] (device): page * page_size + position in the
+ *                page of token t, or -1 for t > budgets[b] and where
+ *                out_starts is -1.
+ *   out_positions  int32 [B, T] (device): out_starts[b] + t, or -1 likewise.
+ *   workspace    device scratch of at least
+ *                spec_verify_pages_plan_workspace_bytes() bytes (256-byte
+ *                aligned), caller-owned, its contents of no account; calls
+ *                that share it must not overlap.
+ * Errors (nothing enqueued): SV_ERR_ARG, SV_ERR_NULL, SV_ERR_ALIGN;
+ * SV_ERR_HIP if a launch fails.
+ */
+int spec_verify_pages_plan(int32_t* page_table, int32_t* page_refs, const int32_t* ctx_lens,
+                           const int32_t* budgets, const int32_t* parents,
+                           const int32_t* prefix_lens, int B, int T, int page_size, int max_pages,
+                           int num_pages, int window, int sinks, int32_t* out_starts,
+                           int32_t* out_slots, int32_t* out_positions, int32_t* out_status,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* spec_verify_pages_plan_workspace_bytes -- scratch spec_verify_pages_plan
+ * needs; 0 on bad arguments. Host only. */
+size_t spec_verify_pages_plan_workspace_bytes(int B, int max_pages, int num_pages);
+
+/*
+ * spec_verify_cache_write_rotated -- a step's projections on their way into the
+ * attention: queries and keys normalised per head and rotated to their
+ * positions, queries stored, keys and values quantised into the cache. Token n
+ * goes to slots[n]; a negative slot skips it (nothing read, nothing written).
+ * Per query or key head of D channels:
+ *   y = x / sqrt(mean(x^2) + eps) * w   (y = x where the weights are NULL)
+ * and its first `rot` channels are turned in pairs by a = positions[n] *
+ * inv_freq[i]: (y_i, y_j) -> factor (y_i cos a - y_j sin a, y_j cos a + y_i
+ * sin a), with j = i + rot / 2, or, interleaved, channels 2 i and 2 i + 1.
+ * Sums, products, sine and cosine are fp32, the angle's fraction of a turn is
+ * right to 2^-29 for |position| <= 2^24 and frequencies up to 1; magnitudes
+ * whose squares' sum leaves fp32's range are not normalised rightly. Queries
+ * are rounded to bf16 once; keys are rounded to bf16 and then quantised, so
+ * that the cache's bytes are those of spec_verify_cache_write on out_keys.
+ * Stream-ordered, one launch.
+ *   queries, keys, values  of type dtype: [tokens, q_heads (kv_heads),
+ *                head_dim] (device, 16-byte aligned), the heads contiguous,
+ *                `*_stride` elements between tokens (a multiple of 16 bytes; a
+ *                slice of a fused projection's rows is taken as it is).
+ *   slots, positions  int32 [tokens] (device), as spec_verify_pages_plan gives
+ *                them. A slot outside the pool is skipped with SV_FLAG_BAD_PAGE.
+ *   tokens       0 (a no-op) .. 2^31 - 1.
+ *   inv_freq     float [rot / 2] (device; NULL if rot is 0).
+ *   rot          0..head_dim, a multiple of 16.
+ *   factor       finite; usually 1.
+ *   q_norm, k_norm  [head_dim] of type norm_dtype (device, 16-byte aligned) or
+ *                NULL; eps finite, at least 0.
+ *   out_queries  bf16 [tokens, q_heads, head_dim]; out_keys bf16 [tokens,
+ *                kv_heads, head_dim] or NULL (device, 16-byte aligned). Rows of
+ *                skipped tokens keep their values.
+ * kv_heads, head_dim, page_size, num_pages, cache, out_status as above;
+ * num_pages * page_size is at most 2^31 - 1.
+ * Errors (nothing enqueued): SV_ERR_ARG, SV_ERR_DTYPE, SV_ERR_NULL,
+ * SV_ERR_ALIGN; SV_ERR_HIP if the launch fails.
+ */
+int spec_verify_cache_write_rotated(const void* queries, const void* keys, const void* values,
+                                    int dtype, int64_t query_stride, int64_t key_stride,
+                                    int64_t value_stride, const int32_t* slots,
+                                    const int32_t* positions, int64_t tokens,
+                                    const float* inv_freq, int rot, int interleaved, float factor,
+                                    const void* q_norm, const void* k_norm, int norm_dtype,
+                                    float eps, int q_heads, int kv_heads, int head_dim,
+                                    int page_size, int num_pages, void* cache, void* out_queries,
+                                    void* out_keys, int32_t* out_status, void* stream);
 
 /*
  * spec_verify_cache_read -- read tokens back as the values their codes stand
