@@ -76,6 +76,8 @@ EXPORTED = (
     "spec_verify_cache_write_rotated",
     "spec_verify_attention",
     "spec_verify_attention_workspace_bytes",
+    "spec_verify_attention_sinks",
+    "spec_verify_attention_sinks_workspace_bytes",
     "spec_head_quantize",
     "spec_head_logits",
     "spec_verify_free",
@@ -155,6 +157,12 @@ def _declare(lib):
                                           _i, _i, _i, _i, ctypes.c_float, _i, _vp, _vp, _vp,
                                           ctypes.c_size_t, _vp]
     lib.spec_verify_attention.restype = _i
+    lib.spec_verify_attention_sinks.argtypes = [
+        _vp, ctypes.c_int64, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.c_float, _i, _i,
+        _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.spec_verify_attention_sinks.restype = _i
+    lib.spec_verify_attention_sinks_workspace_bytes.argtypes = [_i] * 9
+    lib.spec_verify_attention_sinks_workspace_bytes.restype = ctypes.c_size_t
     lib.spec_verify_attention_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i, _i]
     lib.spec_verify_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.spec_head_quantize.argtypes = [_vp, _i, _i, _i, _i, _vp, _vp, _vp]
@@ -692,6 +700,25 @@ def spec_verify_attention_workspace_bytes(B: int, K: int, q_heads: int, kv_heads
         int(max_pages), int(window)))
 
 
+def spec_verify_attention_sinks(queries, query_stride, cache, page_table, ctx_lens, budgets, B, K,
+                                q_heads, kv_heads, head_dim, page_size, max_pages, num_pages,
+                                scale, window, sinks, out, out_status, workspace, workspace_bytes,
+                                stream) -> int:
+    return load().spec_verify_attention_sinks(queries, query_stride, cache, page_table, ctx_lens,
+                                              budgets, B, K, q_heads, kv_heads, head_dim,
+                                              page_size, max_pages, num_pages, scale, window,
+                                              sinks, out, out_status, workspace, workspace_bytes,
+                                              stream)
+
+
+def spec_verify_attention_sinks_workspace_bytes(B: int, K: int, q_heads: int, kv_heads: int,
+                                                head_dim: int, page_size: int, max_pages: int,
+                                                window: int, sinks: int) -> int:
+    return int(load().spec_verify_attention_sinks_workspace_bytes(
+        int(B), int(K), int(q_heads), int(kv_heads), int(head_dim), int(page_size),
+        int(max_pages), int(window), int(sinks)))
+
+
 def spec_head_quantize(src, dtype, rows, H, block_rows, out_codes, out_scales, stream) -> int:
     return load().spec_head_quantize(src, dtype, rows, H, block_rows, out_codes, out_scales, stream)
 
@@ -717,6 +744,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 
 # A function of the shapes alone, for every layer and step: the last shapes' sizes.
 _attention_bytes = functools.lru_cache(maxsize=1024)(spec_verify_attention_workspace_bytes)
+_sinks_bytes = functools.lru_cache(maxsize=1024)(spec_verify_attention_sinks_workspace_bytes)
 
 
 def _need(t, name, dtype, shape, index):
@@ -928,21 +956,23 @@ class BlockCache:
         return out[0], out[1]
 
     def attend(self, queries, page_table, ctx_lens, budgets=None, scale: float | None = None,
-               window: int = 0, out=None, status=None, stream=None):
+               window: int = 0, out=None, status=None, stream=None, sinks: int = 0):
         """Attention of the blocks' rows, bfloat16 [B, K+1, q_heads, head_dim]
         (a slice of a fused projection's rows is fine), over the cache, which
         already holds the blocks' own tokens. ``scale`` None: head_dim ** -0.5.
+        Under a ``window`` a row sees that many positions up to its own, and the
+        first ``sinks`` ones.
         Rows behind budgets[b] and empty slots are left as ``out`` holds them;
         a fresh output is zero there."""
         index = self._index
         if stream is not None:
             with _other_stream(stream, index):
                 return self.attend(queries, page_table, ctx_lens, budgets, scale, window, out,
-                                   status)
+                                   status, sinks=sinks)
         if _current_device() != index:
             with torch.cuda.device(index):
                 return self.attend(queries, page_table, ctx_lens, budgets, scale, window, out,
-                                   status)
+                                   status, sinks=sinks)
         shape = queries.shape
         if len(shape) != 4 or queries.dtype is not torch.bfloat16 or shape[3] != self.head_dim \
                 or shape[1] < 1:
@@ -952,8 +982,16 @@ class BlockCache:
         B, T, heads, dim = shape
         stride = _token_stride(queries, "queries", index)
         table, width = self._table(page_table, B)
-        nbytes = _attention_bytes(max(B, 1), T - 1, heads, self.kv_heads, dim, self.page_size,
-                                  width, window)
+        if not 0 <= sinks <= 0x7fffffff:
+            raise ValueError(f"sinks must be 0..2^31 - 1, got {sinks}")
+        if sinks and window:
+            nbytes = _sinks_bytes(max(B, 1), T - 1, heads, self.kv_heads, dim, self.page_size, width,
+                                  window, sinks)
+            call, seen = load().spec_verify_attention_sinks, (window, sinks)
+        else:
+            nbytes = _attention_bytes(max(B, 1), T - 1, heads, self.kv_heads, dim, self.page_size,
+                                      width, window)
+            call, seen = load().spec_verify_attention, (window,)
         if nbytes == 0:
             raise ValueError(f"bad attention shape: B={B} K={T - 1} q_heads={heads} kv_heads="
                              f"{self.kv_heads} window={window} max_pages={width}")
@@ -961,12 +999,12 @@ class BlockCache:
             out = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
         workspace = self._no_parts if nbytes == 256 else torch.empty(
             nbytes, dtype=torch.uint8, device=self.device)
-        rc = load().spec_verify_attention(
+        rc = call(
             queries.data_ptr(), stride, self._pool_ptr(), table,
             _need(ctx_lens, "ctx_lens", torch.int32, (B,), index),
             None if budgets is None else _need(budgets, "budgets", torch.int32, (B,), index),
             B, T - 1, heads, self.kv_heads, dim, self.page_size, width, self.num_pages,
-            dim ** -0.5 if scale is None else scale, window,
+            dim ** -0.5 if scale is None else scale, *seen,
             _need(out, "out", torch.bfloat16, shape, index),
             None if status is None else _need(status, "status", torch.int32, (1,), index),
             workspace.data_ptr(), nbytes, _raw_stream(index))

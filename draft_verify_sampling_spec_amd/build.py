@@ -8,7 +8,8 @@ statistics), ``csrc/verify_hidden.hip`` (verification from hidden states),
 ``csrc/block_cache.hip`` (the paged 4-bit key/value cache),
 ``csrc/page_tables.hip`` (its page tables from the requests' lengths),
 ``csrc/rotate_write.hip`` (normalised and rotated heads on their way into it),
-``csrc/block_attention.hip`` (attention of drafted blocks over it) and
+``csrc/block_attention.hip`` (attention of drafted blocks over it),
+``csrc/sink_attention.hip`` (under a window with sink tokens) and
 ``csrc/head_fp8.hip`` (the output head in 8-bit floating point) into
 ``libspec_verify.so`` next to this file.
 """
@@ -18,6 +19,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -30,6 +33,7 @@ SOURCES = [SRC, os.path.join(PKG_DIR, "csrc", "budget_schedule.hip"),
            os.path.join(PKG_DIR, "csrc", "page_tables.hip"),
            os.path.join(PKG_DIR, "csrc", "rotate_write.hip"),
            os.path.join(PKG_DIR, "csrc", "block_attention.hip"),
+           os.path.join(PKG_DIR, "csrc", "sink_attention.hip"),
            os.path.join(PKG_DIR, "csrc", "head_fp8.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libspec_verify.so"
@@ -47,14 +51,14 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (set HIPCC or install ROCm)")
 
 
-def compile_command(out: str = LIB_PATH, sources=None) -> list:
+def compile_command(out: str, sources, *flags) -> list:
     return [
         hipcc(),
         f"--offload-arch={ARCH}",
         "-O3",
         "-std=c++17",
         "-fPIC",
-        "-shared",
+        *flags,
         # Floating-point expressions are evaluated as written (no FMA
         # contraction), so identical expressions give identical values.
         "-ffp-contract=off",
@@ -62,21 +66,29 @@ def compile_command(out: str = LIB_PATH, sources=None) -> list:
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-Wall",
         "-I", INCLUDE,
-        *(SOURCES if sources is None else sources),
+        *sources,
         "-o", out,
     ]
 
 
 def build_library(verbose: bool = True) -> str:
     """Compile the library and the tests' helper (always; outputs are
-    replaced atomically)."""
+    replaced atomically). The sources are compiled side by side."""
     if os.path.exists(TEST_SRC):
-        _compile(compile_command(TEST_LIB_PATH + ".tmp", [TEST_SRC]), TEST_LIB_PATH, verbose)
-    return _compile(compile_command(LIB_PATH + ".tmp"), LIB_PATH, verbose)
+        _compile(compile_command(TEST_LIB_PATH + ".tmp", [TEST_SRC], "-shared"), verbose)
+        os.replace(TEST_LIB_PATH + ".tmp", TEST_LIB_PATH)
+    with tempfile.TemporaryDirectory() as work:
+        objects = [os.path.join(work, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda so: _compile(compile_command(so[1], [so[0]], "-c"), verbose),
+                          zip(SOURCES, objects)))
+        _compile([hipcc(), f"--offload-arch={ARCH}", "-shared", *objects, "-o", LIB_PATH + ".tmp"],
+                 verbose)
+    os.replace(LIB_PATH + ".tmp", LIB_PATH)
+    return LIB_PATH
 
 
-def _compile(cmd, out, verbose):
-    tmp = out + ".tmp"
+def _compile(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -88,8 +100,6 @@ def _compile(cmd, out, verbose):
         lines = [l for l in res.stderr.splitlines() if "packed-fp32-ops" not in l]
         if any(l.strip() for l in lines):
             sys.stderr.write("\n".join(lines) + "\n")
-    os.replace(tmp, out)
-    return out
 
 
 if __name__ == "__main__":

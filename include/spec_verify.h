@@ -694,6 +694,28 @@ size_t spec_verify_attention_workspace_bytes(int B, int K, int q_heads, int kv_h
                                              int window);
 
 /*
+ * spec_verify_attention_sinks -- spec_verify_attention under a window with
+ * sinks: a row at position p also sees the positions [0, min(sinks, p + 1)) in
+ * front of its window, each position once. Everything else, errors included, as
+ * there; with window 0 or sinks 0 it is that call.
+ *   sinks        0 or more. Pages between the sinks and every row's window are
+ *                not needed.
+ */
+int spec_verify_attention_sinks(const void* queries, int64_t query_stride, const void* cache,
+                                const int32_t* page_table, const int32_t* ctx_lens,
+                                const int32_t* budgets, int B, int K, int q_heads, int kv_heads,
+                                int head_dim, int page_size, int max_pages, int num_pages,
+                                float scale, int window, int sinks, void* out,
+                                int32_t* out_status, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* spec_verify_attention_sinks_workspace_bytes -- scratch
+ * spec_verify_attention_sinks needs; 0 on bad arguments. Host only. */
+size_t spec_verify_attention_sinks_workspace_bytes(int B, int K, int q_heads, int kv_heads,
+                                                   int head_dim, int page_size, int max_pages,
+                                                   int window, int sinks);
+
+/*
  * The output head in 8-bit floating point (the shared projection of "What
  * DSpark adds", paragraph 1, held in half of bf16's bytes).
  *

@@ -120,3 +120,48 @@ def _rotated(**kw):
 ])
 def test_rotated_write_argument_checks(kw, code):
     assert _rotated(**kw) == code
+
+
+def _sinks(**kw):
+    a = dict(q=A, qs=8 * 128, cache=A, page_table=A, ctx=A, budgets=A, B=4, K=4, q_heads=8, kv_heads=2, head_dim=128,
+             page_size=64, max_pages=8, num_pages=16, scale=0.1, window=100, sinks=4, out=A, status=None, ws=A,
+             ws_bytes=None)
+    a.update(kw)
+    need = sb.spec_verify_attention_sinks_workspace_bytes(max(a["B"], 1), a["K"], a["q_heads"], a["kv_heads"],
+                                                          a["head_dim"], a["page_size"], a["max_pages"],
+                                                          a["window"], a["sinks"])
+    return sb.spec_verify_attention_sinks(
+        a["q"], a["qs"], a["cache"], a["page_table"], a["ctx"], a["budgets"], a["B"], a["K"], a["q_heads"],
+        a["kv_heads"], a["head_dim"], a["page_size"], a["max_pages"], a["num_pages"], a["scale"], a["window"],
+        a["sinks"], a["out"], a["status"], a["ws"], need if a["ws_bytes"] is None else a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=0, q=None, out=None, ws=None), sb.SV_OK),
+    (dict(B=0, q=None, out=None, ws=None, window=0), sb.SV_OK),
+    (dict(sinks=-1), sb.SV_ERR_ARG),
+    (dict(window=-1), sb.SV_ERR_ARG),
+    (dict(window=0, sinks=-1), sb.SV_ERR_ARG),
+    (dict(K=sb.SV_MAX_K + 1), sb.SV_ERR_ARG),
+    (dict(q_heads=7), sb.SV_ERR_ARG),
+    (dict(num_pages=0), sb.SV_ERR_ARG),
+    (dict(scale=math.nan), sb.SV_ERR_ARG),
+    (dict(ws_bytes=0), sb.SV_ERR_ARG),
+    (dict(q=None), sb.SV_ERR_NULL),
+    (dict(ws=None), sb.SV_ERR_NULL),
+    (dict(q=A + 8), sb.SV_ERR_ALIGN),
+    (dict(ws=A + 16), sb.SV_ERR_ALIGN),
+])
+def test_attention_with_sinks_argument_checks(kw, code):
+    assert _sinks(**kw) == code
+
+
+def test_attention_with_sinks_workspace():
+    size = sb.spec_verify_attention_sinks_workspace_bytes
+    plain = sb.spec_verify_attention_workspace_bytes
+    # Short spans are never split; sinks count among them.
+    assert size(4, 4, 8, 2, 128, 64, 2048, 100, 4) == 256
+    assert size(4, 4, 8, 2, 128, 64, 2048, 100, 5000) > 256
+    assert size(4, 4, 8, 2, 128, 64, 2048, 0, 5000) == plain(4, 4, 8, 2, 128, 64, 2048, 0)
+    assert size(4, 4, 8, 2, 128, 64, 2048, 100, -1) == 0 and size(0, 4, 8, 2, 128, 64, 2048, 100, 4) == 0
+    assert size(4, 4, 8, 2, 128, 64, 2048, 2**31 - 1, 2**31 - 1) == plain(4, 4, 8, 2, 128, 64, 2048)
