@@ -50,6 +50,7 @@ SV_MAX_PAGE = 4096
 SV_MAX_CONTEXT = 1 << 24
 SV_MAX_HIDDEN = 65536
 SV_MAX_STRIDE = 2147483647
+SV_MAX_GROUPS = 512
 
 EXPORTED = (
     "spec_verify_init",
@@ -78,6 +79,8 @@ EXPORTED = (
     "spec_verify_attention_workspace_bytes",
     "spec_verify_attention_sinks",
     "spec_verify_attention_sinks_workspace_bytes",
+    "spec_verify_attention_shared",
+    "spec_verify_attention_shared_workspace_bytes",
     "spec_head_quantize",
     "spec_head_logits",
     "spec_verify_free",
@@ -163,6 +166,12 @@ def _declare(lib):
     lib.spec_verify_attention_sinks.restype = _i
     lib.spec_verify_attention_sinks_workspace_bytes.argtypes = [_i] * 9
     lib.spec_verify_attention_sinks_workspace_bytes.restype = ctypes.c_size_t
+    lib.spec_verify_attention_shared.argtypes = [
+        _vp, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i,
+        ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.spec_verify_attention_shared.restype = _i
+    lib.spec_verify_attention_shared_workspace_bytes.argtypes = [_i] * 8
+    lib.spec_verify_attention_shared_workspace_bytes.restype = ctypes.c_size_t
     lib.spec_verify_attention_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i, _i]
     lib.spec_verify_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.spec_head_quantize.argtypes = [_vp, _i, _i, _i, _i, _vp, _vp, _vp]
@@ -719,6 +728,25 @@ def spec_verify_attention_sinks_workspace_bytes(B: int, K: int, q_heads: int, kv
         int(max_pages), int(window), int(sinks)))
 
 
+def spec_verify_attention_shared(queries, query_stride, cache, page_table, ctx_lens, budgets,
+                                 groups, shared_lens, B, K, G, q_heads, kv_heads, head_dim,
+                                 page_size, max_pages, num_pages, scale, out, out_status, workspace,
+                                 workspace_bytes, stream) -> int:
+    return load().spec_verify_attention_shared(queries, query_stride, cache, page_table, ctx_lens,
+                                               budgets, groups, shared_lens, B, K, G, q_heads,
+                                               kv_heads, head_dim, page_size, max_pages, num_pages,
+                                               scale, out, out_status, workspace, workspace_bytes,
+                                               stream)
+
+
+def spec_verify_attention_shared_workspace_bytes(B: int, K: int, G: int, q_heads: int,
+                                                 kv_heads: int, head_dim: int, page_size: int,
+                                                 max_pages: int) -> int:
+    return int(load().spec_verify_attention_shared_workspace_bytes(
+        int(B), int(K), int(G), int(q_heads), int(kv_heads), int(head_dim), int(page_size),
+        int(max_pages)))
+
+
 def spec_head_quantize(src, dtype, rows, H, block_rows, out_codes, out_scales, stream) -> int:
     return load().spec_head_quantize(src, dtype, rows, H, block_rows, out_codes, out_scales, stream)
 
@@ -745,6 +773,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 # A function of the shapes alone, for every layer and step: the last shapes' sizes.
 _attention_bytes = functools.lru_cache(maxsize=1024)(spec_verify_attention_workspace_bytes)
 _sinks_bytes = functools.lru_cache(maxsize=1024)(spec_verify_attention_sinks_workspace_bytes)
+_shared_bytes = functools.lru_cache(maxsize=1024)(spec_verify_attention_shared_workspace_bytes)
 
 
 def _need(t, name, dtype, shape, index):
@@ -1010,6 +1039,56 @@ class BlockCache:
             workspace.data_ptr(), nbytes, _raw_stream(index))
         if rc != SV_OK:
             _check(rc, "spec_verify_attention")
+        return out
+
+    def attend_shared(self, queries, page_table, ctx_lens, groups, shared_lens, budgets=None,
+                      scale: float | None = None, out=None, status=None, stream=None):
+        """``attend`` (without a window) for requests that share a prefix:
+        ``groups`` int32 [B], the group of every request (outside 0 .. G - 1:
+        none), ``shared_lens`` int32 [G], the tokens from position 0 on that all
+        requests of a group have in common. Their keys and values are read and
+        multiplied once for all rows of the group, through the page table row of
+        its first request."""
+        index = self._index
+        if stream is not None:
+            with _other_stream(stream, index):
+                return self.attend_shared(queries, page_table, ctx_lens, groups, shared_lens,
+                                          budgets, scale, out, status)
+        if _current_device() != index:
+            with torch.cuda.device(index):
+                return self.attend_shared(queries, page_table, ctx_lens, groups, shared_lens,
+                                          budgets, scale, out, status)
+        shape = queries.shape
+        if len(shape) != 4 or queries.dtype is not torch.bfloat16 or shape[3] != self.head_dim \
+                or shape[1] < 1:
+            raise ValueError(f"queries must be bfloat16 [B, K+1, q_heads, {self.head_dim}]")
+        if shared_lens.dim() != 1 or shared_lens.shape[0] > SV_MAX_GROUPS:
+            raise ValueError(f"shared_lens must be [G], G up to {SV_MAX_GROUPS}, got "
+                             f"{tuple(shared_lens.shape)}")
+        B, T, heads, dim = shape
+        G = shared_lens.shape[0]
+        stride = _token_stride(queries, "queries", index)
+        table, width = self._table(page_table, B)
+        nbytes = _shared_bytes(max(B, 1), T - 1, G, heads, self.kv_heads, dim, self.page_size, width)
+        if nbytes == 0:
+            raise ValueError(f"bad attention shape: B={B} K={T - 1} q_heads={heads} kv_heads="
+                             f"{self.kv_heads} max_pages={width}")
+        if out is None:
+            out = torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        rc = load().spec_verify_attention_shared(
+            queries.data_ptr(), stride, self._pool_ptr(), table,
+            _need(ctx_lens, "ctx_lens", torch.int32, (B,), index),
+            None if budgets is None else _need(budgets, "budgets", torch.int32, (B,), index),
+            _need(groups, "groups", torch.int32, (B,), index),
+            _need(shared_lens, "shared_lens", torch.int32, (G,), index),
+            B, T - 1, G, heads, self.kv_heads, dim, self.page_size, width, self.num_pages,
+            dim ** -0.5 if scale is None else scale,
+            _need(out, "out", torch.bfloat16, shape, index),
+            None if status is None else _need(status, "status", torch.int32, (1,), index),
+            workspace.data_ptr(), nbytes, _raw_stream(index))
+        if rc != SV_OK:
+            _check(rc, "spec_verify_attention_shared")
         return out
 
 

@@ -9,7 +9,8 @@ statistics), ``csrc/verify_hidden.hip`` (verification from hidden states),
 ``csrc/page_tables.hip`` (its page tables from the requests' lengths),
 ``csrc/rotate_write.hip`` (normalised and rotated heads on their way into it),
 ``csrc/block_attention.hip`` (attention of drafted blocks over it),
-``csrc/sink_attention.hip`` (under a window with sink tokens) and
+``csrc/sink_attention.hip`` (under a window with sink tokens),
+``csrc/shared_attention.hip`` (for requests that share a prefix) and
 ``csrc/head_fp8.hip`` (the output head in 8-bit floating point) into
 ``libspec_verify.so`` next to this file.
 """
@@ -34,6 +35,7 @@ SOURCES = [SRC, os.path.join(PKG_DIR, "csrc", "budget_schedule.hip"),
            os.path.join(PKG_DIR, "csrc", "rotate_write.hip"),
            os.path.join(PKG_DIR, "csrc", "block_attention.hip"),
            os.path.join(PKG_DIR, "csrc", "sink_attention.hip"),
+           os.path.join(PKG_DIR, "csrc", "shared_attention.hip"),
            os.path.join(PKG_DIR, "csrc", "head_fp8.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libspec_verify.so"

@@ -50,8 +50,9 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
 
 // What a row sees of the positions up to its own: those of a window, or also some
-// sinks in front of it.
-enum Mode { kWindow, kSinks };
+// sinks in front of it; or those behind a shared prefix, whose partial results
+// (made elsewhere) are joined with its own.
+enum Mode { kWindow, kSinks, kTail };
 
 constexpr int kFew = 4, kMany = 8;      // wavefronts of a workgroup (see plan_of)
 constexpr float kNegInf = -INFINITY;
@@ -88,6 +89,15 @@ constexpr int kLeastShare = 48;     // a few tiles for each of a workgroup's wav
 constexpr int kDirectTiles = 32;
 constexpr int kDirectUnits = 4;
 
+// Where the partial results of a request's shared prefix are: its rows (row
+// block's place first, as elsewhere: t group + head of the group) follow each
+// other from `row` on among its group's, in blocks of 1 << prefix_shift rows;
+// part i of block n of head h lies in slot first + (i blocks + n) heads + h.
+struct Prefix {
+    int tiles;          // tiles of the prefix; 0: none, and no parts
+    int row, first, blocks, parts, pad[3];
+};
+
 struct AttendArgs {
     const uint16_t* q;
     long long q_stride;
@@ -105,9 +115,21 @@ struct AttendArgs {
     int row_blocks;     // blocks of 16 kMT rows of a full block's (K + 1) group rows
     int window;
     int sinks;          // kSinks: positions that stay visible in front of the window
+    const Prefix* prefix;       // kTail: [B], and the partial results that they name
+    const float* prefix_o;      // [slot][1 << prefix_shift rows][D]
+    const float2* prefix_ml;
+    int prefix_shift;
     bool direct;        // a workgroup per unit
     bool negate;        // scale < 0: queries are negated and |scale| is used
     float c;            // |scale| * log2(e)
+};
+
+// A request's block, and in kTail where its own tokens start.
+template <Mode kMode>
+struct Req : Block {};
+template <>
+struct Req<kTail> : Block {
+    int tiles;          // of the shared prefix
 };
 
 // The tiles a request's block reads: [first, end), by numbers that are the tiles'
@@ -146,8 +168,9 @@ struct SinkTiles {
 };
 
 template <Mode kMode>
-__device__ __forceinline__ Span span_of(const Block& blk, const AttendArgs& a) {
+__device__ __forceinline__ Span span_of(const Req<kMode>& blk, const AttendArgs& a) {
     const int end = (blk.ctx + blk.len + kTile - 1) / kTile;
+    if constexpr (kMode == kTail) return Span{min(blk.tiles, end), end};
     if constexpr (kMode == kSinks) {
         const SinkTiles s(blk, a.window, a.sinks);
         return Span{s.low - s.whole - s.part, end};
@@ -186,7 +209,14 @@ __device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirst
 __device__ __forceinline__ unsigned long long scalar(unsigned long long v) {
     return (unsigned long long)(unsigned)scalar((int)(v >> 32)) << 32 | (unsigned)scalar((int)v);
 }
-__device__ __forceinline__ Block scalar(const Block& k) { return Block{scalar(k.ctx), scalar(k.len)}; }
+template <Mode kMode>
+__device__ __forceinline__ Req<kMode> scalar(const Req<kMode>& k) {
+    Req<kMode> r;
+    r.ctx = scalar(k.ctx);
+    r.len = scalar(k.len);
+    if constexpr (kMode == kTail) r.tiles = scalar(k.tiles);
+    return r;
+}
 
 // Maximum / sum over the four lanes that hold the same row (lane ^ 16, ^ 32).
 __device__ __forceinline__ float quad_max(float v) {
@@ -514,13 +544,27 @@ struct Stream {
     }
 };
 
+template <Mode kMode>
+__device__ __forceinline__ Req<kMode> plain_block(const AttendArgs& a, int b) {
+    Req<kMode> r;
+    static_cast<Block&>(r) = block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, nullptr, false);
+    if constexpr (kMode == kTail) r.tiles = r.len > 0 ? a.prefix[b].tiles : 0;
+    return r;
+}
+// The same, where there may be no request.
+template <Mode kMode>
+__device__ __forceinline__ Req<kMode> plain_block(const AttendArgs& a, int b, bool some) {
+    Req<kMode> none{};
+    return some ? plain_block<kMode>(a, b) : none;
+}
+
 // A request's share of the line.
 template <int kMT, Mode kMode>
 struct Share {
-    Block blk;
+    Req<kMode> blk;
     Span span;
     int rows, blocks;           // rows, row blocks that hold some
-    __device__ __forceinline__ Share(const AttendArgs& a, const Block& k)
+    __device__ __forceinline__ Share(const AttendArgs& a, const Req<kMode>& k)
         : blk(k), span(span_of<kMode>(k, a)), rows(k.len * a.group),
           blocks((rows + 16 * kMT - 1) / (16 * kMT)) {}
     // Row tiles of row block rb, and what one tile of its units costs.
@@ -547,14 +591,41 @@ constexpr int occupancy() {
     return D == 256 ? 3 - kMT : D * kMT <= 64 ? 4 : D * kMT <= 128 ? 3 : 2;
 }
 
+// A sum of partial results under its running reference.
+struct Joined {
+    float ref, sum;
+    f32x4 acc;
+    __device__ __forceinline__ void add(float other_ref, float other_sum, const f32x4& other) {
+        const float top = fmaxf(ref, other_ref), base = top == kNegInf ? 0.0f : top;
+        const float f = exp2_fast(ref - base), g = exp2_fast(other_ref - base);
+        sum = sum * f + other_sum * g;
+        acc = acc * f + other * g;
+        ref = top;
+    }
+};
+
+// The partial results of row `row` (of its request's, for head h) over the shared
+// prefix, from part s on, every `by`-th.
+template <int D>
+__device__ __forceinline__ void join_prefix(const AttendArgs& a, Joined& j, const Prefix& p, int h, int row,
+                                            int ch, int s, int by) {
+    const int at = p.row + row, block = at >> a.prefix_shift, in = at & ((1 << a.prefix_shift) - 1);
+    for (; s < p.parts; s += by) {
+        const long long slot = p.first + ((long long)s * p.blocks + block) * a.pages.heads + h;
+        const long long part = (slot << a.prefix_shift) + in;
+        const float2 ml = a.prefix_ml[part];
+        j.add(ml.x, ml.y, *reinterpret_cast<const f32x4*>(a.prefix_o + part * D + ch));
+    }
+}
+
 // One run of tiles, from the queries to the output or a partial result, for a
 // row block of which kAct row tiles hold rows.
 template <int D, int kMT, int kWaves, int kAct, Mode kMode>
-__device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any, const Block& its,
+__device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any, const Req<kMode>& its,
                                            Lds<D, kMT, kWaves>& sh, int lane, int wave) {
     // The same for the whole wavefront, and to be kept in scalar registers.
     const Work wk{scalar(any.b), scalar(any.h), scalar(any.rb), scalar(any.t0), scalar(any.t1), scalar(any.slot)};
-    const Block blk = scalar(its);
+    const Req<kMode> blk = scalar(its);
     using S = State<D, kAct>;
     constexpr int kPlanes = S::kPlanes, kChans = S::kChans, kPieces = kAct * kPlanes * kChans / 4;
     constexpr int kOwn = (kAct * S::kSteps + kWaves - 1) / kWaves;
@@ -666,6 +737,12 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any,
                 ref = mt == n ? top[n] : ref;
             }
             if (wk.slot < 0) {
+                if constexpr (kMode == kTail) {
+                    Joined j{ref, sum, v};
+                    join_prefix<D>(a, j, a.prefix[wk.b], wk.h, row, ch, 0, 1);
+                    v = j.acc;
+                    sum = j.sum;
+                }
                 const int t = row / a.group;
                 const float inv = 1.0f / sum;
                 const unsigned w[2] = {pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)};
@@ -682,9 +759,6 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any,
     }
 }
 
-__device__ __forceinline__ Block plain_block(const AttendArgs& a, int b) {
-    return block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, nullptr, false);
-}
 template <int D, int kMT, int kWaves, Mode kMode>
 __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_kernel(AttendArgs a) {
     __shared__ Lds<D, kMT, kWaves> sh;
@@ -702,12 +776,12 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
     int b = -1, h = 0, rb = 0, part = 0;
     unsigned long long at = 0, lo = 0, hi = 0, share = 1;
     bool aligned = false;
-    Block blk{0, 0};
+    Req<kMode> blk{};
     if (kWaves != kFew || a.direct) {
         rb = scalar(g % a.row_blocks);
         h = scalar(g / a.row_blocks % heads);
         const int mine = scalar(g / a.row_blocks / heads);
-        blk = scalar(plain_block(a, mine));
+        blk = scalar(plain_block<kMode>(a, mine));
         if (rb < Share<kMT, kMode>(a, blk).blocks) b = mine;
     } else if constexpr (kWaves == kFew) {
         const int per = (a.B + 255) / 256;
@@ -715,11 +789,11 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
         if (tid == 0) sh.found = -1;
         if (tid < 2) a.parts[2 * g + tid] = make_int4(0, 0, 0, 0);
         // The first of this thread's requests (the only one up to 256) is kept.
-        const Share<kMT, kMode> first(a, b0 < b1 ? plain_block(a, b0) : Block{0, 0});
+        const Share<kMT, kMode> first(a, plain_block<kMode>(a, b0, b0 < b1));
         unsigned long long cost = 0;
         unsigned units = 0;
         for (int i = b0; i < b1; ++i) {
-            const Share<kMT, kMode> s = i == b0 ? first : Share<kMT, kMode>(a, plain_block(a, i));
+            const Share<kMT, kMode> s = i == b0 ? first : Share<kMT, kMode>(a, plain_block<kMode>(a, i));
             cost += s.sum(heads, [&](int r) { return s.tiles(r); });
             units += s.blocks * heads;
         }
@@ -741,7 +815,7 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
         unsigned longest = 0;
         const int width = (int)min(share, 1ull << 30);
         for (int i = b0; i < b1; ++i) {
-            const Share<kMT, kMode> s = i == b0 ? first : Share<kMT, kMode>(a, plain_block(a, i));
+            const Share<kMT, kMode> s = i == b0 ? first : Share<kMT, kMode>(a, plain_block<kMode>(a, i));
             if (s.blocks > 0) longest = max(longest, (unsigned)(s.tiles(0) / s.parts(0, width)));
         }
         #pragma unroll
@@ -762,7 +836,7 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
         hi = aligned ? g + 1 : lo + share;
         unsigned long long mine = 0;
         for (int i = b0; i < b1; ++i) {
-            mine += length(i == b0 ? first : Share<kMT, kMode>(a, plain_block(a, i)));
+            mine += length(i == b0 ? first : Share<kMT, kMode>(a, plain_block<kMode>(a, i)));
         }
         unsigned long long upto = mine;
         #pragma unroll
@@ -777,7 +851,7 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
             at = upto - mine;
             int i = b0;
             for (; i < b1 - 1; ++i) {
-                const unsigned long long n = length(Share<kMT, kMode>(a, plain_block(a, i)));
+                const unsigned long long n = length(Share<kMT, kMode>(a, plain_block<kMode>(a, i)));
                 if (lo < at + n) break;
                 at += n;
             }
@@ -788,7 +862,7 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
         b = scalar(sh.found);
         if (b >= 0 && (aligned || g < a.groups)) {
             at = scalar(sh.before);
-            blk = scalar(plain_block(a, b));
+            blk = scalar(plain_block<kMode>(a, b));
             if (aligned) {
                 const Share<kMT, kMode> s(a, blk);
                 const int full = heads * scalar(s.parts(0, (int)share));    // of a full row block
@@ -856,13 +930,14 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
                 int next = b + 1;
                 b = -1;
                 for (; next < a.B && b < 0; next += 64) {     // the next request that holds anything
-                    Block k{0, 0};
-                    if (next + lane < a.B) k = plain_block(a, next + lane);
+                    const Req<kMode> k = plain_block<kMode>(a, next + lane, next + lane < a.B);
                     const unsigned long long some = __ballot(k.len > 0);
                     if (some != 0) {
                         const int i = __builtin_ctzll(some);
                         b = next + i;
-                        blk = Block{__builtin_amdgcn_readlane(k.ctx, i), __builtin_amdgcn_readlane(k.len, i)};
+                        blk.ctx = __builtin_amdgcn_readlane(k.ctx, i);
+                        blk.len = __builtin_amdgcn_readlane(k.len, i);
+                        if constexpr (kMode == kTail) blk.tiles = __builtin_amdgcn_readlane(k.tiles, i);
                     }
                 }
             }
@@ -870,19 +945,6 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
         if (b >= 0 && at + (unsigned long long)h * (kUnitCost + Share<kMT, kMode>(a, blk).tiles(rb)) >= hi) b = -1;
     }
 }
-
-// A sum of partial results under its running reference.
-struct Joined {
-    float ref, sum;
-    f32x4 acc;
-    __device__ __forceinline__ void add(float other_ref, float other_sum, const f32x4& other) {
-        const float top = fmaxf(ref, other_ref), base = top == kNegInf ? 0.0f : top;
-        const float f = exp2_fast(ref - base), g = exp2_fast(other_ref - base);
-        sum = sum * f + other_sum * g;
-        acc = acc * f + other * g;
-        ref = top;
-    }
-};
 
 // Joins the units that the first kernel left in parts. A workgroup here belongs
 // to one there and to 16 rows of a row block. The 16 rows of a unit of fewer
@@ -892,7 +954,7 @@ struct Joined {
 // hold 4 channels, 256 / D parts lie side by side in a wavefront, kDeep of them
 // each are in flight. The order of the sums is fixed by the shapes and lengths
 // of the call.
-template <int D, int kMT>
+template <int D, int kMT, Mode kMode>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     constexpr int kSide = 256 / D, kLanes = 64 / kSide;     // parts side by side, lanes of each
     constexpr int kDeep = 8;
@@ -908,7 +970,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
         if (n == 0 || s0 >= (many ? 16 : 4)) continue;
         const int rb = both[slot].x % a.row_blocks, h = both[slot].x / a.row_blocks % a.pages.heads;
         const int b = both[slot].x / a.row_blocks / a.pages.heads;
-        const int rows = plain_block(a, b).len * a.group - rb * (16 * kMT);
+        const int rows = plain_block<kMode>(a, b).len * a.group - rb * (16 * kMT);
         const int by = many ? kFew * kSide : kSide;
         for (int i = many ? s0 : s0 * kFew + wave; i < 16 && in0 + i < rows; i += many ? 16 : min(n, 4) * kFew) {
             const int in = in0 + i;
@@ -926,6 +988,10 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
                 for (int k = 0; k < kDeep; ++k) {
                     if (s + k * by < n) j.add(ml[k].x, ml[k].y, v[k]);
                 }
+            }
+            if constexpr (kMode == kTail) {
+                join_prefix<D>(a, j, a.prefix[b], h, rb * (16 * kMT) + in, ch,
+                               (many ? wave * kSide : 0) + side, by);
             }
             #pragma unroll
             for (int o = kLanes; o < 64; o <<= 1) {
@@ -1018,7 +1084,7 @@ void launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
     hipLaunchKernelGGL((attend_kernel<D, kMT, kFew, kMode>), dim3((unsigned)p.grid), dim3(64 * kFew), 0, s, a);
     if (!p.direct) {
         const unsigned blocks = (unsigned)(p.grid * kMT);
-        hipLaunchKernelGGL((attend_join_kernel<D, kMT>), dim3(blocks), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((attend_join_kernel<D, kMT, kMode>), dim3(blocks), dim3(256), 0, s, a);
     }
 }
 
@@ -1028,15 +1094,13 @@ size_t workspace_of(const Plan& p, int head_dim) {
            parts_of(p) * head_dim * sizeof(float);
 }
 
-// The host side of a call: checks, plan, launches.
-template <Mode kMode>
-int attend(const void* queries, int64_t query_stride, const void* cache, const int32_t* page_table,
-           const int32_t* ctx_lens, const int32_t* budgets, int B, int K, int q_heads,
-           int kv_heads, int head_dim, int page_size, int max_pages, int num_pages, float scale,
-           int window, int sinks, void* out, int32_t* out_status, void* workspace,
-           size_t workspace_bytes, void* stream) {
+// Whether a call's arguments are in order (an sv_status).
+int check(const void* queries, int64_t query_stride, const void* cache, const int32_t* page_table,
+          const int32_t* ctx_lens, const int32_t* budgets, int B, int K, int q_heads, int kv_heads,
+          int head_dim, int page_size, int max_pages, int num_pages, float scale, int window,
+          const void* out, const int32_t* out_status, const void* workspace) {
     if (!shape_ok(B, K, q_heads, kv_heads, head_dim, page_size, max_pages, window) ||
-        sinks < 0 || num_pages < 1 || !std::isfinite(scale)) {
+        num_pages < 1 || !std::isfinite(scale)) {
         return SV_ERR_ARG;
     }
     if (B == 0) return SV_OK;
@@ -1049,8 +1113,14 @@ int attend(const void* queries, int64_t query_stride, const void* cache, const i
         !aligned(ctx_lens, 4) || !aligned(budgets, 4) || !aligned(out_status, 4)) {
         return SV_ERR_ALIGN;
     }
-    const Plan p = plan_of(B, K, q_heads, kv_heads, head_dim, page_size, max_pages, window, sinks);
-    if (workspace_bytes < workspace_of(p, head_dim)) return SV_ERR_ARG;
+    return SV_OK;
+}
+
+// The kernels' arguments for a call that is in order.
+AttendArgs args_of(const Plan& p, const void* queries, int64_t query_stride, const void* cache,
+                   const int32_t* page_table, const int32_t* ctx_lens, const int32_t* budgets, int B,
+                   int K, int q_heads, int kv_heads, int page_size, int max_pages, int num_pages,
+                   float scale, void* out, int32_t* out_status, void* workspace) {
     AttendArgs a{};
     a.q = static_cast<const uint16_t*>(queries);
     a.q_stride = query_stride;
@@ -1071,15 +1141,17 @@ int attend(const void* queries, int64_t query_stride, const void* cache, const i
     a.group = q_heads / kv_heads;
     a.groups = p.groups;
     a.row_blocks = p.row_blocks;
-    a.window = window;
-    a.sinks = sinks;
     a.direct = p.direct;
     a.negate = scale < 0.0f;
     // A scale of 0 becomes 2^-126, under which every seen score is as good as 0
     // and an unseen one (-inf) still is -inf; one too large for fp32 its largest
     // value, under which a score of 0 still is 0.
     a.c = (float)std::clamp(std::fabs((double)scale) * 1.4426950408889634, (double)FLT_MIN, (double)FLT_MAX);
-    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return a;
+}
+
+template <Mode kMode>
+int launch_attend(const AttendArgs& a, const Plan& p, int head_dim, hipStream_t s) {
     switch (head_dim * 8 + p.mt) {
         case 64 * 8 + 1: launch<64, 1, kMode>(a, p, s); break;
         case 64 * 8 + 2: launch<64, 2, kMode>(a, p, s); break;
@@ -1093,6 +1165,26 @@ int attend(const void* queries, int64_t query_stride, const void* cache, const i
         default: launch<256, 2, kMode>(a, p, s); break;
     }
     return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+// A call without a shared prefix.
+template <Mode kMode>
+int attend(const void* queries, int64_t query_stride, const void* cache, const int32_t* page_table,
+           const int32_t* ctx_lens, const int32_t* budgets, int B, int K, int q_heads,
+           int kv_heads, int head_dim, int page_size, int max_pages, int num_pages, float scale,
+           int window, int sinks, void* out, int32_t* out_status, void* workspace,
+           size_t workspace_bytes, void* stream) {
+    const int rc = check(queries, query_stride, cache, page_table, ctx_lens, budgets, B, K, q_heads,
+                         kv_heads, head_dim, page_size, max_pages, num_pages, scale, window, out,
+                         out_status, workspace);
+    if (rc != SV_OK || B == 0) return rc;
+    const Plan p = plan_of(B, K, q_heads, kv_heads, head_dim, page_size, max_pages, window, sinks);
+    if (workspace_bytes < workspace_of(p, head_dim)) return SV_ERR_ARG;
+    AttendArgs a = args_of(p, queries, query_stride, cache, page_table, ctx_lens, budgets, B, K, q_heads,
+                           kv_heads, page_size, max_pages, num_pages, scale, out, out_status, workspace);
+    a.window = window;
+    a.sinks = sinks;
+    return launch_attend<kMode>(a, p, head_dim, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace

@@ -106,6 +106,7 @@ enum sv_status {
 #define SV_MAX_CONTEXT (1 << 24)
 #define SV_MAX_HIDDEN 65536
 #define SV_MAX_STRIDE 2147483647
+#define SV_MAX_GROUPS 512
 
 /* Size of the static device scratch of spec_verify_run_noalloc (per GPU). */
 #define SV_NOALLOC_SCRATCH_BYTES (16u << 20)
@@ -714,6 +715,40 @@ int spec_verify_attention_sinks(const void* queries, int64_t query_stride, const
 size_t spec_verify_attention_sinks_workspace_bytes(int B, int K, int q_heads, int kv_heads,
                                                    int head_dim, int page_size, int max_pages,
                                                    int window, int sinks);
+
+/*
+ * spec_verify_attention_shared -- spec_verify_attention (without a window) for
+ * requests that share a prefix: what the requests of a group have in common is
+ * read and computed once for all their rows. The result is that call's but for
+ * the order of its sums. Three or four launches.
+ *   groups       int32 [B] (device): the group of request b; a number outside
+ *                [0, G): none.
+ *   shared_lens  int32 [G] (device): tokens from position 0 on that all
+ *                requests of the group have in common: the page table rows
+ *                agree on the pages that lie wholly in front of it or the
+ *                tokens are the same. Read through the row of the group's
+ *                first request that holds any (a bad page there leaves the
+ *                whole group's outputs undefined). Whole tiles of 32 tokens up
+ *                to the shortest context of the group are shared; groups of
+ *                fewer than two requests, and lengths below 32, share nothing.
+ *   G            0 (nothing is shared) .. SV_MAX_GROUPS.
+ *   workspace    at least spec_verify_attention_shared_workspace_bytes() bytes;
+ *                it holds fp32 partial results of all rows.
+ * Everything else as in spec_verify_attention.
+ */
+int spec_verify_attention_shared(const void* queries, int64_t query_stride, const void* cache,
+                                 const int32_t* page_table, const int32_t* ctx_lens,
+                                 const int32_t* budgets, const int32_t* groups,
+                                 const int32_t* shared_lens, int B, int K, int G, int q_heads,
+                                 int kv_heads, int head_dim, int page_size, int max_pages,
+                                 int num_pages, float scale, void* out, int32_t* out_status,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* spec_verify_attention_shared_workspace_bytes -- scratch
+ * spec_verify_attention_shared needs; 0 on bad arguments. Host only. */
+size_t spec_verify_attention_shared_workspace_bytes(int B, int K, int G, int q_heads,
+                                                    int kv_heads, int head_dim, int page_size,
+                                                    int max_pages);
 
 /*
  * The output head in 8-bit floating point (the shared projection of "What

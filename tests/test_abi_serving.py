@@ -165,3 +165,52 @@ def test_attention_with_sinks_workspace():
     assert size(4, 4, 8, 2, 128, 64, 2048, 0, 5000) == plain(4, 4, 8, 2, 128, 64, 2048, 0)
     assert size(4, 4, 8, 2, 128, 64, 2048, 100, -1) == 0 and size(0, 4, 8, 2, 128, 64, 2048, 100, 4) == 0
     assert size(4, 4, 8, 2, 128, 64, 2048, 2**31 - 1, 2**31 - 1) == plain(4, 4, 8, 2, 128, 64, 2048)
+
+
+def _shared(**kw):
+    a = dict(q=A, qs=8 * 128, cache=A, page_table=A, ctx=A, budgets=A, groups=A, lens=A, B=4, K=4, G=2, q_heads=8,
+             kv_heads=2, head_dim=128, page_size=64, max_pages=8, num_pages=16, scale=0.1, out=A, status=None, ws=A,
+             ws_bytes=None)
+    a.update(kw)
+    need = sb.spec_verify_attention_shared_workspace_bytes(max(a["B"], 1), a["K"], a["G"], a["q_heads"],
+                                                           a["kv_heads"], a["head_dim"], a["page_size"],
+                                                           a["max_pages"])
+    return sb.spec_verify_attention_shared(
+        a["q"], a["qs"], a["cache"], a["page_table"], a["ctx"], a["budgets"], a["groups"], a["lens"], a["B"], a["K"],
+        a["G"], a["q_heads"], a["kv_heads"], a["head_dim"], a["page_size"], a["max_pages"], a["num_pages"],
+        a["scale"], a["out"], a["status"], a["ws"], need if a["ws_bytes"] is None else a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=0, q=None, out=None, ws=None, groups=None), sb.SV_OK),
+    (dict(B=0, G=0, q=None, out=None, ws=None, groups=None), sb.SV_OK),
+    (dict(G=-1), sb.SV_ERR_ARG),
+    (dict(G=sb.SV_MAX_GROUPS + 1), sb.SV_ERR_ARG),
+    (dict(K=-1), sb.SV_ERR_ARG),
+    (dict(q_heads=7), sb.SV_ERR_ARG),
+    (dict(head_dim=32), sb.SV_ERR_ARG),
+    (dict(num_pages=0), sb.SV_ERR_ARG),
+    (dict(scale=math.inf), sb.SV_ERR_ARG),
+    (dict(ws_bytes=4096), sb.SV_ERR_ARG),
+    (dict(qs=1016), sb.SV_ERR_ARG),
+    (dict(q=None), sb.SV_ERR_NULL),
+    (dict(groups=None), sb.SV_ERR_NULL),
+    (dict(lens=None), sb.SV_ERR_NULL),
+    (dict(ws=None), sb.SV_ERR_NULL),
+    (dict(groups=A + 2), sb.SV_ERR_ALIGN),
+    (dict(lens=A + 1), sb.SV_ERR_ALIGN),
+    (dict(q=A + 8), sb.SV_ERR_ALIGN),
+    (dict(ws=A + 16), sb.SV_ERR_ALIGN),
+])
+def test_attention_behind_shared_prefixes_argument_checks(kw, code):
+    assert _shared(**kw) == code
+
+
+def test_attention_behind_shared_prefixes_workspace():
+    size = sb.spec_verify_attention_shared_workspace_bytes
+    assert size(0, 4, 2, 8, 2, 128, 64, 8) == 0 and size(4, 4, -1, 8, 2, 128, 64, 8) == 0
+    assert size(4, 4, sb.SV_MAX_GROUPS + 1, 8, 2, 128, 64, 8) == 0 and size(4, 4, 2, 8, 3, 128, 64, 8) == 0
+    assert size(4, 4, 0, 8, 2, 128, 64, 8) == sb.spec_verify_attention_workspace_bytes(4, 4, 8, 2, 128, 64, 8)
+    # At least one fp32 partial result of every row.
+    assert size(128, 8, 1, 32, 8, 128, 64, 100) > 128 * 9 * 32 * 128 * 4
+    assert size(sb.SV_MAX_BATCH, 32, 512, 256, 256, 256, 64, 1 << 18) > 1 << 35
