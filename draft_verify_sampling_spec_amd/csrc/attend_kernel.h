@@ -50,8 +50,8 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
 
 // What a row sees of the positions up to its own: those of a window, or also some
-// sinks in front of it; or those behind a shared prefix, whose partial results
-// (made elsewhere) are joined with its own.
+// sinks in front of it; or, as partial results that are joined elsewhere, those
+// behind a shared prefix.
 enum Mode { kWindow, kSinks, kTail };
 
 constexpr int kFew = 4, kMany = 8;      // wavefronts of a workgroup (see plan_of)
@@ -89,15 +89,6 @@ constexpr int kLeastShare = 48;     // a few tiles for each of a workgroup's wav
 constexpr int kDirectTiles = 32;
 constexpr int kDirectUnits = 4;
 
-// Where the partial results of a request's shared prefix are: its rows (row
-// block's place first, as elsewhere: t group + head of the group) follow each
-// other from `row` on among its group's, in blocks of 1 << prefix_shift rows;
-// part i of block n of head h lies in slot first + (i blocks + n) heads + h.
-struct Prefix {
-    int tiles;          // tiles of the prefix; 0: none, and no parts
-    int row, first, blocks, parts, pad[3];
-};
-
 struct AttendArgs {
     const uint16_t* q;
     long long q_stride;
@@ -115,10 +106,9 @@ struct AttendArgs {
     int row_blocks;     // blocks of 16 kMT rows of a full block's (K + 1) group rows
     int window;
     int sinks;          // kSinks: positions that stay visible in front of the window
-    const Prefix* prefix;       // kTail: [B], and the partial results that they name
-    const float* prefix_o;      // [slot][1 << prefix_shift rows][D]
-    const float2* prefix_ml;
-    int prefix_shift;
+    const int* skip;    // kTail: [B], tiles of each request that are not its own
+    int2* units;        // kTail: [unit]: first slot (see slot_of) and parts
+    int whole;          // kTail: the slot of unit 0, for units that are not cut
     bool direct;        // a workgroup per unit
     bool negate;        // scale < 0: queries are negated and |scale| is used
     float c;            // |scale| * log2(e)
@@ -548,7 +538,7 @@ template <Mode kMode>
 __device__ __forceinline__ Req<kMode> plain_block(const AttendArgs& a, int b) {
     Req<kMode> r;
     static_cast<Block&>(r) = block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, nullptr, false);
-    if constexpr (kMode == kTail) r.tiles = r.len > 0 ? a.prefix[b].tiles : 0;
+    if constexpr (kMode == kTail) r.tiles = r.len > 0 ? a.skip[b] : 0;
     return r;
 }
 // The same, where there may be no request.
@@ -603,20 +593,6 @@ struct Joined {
         ref = top;
     }
 };
-
-// The partial results of row `row` (of its request's, for head h) over the shared
-// prefix, from part s on, every `by`-th.
-template <int D>
-__device__ __forceinline__ void join_prefix(const AttendArgs& a, Joined& j, const Prefix& p, int h, int row,
-                                            int ch, int s, int by) {
-    const int at = p.row + row, block = at >> a.prefix_shift, in = at & ((1 << a.prefix_shift) - 1);
-    for (; s < p.parts; s += by) {
-        const long long slot = p.first + ((long long)s * p.blocks + block) * a.pages.heads + h;
-        const long long part = (slot << a.prefix_shift) + in;
-        const float2 ml = a.prefix_ml[part];
-        j.add(ml.x, ml.y, *reinterpret_cast<const f32x4*>(a.prefix_o + part * D + ch));
-    }
-}
 
 // One run of tiles, from the queries to the output or a partial result, for a
 // row block of which kAct row tiles hold rows.
@@ -736,13 +712,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any,
                 sum = mt == n ? total[n] : sum;
                 ref = mt == n ? top[n] : ref;
             }
-            if (wk.slot < 0) {
-                if constexpr (kMode == kTail) {
-                    Joined j{ref, sum, v};
-                    join_prefix<D>(a, j, a.prefix[wk.b], wk.h, row, ch, 0, 1);
-                    v = j.acc;
-                    sum = j.sum;
-                }
+            if (kMode != kTail && wk.slot < 0) {
                 const int t = row / a.group;
                 const float inv = 1.0f / sum;
                 const unsigned w[2] = {pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)};
@@ -759,12 +729,12 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Work& any,
     }
 }
 
+// Workgroup g of `grid`.
 template <int D, int kMT, int kWaves, Mode kMode>
-__global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_kernel(AttendArgs a) {
-    __shared__ Lds<D, kMT, kWaves> sh;
+__device__ __forceinline__ void attend_body(const AttendArgs& a, Lds<D, kMT, kWaves>& sh, int g, unsigned grid) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = scalar(tid >> 6);
-    const int heads = a.pages.heads, g = blockIdx.x;
+    const int heads = a.pages.heads;
 
     if (g == 0) {                     // report bad budgets and lengths, once per call
         for (int b = tid; b < a.B; b += 64 * kWaves) {
@@ -787,7 +757,7 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
         const int per = (a.B + 255) / 256;
         const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
         if (tid == 0) sh.found = -1;
-        if (tid < 2) a.parts[2 * g + tid] = make_int4(0, 0, 0, 0);
+        if (kMode != kTail && tid < 2) a.parts[2 * g + tid] = make_int4(0, 0, 0, 0);
         // The first of this thread's requests (the only one up to 256) is kept.
         const Share<kMT, kMode> first(a, plain_block<kMode>(a, b0, b0 < b1));
         unsigned long long cost = 0;
@@ -823,7 +793,7 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
         if (lane == 0) sh.longest[wave] = longest;
         __syncthreads();
         longest = max(max(sh.longest[0], sh.longest[1]), max(sh.longest[2], sh.longest[3]));
-        aligned = scalar((int)(a.groups + units <= gridDim.x && longest <= share + kSlack)) != 0;
+        aligned = scalar((int)(a.groups + units <= grid && longest <= share + kSlack)) != 0;
         if (!aligned) {
             cost += (unsigned long long)units * kUnitCost;
             share = scalar(max((cost + a.groups - 1) / a.groups, (unsigned long long)kLeastShare));
@@ -886,10 +856,12 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
             const int parts = s.parts(rb, (int)share);
             i0 = (int)((long long)n * part / parts);
             i1 = (int)((long long)n * (part + 1) / parts);
-            if (parts > 1) {
+            if (kMode == kTail || parts > 1) {
                 slot = g;
+                const int u = (b * heads + h) * a.row_blocks + rb;
                 if (tid == 0) {
-                    a.parts[2 * g] = make_int4((b * heads + h) * a.row_blocks + rb, parts, part, g - part);
+                    if (kMode != kTail) a.parts[2 * g] = make_int4(u, parts, part, g - part);
+                    else if (part == 0) a.units[u] = make_int2(g, parts);
                 }
             }
         } else if (!a.direct) {
@@ -907,10 +879,16 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
                 const int before = from > 0 ? (int)((from + width - 1) / width) : 0;
                 const int after = (int)((unsigned)((n - 1) * (int)cost - from) / width);
                 if (tid == 0) {
-                    a.parts[slot] = make_int4((b * heads + h) * a.row_blocks + rb, before + after + 1, before,
-                                              ~(2 * (g - before) + 1));
+                    const int u = (b * heads + h) * a.row_blocks + rb, from = ~(2 * (g - before) + 1);
+                    if (kMode != kTail) a.parts[slot] = make_int4(u, before + after + 1, before, from);
+                    else if (before == 0) a.units[u] = make_int2(from, after + 1);
                 }
             }
+        }
+        if (kMode == kTail && slot < 0 && i0 < i1) {
+            const int u = (b * heads + h) * a.row_blocks + rb;
+            slot = a.whole + u;
+            if (tid == 0) a.units[u] = make_int2(slot, 1);
         }
         if (i0 < i1) {
             const Work wk{b, h, rb, s.span.first + scalar(i0), s.span.first + scalar(i1), slot};
@@ -946,6 +924,12 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
     }
 }
 
+template <int D, int kMT, int kWaves, Mode kMode>
+__global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_kernel(AttendArgs a) {
+    __shared__ Lds<D, kMT, kWaves> sh;
+    attend_body<D, kMT, kWaves, kMode>(a, sh, blockIdx.x, gridDim.x);
+}
+
 // Joins the units that the first kernel left in parts. A workgroup here belongs
 // to one there and to 16 rows of a row block. The 16 rows of a unit of fewer
 // than 16 parts are dealt to the workgroups of its first four parts, a
@@ -954,7 +938,7 @@ __global__ __launch_bounds__(64 * kWaves, (occupancy<D, kMT>())) void attend_ker
 // hold 4 channels, 256 / D parts lie side by side in a wavefront, kDeep of them
 // each are in flight. The order of the sums is fixed by the shapes and lengths
 // of the call.
-template <int D, int kMT, Mode kMode>
+template <int D, int kMT>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     constexpr int kSide = 256 / D, kLanes = 64 / kSide;     // parts side by side, lanes of each
     constexpr int kDeep = 8;
@@ -970,7 +954,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
         if (n == 0 || s0 >= (many ? 16 : 4)) continue;
         const int rb = both[slot].x % a.row_blocks, h = both[slot].x / a.row_blocks % a.pages.heads;
         const int b = both[slot].x / a.row_blocks / a.pages.heads;
-        const int rows = plain_block<kMode>(a, b).len * a.group - rb * (16 * kMT);
+        const int rows = plain_block<kWindow>(a, b).len * a.group - rb * (16 * kMT);
         const int by = many ? kFew * kSide : kSide;
         for (int i = many ? s0 : s0 * kFew + wave; i < 16 && in0 + i < rows; i += many ? 16 : min(n, 4) * kFew) {
             const int in = in0 + i;
@@ -988,10 +972,6 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
                 for (int k = 0; k < kDeep; ++k) {
                     if (s + k * by < n) j.add(ml[k].x, ml[k].y, v[k]);
                 }
-            }
-            if constexpr (kMode == kTail) {
-                join_prefix<D>(a, j, a.prefix[b], h, rb * (16 * kMT) + in, ch,
-                               (many ? wave * kSide : 0) + side, by);
             }
             #pragma unroll
             for (int o = kLanes; o < 64; o <<= 1) {
@@ -1037,7 +1017,7 @@ int resident(int mt) {      // workgroups of a kernel that the 256 CUs hold at o
 }
 
 Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_pages, int window,
-             int sinks = 0) {
+             int sinks = 0, int resident_groups = 0) {
     Plan p;
     const int rows = (K + 1) * (Hq / kv_heads);
     const int widest = D == 256 ? 2 : 4;     // accumulators: kMT D / 4 registers a lane
@@ -1048,7 +1028,8 @@ Plan plan_of(int B, int K, int Hq, int kv_heads, int D, int page_size, int max_p
     if (window > 0) tokens = std::min(tokens, (long long)window + K + kTile + (sinks > 0 ? (long long)sinks + kTile : 0));
     const long long tiles = (tokens + kTile - 1) / kTile + 1;
     const long long most = (units * tiles * (kTileCost + p.mt) + kLeastShare - 1) / kLeastShare;
-    const int held = D == 64 ? resident<64>(p.mt) : D == 128 ? resident<128>(p.mt) : resident<256>(p.mt);
+    const int held = resident_groups > 0 ? resident_groups
+                     : D == 64 ? resident<64>(p.mt) : D == 128 ? resident<128>(p.mt) : resident<256>(p.mt);
     p.groups = (int)std::min<long long>(held, most);
     p.direct = tiles <= kDirectTiles || (units >= held && tiles <= 2 * kDirectTiles) ||
                (units >= (long long)kDirectUnits * held && tiles * held <= kDirectTiles * units);
@@ -1084,7 +1065,7 @@ void launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
     hipLaunchKernelGGL((attend_kernel<D, kMT, kFew, kMode>), dim3((unsigned)p.grid), dim3(64 * kFew), 0, s, a);
     if (!p.direct) {
         const unsigned blocks = (unsigned)(p.grid * kMT);
-        hipLaunchKernelGGL((attend_join_kernel<D, kMT, kMode>), dim3(blocks), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((attend_join_kernel<D, kMT>), dim3(blocks), dim3(256), 0, s, a);
     }
 }
 
