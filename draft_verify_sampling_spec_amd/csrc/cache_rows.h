@@ -30,8 +30,8 @@ __device__ __forceinline__ unsigned quantise8(const float (&x)[8], unsigned& byt
     unsigned amax = 0;
     #pragma unroll
     for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
-    amax = max(amax, (unsigned)__shfl_xor((int)amax, 1));
-    amax = max(amax, (unsigned)__shfl_xor((int)amax, 2));
+    amax = max(amax, (unsigned)__builtin_amdgcn_update_dpp(0, (int)amax, 0xb1, 0xf, 0xf, true));    // lane ^ 1
+    amax = max(amax, (unsigned)__builtin_amdgcn_update_dpp(0, (int)amax, 0x4e, 0xf, 0xf, true));    // lane ^ 2
     byte = cache_scale_byte(amax);
     if (byte == 255u) return 0;
     const float s = scale_of(byte);

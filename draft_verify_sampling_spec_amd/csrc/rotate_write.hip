@@ -13,10 +13,15 @@
 // rounded to bf16 too before they are quantised, so that the cache holds the
 // same bytes as if the rotated keys had been stored and written.
 //
-// A workgroup takes some consecutive tokens of one kv head: its group of query
-// heads, its keys and its values. The angles' sines and cosines lie in LDS, one
-// set for all of the workgroup's heads. D / 8 lanes share a head's row, 8
-// channels each.
+// A wavefront takes a token, its weights and its angles' sines and cosines in registers:
+// D / 8 lanes share a head's row, 8 channels each, 64 lanes a step of 512 / D rows,
+// with kBatch steps' rows asked for together. Sums over a row and its halves'
+// exchange go through lane permutations of the VALU, not through LDS.
+//
+// What bounds it: reads and writes, 4.2 TB/s for prompts (16 of 1,025..2,049 tokens, 32
+// query and 8 kv heads of 128, bf16: 125 us; a copy moves 5.1), then the VALU (a
+// workgroup per token chunk and head, whose rows changed kind and token from step to
+// step, took 212). A step's 48 tokens take 5.4 us.
 #include <cmath>
 
 #include "cache_rows.h"
@@ -43,120 +48,185 @@ struct RotateArgs {
     float eps, factor;
     int Hq, group, heads, shift, num_pages;
     int rot;
-    int per;            // tokens of a workgroup
+    int span;           // kv heads of a workgroup
     bool interleaved, norm_bf16;
 };
 
-constexpr int kMostTokens = 32;
+constexpr int kLeastWaves = 2048;
+constexpr int kBatch = 4;           // steps of a wavefront in flight
 
-template <int D>
-__device__ __forceinline__ void weights8(const void* w, bool bf16, int c, float (&y)[8]) {
-    if (bf16) load8(static_cast<const uint16_t*>(w) + 8 * c, y);
-    else load8(static_cast<const float*>(w) + 8 * c, y);
+// Eight channels as they are stored.
+template <typename S>
+struct Eight {
+    uint4 raw[sizeof(S) / 2];
+    __device__ __forceinline__ void load(const S* p) {
+        #pragma unroll
+        for (int i = 0; i < (int)sizeof(S) / 2; ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const { load8(reinterpret_cast<const S*>(raw), x); }
+};
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, true));
+}
+
+// Sum over the kLanes lanes of a row, in all of them.
+template <int kLanes>
+__device__ __forceinline__ float row_sum(float v) {
+    v += dpp<0xb1>(v);                          // lane ^ 1
+    v += dpp<0x4e>(v);                          // lane ^ 2
+    v += dpp<0x141>(v);                         // the other four of eight
+    if (kLanes >= 16) v += dpp<0x140>(v);       // the other eight of sixteen
+    if (kLanes == 32) {
+        auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    }
+    return v;
+}
+
+// The value half a row of kLanes lanes away.
+template <int kLanes>
+__device__ __forceinline__ float half_row(float v, int lane) {
+    if constexpr (kLanes == 8) return dpp<0x1b>(dpp<0x141>(v));     // 7 - lane, then reversed in fours
+    if constexpr (kLanes == 16) return dpp<0x128>(v);
+    auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(lane & 16 ? a[0] : a[1]);
 }
 
 template <int D, typename S>
-__global__ __launch_bounds__(256) void rotate_write_kernel(RotateArgs a) {
-    constexpr int kLanes = D / 8;
-    __shared__ float2 turn[kMostTokens * (D / 2)];
-    const int h = blockIdx.y, half = a.rot / 2;
-    const long long n0 = (long long)blockIdx.x * a.per;
-    const int count = (int)min((long long)a.per, a.tokens - n0);
-    for (int i = threadIdx.x; i < count * half; i += 256) {
-        const int t = i / half, j = i - t * half;
+__global__ __launch_bounds__(256, 4) void rotate_write_kernel(RotateArgs a) {
+    constexpr int kLanes = D / 8, kSide = 64 / kLanes;      // lanes of a row, rows of a step
+    __shared__ float2 turns[4][D / 2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int c = lane % kLanes, side = lane / kLanes;
+    const int h0 = blockIdx.y * a.span, heads = min(a.span, a.heads - h0), queries = heads * a.group;
+    const int half = a.rot / 2, qs = (queries + kSide - 1) / kSide, ks = (heads + kSide - 1) / kSide;
+    float wq[8], wk[8];
+    if (a.q_norm) {
+        if (a.norm_bf16) load8(static_cast<const uint16_t*>(a.q_norm) + 8 * c, wq);
+        else load8(static_cast<const float*>(a.q_norm) + 8 * c, wq);
+    }
+    if (a.k_norm) {
+        if (a.norm_bf16) load8(static_cast<const uint16_t*>(a.k_norm) + 8 * c, wk);
+        else load8(static_cast<const float*>(a.k_norm) + 8 * c, wk);
+    }
+    const long long n = (long long)blockIdx.x * 4 + wave;
+    if (n >= a.tokens) return;
+    const int slot = __builtin_amdgcn_readfirstlane(a.slots[n]);
+    if (slot < 0) return;
+    if (slot >= (long long)a.num_pages << a.shift) {
+        if (lane == 0) flag(a.status, SV_FLAG_BAD_PAGE);
+        return;
+    }
+    // Steps of kSide rows: queries, then keys, then values.
+    const S* const q = static_cast<const S*>(a.q) + n * a.q_stride + (long long)h0 * a.group * D;
+    const S* const kk = static_cast<const S*>(a.k) + n * a.k_stride + (long long)h0 * D;
+    const S* const v = static_cast<const S*>(a.v) + n * a.v_stride + (long long)h0 * D;
+    Eight<S> in[kBatch];
+    auto ask = [&](int s0) {
+        #pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int s = s0 + i;
+            const S* const src = s < qs ? q : s < qs + ks ? kk : v;
+            const int r = (s < qs ? s : s < qs + ks ? s - qs : s - qs - ks) * kSide + side;
+            if (s < qs + 2 * ks && r < (s < qs ? queries : heads)) in[i].load(src + r * D + 8 * c);
+        }
+    };
+    ask(0);
+    // The angles, while the first rows are on their way.
+    for (int i = lane; i < half; i += 64) {
         // 1 / (2 pi): the angle in turns, of which only the fraction counts.
-        double x = (double)a.positions[n0 + t] * ((double)a.inv_freq[j] * 0.15915494309189533577);
+        double x = (double)a.positions[n] * ((double)a.inv_freq[i] * 0.15915494309189533577);
         x -= rint(x);
         float sn, cs;
         sincospif(2.0f * (float)x, &sn, &cs);
-        turn[t * (D / 2) + j] = make_float2(cs * a.factor, sn * a.factor);
+        turns[wave][i] = make_float2(cs * a.factor, sn * a.factor);
     }
-    __syncthreads();
-    const int rows = a.group + 2, c = threadIdx.x % kLanes;
-    const long long capacity = (long long)a.num_pages << a.shift;
-    // Whole rows at a time: the lanes of a row agree on every branch.
-    for (int i = threadIdx.x / kLanes; i < count * rows; i += 256 / kLanes) {
-        const int t = i / rows, r = i - t * rows;
-        const long long n = n0 + t;
-        const int slot = a.slots[n];
-        if (slot < 0) continue;
-        if (slot >= capacity) {
-            if (c == 0) flag(a.status, SV_FLAG_BAD_PAGE);
-            continue;
-        }
-        const bool query = r < a.group, value = r == a.group + 1;
-        const S* src = query   ? static_cast<const S*>(a.q) + n * a.q_stride + (long long)(h * a.group + r) * D
-                       : value ? static_cast<const S*>(a.v) + n * a.v_stride + (long long)h * D
-                               : static_cast<const S*>(a.k) + n * a.k_stride + (long long)h * D;
-        float x[8];
-        load8(src + 8 * c, x);
-        if (!value) {
-            const void* norm = query ? a.q_norm : a.k_norm;
-            if (norm) {
-                float sum = 0.0f;
-                #pragma unroll
-                for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(x[j], x[j], sum);
-                #pragma unroll
-                for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor(sum, o);
-                const float f = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
-                float w[8];
-                weights8<D>(norm, a.norm_bf16, c, w);
-                #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = x[j] * f * w[j];
-            }
-            if (a.interleaved) {
-                if (8 * c < a.rot) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // read by other lanes of the wavefront only
+    // Channel j becomes x_j cs_j + (its pair's other) sn_j.
+    float cs[8], sn[8];
+    #pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int ch = 8 * c + j;
+        const bool second = a.interleaved ? (j & 1) != 0 : ch >= half;
+        float2 turn = make_float2(1.0f, 0.0f);
+        if (8 * c < a.rot) turn = turns[wave][a.interleaved ? ch / 2 : second ? ch - half : ch];
+        cs[j] = turn.x;
+        sn[j] = second ? turn.y : -turn.y;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int in_page = slot & ((1 << a.shift) - 1), tok = in_page & (kTile - 1);
+    uint8_t* const tile = a.cache + ((((long long)(slot >> a.shift) * a.heads + h0) << (a.shift - 5)) + (in_page >> 5)) * Tile<D>::kBytes;
+    const int head_bytes = Tile<D>::kBytes << (a.shift - 5);
+    for (int s0 = 0; s0 < qs + 2 * ks; s0 += kBatch) {
+        if (s0 > 0) ask(s0);
+        #pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int s = s0 + i;
+            if (s >= qs + 2 * ks) break;
+            const bool query = s < qs, value = s >= qs + ks;
+            const int r = (query ? s : value ? s - qs - ks : s - qs) * kSide + side;
+            if (r >= (query ? queries : heads)) continue;       // whole rows
+            float x[8];
+            in[i].get(x);
+            if (!value) {
+                if (query ? a.q_norm != nullptr : a.k_norm != nullptr) {
+                    float sum = 0.0f;
                     #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 cs = turn[t * (D / 2) + 4 * c + j];
-                        const float p = x[2 * j], q = x[2 * j + 1];
-                        x[2 * j] = __builtin_fmaf(p, cs.x, -(q * cs.y));
-                        x[2 * j + 1] = __builtin_fmaf(q, cs.x, p * cs.y);
+                    for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(x[j], x[j], sum);
+                    const float f = __builtin_amdgcn_rsqf(row_sum<kLanes>(sum) * (1.0f / D) + a.eps);
+                    #pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = x[j] * f * (query ? wq[j] : wk[j]);
+                }
+                if (a.rot > 0) {
+                    float other[8];
+                    if (a.interleaved) {
+                        #pragma unroll
+                        for (int j = 0; j < 8; ++j) other[j] = x[j ^ 1];
+                    } else if (a.rot == D) {
+                        #pragma unroll
+                        for (int j = 0; j < 8; ++j) other[j] = half_row<kLanes>(x[j], lane);
+                    } else {
+                        // rot / 16 lanes away; lanes that do not turn take their own.
+                        const int away = a.rot / 16;
+                        const int from = 8 * c < half ? lane + away : 8 * c < a.rot ? lane - away : lane;
+                        #pragma unroll
+                        for (int j = 0; j < 8; ++j) other[j] = __shfl(x[j], from);
+                    }
+                    if (8 * c < a.rot) {        // a product with 0 would spread an infinity
+                        #pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(x[j], cs[j], other[j] * sn[j]);
                     }
                 }
-            } else {
-                // The other channel of a pair lies rot / 16 lanes away.
-                const int away = a.rot / 16, first = 8 * c < half ? c : c - away;
-                const bool turns = 8 * c < a.rot;
-                const int lane = threadIdx.x & 63;
-                const int from = turns ? (8 * c < half ? lane + away : lane - away) : lane;
+                unsigned w[4];
                 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float other = __shfl(x[j], from);
-                    if (turns) {
-                        const float2 cs = turn[t * (D / 2) + 8 * first + j];
-                        x[j] = __builtin_fmaf(x[j], cs.x, 8 * c < half ? -(other * cs.y) : other * cs.y);
-                    }
+                for (int j = 0; j < 4; ++j) w[j] = pack2(x[2 * j], x[2 * j + 1]);
+                uint16_t* out = query ? a.out + (n * a.Hq + h0 * a.group) * (long long)D
+                                      : a.out_keys ? a.out_keys + (n * a.heads + h0) * (long long)D : nullptr;
+                if (out) *reinterpret_cast<uint4*>(out + r * D + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (query) continue;
+                #pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[2 * j] = __uint_as_float(w[j] << 16);
+                    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
                 }
             }
-            unsigned w[4];
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = pack2(x[2 * j], x[2 * j + 1]);
-            uint16_t* out = query ? a.out + (n * a.Hq + h * a.group + r) * (long long)D
-                                  : a.out_keys ? a.out_keys + (n * a.heads + h) * (long long)D : nullptr;
-            if (out) *reinterpret_cast<uint4*>(out + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (query) continue;
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[2 * j] = __uint_as_float(w[j] << 16);
-                x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            uint8_t* const mine = tile + (long long)r * head_bytes;
+            unsigned byte;
+            const unsigned w = quantise8(x, byte);
+            put_codes<D>(mine, value, tok, c, w);
+            if ((c & 3) == 0) {
+                mine[value ? Tile<D>::v_scale(tok, c >> 2) : Tile<D>::k_scale(tok, c >> 2)] = (uint8_t)byte;
             }
-        }
-        const int in = slot & ((1 << a.shift) - 1), tok = in & (kTile - 1);
-        uint8_t* tile = a.cache + ((((long long)(slot >> a.shift) * a.heads + h) << (a.shift - 5)) + (in >> 5)) * Tile<D>::kBytes;
-        unsigned byte;
-        const unsigned w = quantise8(x, byte);
-        put_codes<D>(tile, value, tok, c, w);
-        if ((c & 3) == 0) {
-            tile[value ? Tile<D>::v_scale(tok, c >> 2) : Tile<D>::k_scale(tok, c >> 2)] = (uint8_t)byte;
         }
     }
 }
 
 template <int D, typename S>
-void launch(RotateArgs a, hipStream_t s) {
-    const unsigned chunks = (unsigned)((a.tokens + a.per - 1) / a.per);
-    hipLaunchKernelGGL((rotate_write_kernel<D, S>), dim3(chunks, (unsigned)a.heads), dim3(256), 0, s, a);
+void launch(const RotateArgs& a, hipStream_t s) {
+    const unsigned chunks = (unsigned)((a.tokens + 3) / 4);
+    hipLaunchKernelGGL((rotate_write_kernel<D, S>), dim3(chunks, (unsigned)((a.heads + a.span - 1) / a.span)), dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -222,7 +292,11 @@ extern "C" int spec_verify_cache_write_rotated(
     a.shift = __builtin_ctz((unsigned)page_size);
     a.num_pages = num_pages;
     a.rot = rot;
-    a.per = 8;
+    // All heads of a token to one wavefront, which then forms its angles once, or
+    // fewer where that gives the chip too few wavefronts (prompts of 32,784 tokens: 125
+    // us with 8 heads, 143 with 4; a step's 48 tokens: 5.4 with 1 head, 7.2 with 4).
+    a.span = kv_heads;
+    while (a.span > 1 && tokens * ((kv_heads + a.span - 1) / a.span) < kLeastWaves) a.span = (a.span + 1) / 2;
     a.interleaved = interleaved != 0;
     a.norm_bf16 = norm_dtype == SV_DTYPE_BF16;
     const hipStream_t s = static_cast<hipStream_t>(stream);
