@@ -1123,6 +1123,8 @@ class PageTables:
         self.refs = torch.zeros(self.num_pages, dtype=torch.int32, device=device) \
             if refs is None else refs
         self._state()
+        # For small tables, whose plan leaves its 256 bytes alone.
+        self._unused = torch.empty(256, dtype=torch.uint8, device=device)
 
     def _state(self):
         return (_need(self.table, "table", torch.int32, (self.B, self.max_pages), self._index),
@@ -1157,7 +1159,8 @@ class PageTables:
             out = (torch.empty_strided((B,), (1,), dtype=torch.int32, device=device),
                    torch.empty_strided((B, T), (T, 1), dtype=torch.int32, device=device),
                    torch.empty_strided((B, T), (T, 1), dtype=torch.int32, device=device))
-        workspace = torch.empty_strided((self._bytes,), (1,), dtype=torch.uint8, device=self.device)
+        workspace = self._unused if self._bytes == 256 else torch.empty_strided(
+            (self._bytes,), (1,), dtype=torch.uint8, device=self.device)
         table, refs = self._state()
         rows = (B,)
         rc = load().spec_verify_pages_plan(

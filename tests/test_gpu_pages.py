@@ -63,6 +63,12 @@ class Steps:
     (12, 40, 300, 64, 1, 1, 0),
     (12, 40, 90, 32, 9, 300, 70),
     (5, 700, 3000, 32, 2049, 3000, 33),  # chunks of prompts
+    (12, 200, 2000, 32, 2000, 0, 0),     # one workgroup's table, more tokens than it writes itself
+    (40, 500, 9000, 32, 9, 0, 0),        # a workgroup a row, several chunks of the pool
+    (40, 500, 5500, 32, 9, 700, 40),     # too few pages
+    (7, 3000, 17000, 32, 2100, 0, 0),    # tokens by a kernel of their own
+    (3, 40, 70000, 32, 9, 0, 0),         # a small table over a large pool
+    (1024, 16, 16384, 32, 16, 0, 0),     # the largest table of one workgroup
 ])
 def test_steps(B, width, pages, page, T, window, sinks):
     _log(f"[pages] B={B} width={width} pages={pages} page={page} T={T} window={window} sinks={sinks}")
@@ -94,6 +100,17 @@ def test_more_requests_than_a_round_of_the_sum():
     for _ in range(3):
         s.step(ctx, rng.integers(0, 2, 2500))
         ctx = np.where(ctx < 0, 5, np.where(ctx > 90, -1, ctx + 20))
+
+
+def test_a_pool_of_millions_of_pages():
+    """Chunks of the pool that take a workgroup several rounds; free pages far apart."""
+    s = Steps(3, 9, 5_000_000, 32, 2)
+    s.refs[:] = 1
+    s.refs[[0, 4095, 4096, 8191, 8192, 12345, 4_999_999, 4_500_000]] = 0
+    s.set()
+    assert s.step([60, 10, 100], [1, 1, 1]) == 0
+    assert s.step([96, 40, 130], [1, 1, 1]) == sb.SV_FLAG_NO_PAGES
+    s.step([-1, 40, 130], [1, 1, 1])
 
 
 def test_the_largest_lengths():
