@@ -20,6 +20,11 @@
 // chunk of the pool (its free pages listed) and one that sums the rows' counts,
 // then the rows again (new pages, slots); a row's classification is cheaper to
 // repeat than to keep. Tokens that are many for a row's workgroup take one more.
+//
+// What bounds them is the latency of a few trips to memory one after another: the
+// small kernel 7.4 us (8 requests of 64 pages), the three others 5.5 + 4.2 + 7.5 for
+// 512 requests of 1,024 pages out of 524,288, where reading table and counts once
+// takes 0.7.
 #include <initializer_list>
 
 #include "cache_tile.h"

@@ -8,8 +8,8 @@
 //   (y_i cos a - y_j sin a, y_j cos a + y_i sin a) * factor.
 // Sums and products are fp32. A position times a frequency loses its fraction
 // in fp32 (at 10^6 a step is 2^-4 radians), so the angle is formed in fp64, in
-// turns, its fraction is exact to 2^-29, and only then sine and cosine are taken
-// in fp32. Queries are rounded to bf16, what the attention reads. Keys are
+// turns, and its sine and cosine too, once a token, before they are rounded to
+// fp32. Queries are rounded to bf16, what the attention reads. Keys are
 // rounded to bf16 too before they are quantised, so that the cache holds the
 // same bytes as if the rotated keys had been stored and written.
 //
@@ -18,8 +18,8 @@
 // with kBatch steps' rows asked for together. Sums over a row and its halves'
 // exchange go through lane permutations of the VALU, not through LDS.
 //
-// What bounds it: reads and writes, 4.2 TB/s for prompts (16 of 1,025..2,049 tokens, 32
-// query and 8 kv heads of 128, bf16: 125 us; a copy moves 5.1), then the VALU (a
+// What bounds it: reads and writes, 4.3 TB/s for prompts (16 of 1,025..2,049 tokens, 32
+// query and 8 kv heads of 128, bf16: 122 us; a copy moves 5.1), then the VALU (a
 // workgroup per token chunk and head, whose rows changed kind and token from step to
 // step, took 212). A step's 48 tokens take 5.4 us.
 #include <cmath>
@@ -139,9 +139,9 @@ __global__ __launch_bounds__(256, 4) void rotate_write_kernel(RotateArgs a) {
         // 1 / (2 pi): the angle in turns, of which only the fraction counts.
         double x = (double)a.positions[n] * ((double)a.inv_freq[i] * 0.15915494309189533577);
         x -= rint(x);
-        float sn, cs;
-        sincospif(2.0f * (float)x, &sn, &cs);
-        turns[wave][i] = make_float2(cs * a.factor, sn * a.factor);
+        double sn, cs;
+        sincospi(2.0 * x, &sn, &cs);
+        turns[wave][i] = make_float2((float)cs * a.factor, (float)sn * a.factor);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // read by other lanes of the wavefront only
     // Channel j becomes x_j cs_j + (its pair's other) sn_j.
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(256, 4) void rotate_write_kernel(RotateArgs a) {
                     }
                     if (8 * c < a.rot) {        // a product with 0 would spread an infinity
                         #pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(x[j], cs[j], other[j] * sn[j]);
+                        for (int j = 0; j < 8; ++j) x[j] = x[j] * cs[j] + other[j] * sn[j];
                     }
                 }
                 unsigned w[4];

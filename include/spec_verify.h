@@ -587,9 +587,10 @@ size_t spec_verify_pages_plan_workspace_bytes(int B, int max_pages, int num_page
  * and its first `rot` channels are turned in pairs by a = positions[n] *
  * inv_freq[i]: (y_i, y_j) -> factor (y_i cos a - y_j sin a, y_j cos a + y_i
  * sin a), with j = i + rot / 2, or, interleaved, channels 2 i and 2 i + 1.
- * Sums, products, sine and cosine are fp32, the angle's fraction of a turn is
- * right to 2^-29 for |position| <= 2^24 and frequencies up to 1; magnitudes
- * whose squares' sum leaves fp32's range are not normalised rightly. Queries
+ * Sums and products are fp32; angles, sine and cosine are formed in fp64 (right
+ * to 2^-29 of a turn for |position| <= 2^24 and frequencies up to 1) and rounded
+ * to fp32; magnitudes whose squares' sum leaves fp32's range are not normalised
+ * rightly. Queries
  * are rounded to bf16 once; keys are rounded to bf16 and then quantised, so
  * that the cache's bytes are those of spec_verify_cache_write on out_keys.
  * Stream-ordered, one launch.
