@@ -49,6 +49,7 @@ constexpr int kRows = 128;          // rows of a workgroup of the prefix part
 // more parts save less (8 requests behind 2,000 tokens: the work 14.9 and the join
 // 5.0 us with 8, 16.7 and 6.9 with 4, 16.8 and 4.1 with 16).
 constexpr int kLeastTiles = 8;
+constexpr int kFewRows = 4096;      // of a call, a workgroup of the join each
 
 // What the plan leaves for a group that shares something.
 struct Group {
@@ -501,13 +502,16 @@ __global__ __launch_bounds__(256, shared_occupancy<D>()) void shared_work_kernel
 }
 
 // A workgroup joins 1024 / D rows of the outputs, D / 4 lanes and 4 channels a lane
-// each. Parts in the order of the positions, kDeep of them in flight.
-template <int D>
+// each, or (kSplit) one row, whose parts are dealt to its 1024 / D sets of lanes: few
+// rows may have many parts each. The prefix's parts, then the request's own;
+// kDeep of them in flight.
+template <int D, bool kSplit>
 __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s, int unit_rows) {
     const AttendArgs& a = s.a;
-    constexpr int kLanes = D / 4, kDeep = 4;
-    const long long row = (long long)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
-    const int ch = threadIdx.x % kLanes * 4;
+    constexpr int kLanes = D / 4, kSets = 256 / kLanes, kDeep = 4, kBy = kSplit ? kSets : 1;
+    __shared__ Joined sh[kSplit ? 256 : 1];
+    const int set = threadIdx.x / kLanes, ch = threadIdx.x % kLanes * 4;
+    const long long row = kSplit ? blockIdx.x : (long long)blockIdx.x * kSets + set;
     if (row >= (long long)a.B * (a.K + 1) * a.Hq) return;
     const int head = (int)(row % a.Hq), b = (int)(row / a.Hq / (a.K + 1)), t = (int)(row / a.Hq % (a.K + 1));
     const Block blk = block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, nullptr, false);
@@ -515,28 +519,36 @@ __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s, int unit
     const int h = head / a.group, r = t * a.group + (head - h * a.group);
     const Prefix p = s.prefix[b];
     const int2 unit = a.units[(b * a.pages.heads + h) * a.row_blocks + r / unit_rows];
+    const int at = p.row + r, n = p.parts + unit.y;
     Joined j{kNegInf, 0.0f, {0, 0, 0, 0}};
-    auto take = [&](int n, const float2* ml, const float* o, auto place) {
-        for (int i = 0; i < n; i += kDeep) {
-            float2 m[kDeep];
-            f32x4 v[kDeep];
-            #pragma unroll
-            for (int k = 0; k < kDeep; ++k) {
-                const long long at = place(min(i + k, n - 1));
-                m[k] = ml[at];
-                v[k] = *reinterpret_cast<const f32x4*>(o + at * D + ch);
-            }
-            #pragma unroll
-            for (int k = 0; k < kDeep; ++k) {
-                if (i + k < n) j.add(m[k].x, m[k].y, v[k]);
-            }
+    for (int i = kSplit ? set : 0; i < n; i += kDeep * kBy) {
+        float2 m[kDeep];
+        f32x4 v[kDeep];
+        #pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            const int x = min(i + k * kBy, n - 1);
+            const bool shared = x < p.parts;
+            const long long place =
+                shared ? (p.first + ((long long)x * p.blocks + at / kRows) * a.pages.heads + h) * kRows + at % kRows
+                       : (long long)slot_of(unit.x, x - p.parts) * unit_rows + r % unit_rows;
+            m[k] = (shared ? s.prefix_ml : a.part_ml)[place];
+            v[k] = *reinterpret_cast<const f32x4*>((shared ? s.prefix_o : a.part_o) + place * D + ch);
         }
-    };
-    const int at = p.row + r;
-    take(p.parts, s.prefix_ml, s.prefix_o, [&](int i) {
-        return (p.first + ((long long)i * p.blocks + at / kRows) * a.pages.heads + h) * kRows + at % kRows;
-    });
-    take(unit.y, a.part_ml, a.part_o, [&](int i) { return (long long)slot_of(unit.x, i) * unit_rows + r % unit_rows; });
+        #pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            if (i + k * kBy < n) j.add(m[k].x, m[k].y, v[k]);
+        }
+    }
+    if constexpr (kSplit) {
+        sh[threadIdx.x] = j;
+        __syncthreads();
+        if (set > 0) return;
+        #pragma unroll
+        for (int k = 1; k < kSets; ++k) {
+            const Joined& other = sh[k * kLanes + threadIdx.x];
+            j.add(other.ref, other.sum, other.acc);
+        }
+    }
     const float inv = 1.0f / j.sum;
     const unsigned w[2] = {pack_bf16(j.acc[0] * inv, j.acc[1] * inv), pack_bf16(j.acc[2] * inv, j.acc[3] * inv)};
     __builtin_memcpy(__builtin_assume_aligned(a.out + row * D + ch, 8), w, 8);
@@ -587,9 +599,14 @@ void launch_shared(const SharedArgs& s, const SharedPlan& p, hipStream_t stm) {
         case 3: hipLaunchKernelGGL((shared_work_kernel<D, (D == 256 ? 2 : 3)>), grid, dim3(256), 0, stm, s); break;
         default: hipLaunchKernelGGL((shared_work_kernel<D, (D == 256 ? 2 : 4)>), grid, dim3(256), 0, stm, s); break;
     }
+    // The fewer rows, the more parts each may have (at most the prefix part's workgroups).
     const long long rows = (long long)s.a.B * (s.a.K + 1) * s.a.Hq;
-    hipLaunchKernelGGL((shared_join_kernel<D>), dim3((unsigned)((rows * D + 1023) / 1024)), dim3(256), 0, stm, s,
-                       16 * p.tail.mt);
+    if (rows <= kFewRows) {
+        hipLaunchKernelGGL((shared_join_kernel<D, true>), dim3((unsigned)rows), dim3(256), 0, stm, s, 16 * p.tail.mt);
+    } else {
+        hipLaunchKernelGGL((shared_join_kernel<D, false>), dim3((unsigned)((rows * D + 1023) / 1024)), dim3(256), 0, stm,
+                           s, 16 * p.tail.mt);
+    }
 }
 
 }  // namespace
@@ -629,7 +646,7 @@ extern "C" int spec_verify_attention_shared(const void* queries, int64_t query_s
     char* ws = static_cast<char*>(workspace);
     SharedArgs s{};
     s.a = args_of(p.tail, queries, query_stride, cache, page_table, ctx_lens, budgets, B, K, q_heads, kv_heads,
-                  page_size, max_pages, num_pages, scale, out, out_status, nullptr);
+                  page_size, max_pages, num_pages, scale, out, out_status, ws + p.at_units);
     s.a.skip = s.skip = reinterpret_cast<int*>(ws + p.at_skip);
     s.a.units = reinterpret_cast<int2*>(ws + p.at_units);
     s.a.whole = p.tail.slots;

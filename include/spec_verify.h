@@ -608,7 +608,8 @@ size_t spec_verify_pages_plan_workspace_bytes(int B, int max_pages, int num_page
  *                NULL; eps finite, at least 0.
  *   out_queries  bf16 [tokens, q_heads, head_dim]; out_keys bf16 [tokens,
  *                kv_heads, head_dim] or NULL (device, 16-byte aligned). Rows of
- *                skipped tokens keep their values.
+ *                skipped tokens keep their values. They may not overlap any
+ *                other argument.
  * kv_heads, head_dim, page_size, num_pages, cache, out_status as above;
  * num_pages * page_size is at most 2^31 - 1.
  * Errors (nothing enqueued): SV_ERR_ARG, SV_ERR_DTYPE, SV_ERR_NULL,

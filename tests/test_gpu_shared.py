@@ -132,6 +132,8 @@ def test_lengths_of_the_prefix(lens):
 @pytest.mark.parametrize("B,G,K,Hq,Hkv,D,prefix,tail", [
     (70, 1, 3, 16, 2, 128, 3000, 300),      # several row blocks, parts of the prefix
     (3, 1, 0, 8, 8, 128, 40000, 90),        # few rows, many parts
+    (2, 1, 0, 4, 1, 64, 60000, 50),         # eight rows, hundreds of parts each
+    (2, 1, 1, 2, 1, 256, 20000, 9000),
     (40, 9, 1, 12, 4, 64, 1500, 700),       # groups of unlike sizes
     (33, 2, 8, 8, 1, 256, 2500, 1100),
     (300, 1, 0, 8, 8, 64, 700, 40),
