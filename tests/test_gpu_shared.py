@@ -164,6 +164,21 @@ def test_more_requests_than_a_round_of_the_plan():
     c.check(c.run())
 
 
+@pytest.mark.parametrize("used,longest", [(1500, 3000), (150, 400)])
+def test_own_tokens_of_many_requests_are_cut(used, longest):
+    """1,500 requests under tables of more than 2,048 tokens: all in use, a few of them long (on a
+    line), and a tenth in use, much alike (equal parts)."""
+    rng = np.random.default_rng(used)
+    B, G = 1500, 12
+    ctx = np.full(B, -1)
+    some = np.sort(rng.permutation(B)[:used])
+    ctx[some] = 64 + rng.integers(0, 60 if used == B else longest, used)
+    ctx[some[::200]] = 64 + longest
+    c = Case(rng.integers(-1, G, B), np.full(G, 64), ctx, rng.integers(0, 2, B), 1, 2, 1, 64, 32, seed=4)
+    c.table = np.pad(c.table, ((0, 0), (0, 80)), constant_values=-1)
+    c.check(c.run())
+
+
 def test_the_most_groups():
     B = 2 * sb.SV_MAX_GROUPS
     groups = np.arange(B) % sb.SV_MAX_GROUPS
