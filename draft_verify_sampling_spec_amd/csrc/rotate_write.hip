@@ -54,6 +54,7 @@ struct RotateArgs {
 
 constexpr int kLeastWaves = 2048;
 constexpr int kBatch = 4;           // steps of a wavefront in flight
+constexpr unsigned kAcross = 1 << 16;   // workgroups of a grid's x; a dimension holds less than 2^32 threads
 
 // Eight channels as they are stored.
 template <typename S>
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(256, 4) void rotate_write_kernel(RotateArgs a) {
         if (a.norm_bf16) load8(static_cast<const uint16_t*>(a.k_norm) + 8 * c, wk);
         else load8(static_cast<const float*>(a.k_norm) + 8 * c, wk);
     }
-    const long long n = (long long)blockIdx.x * 4 + wave;
+    const long long n = ((long long)blockIdx.z * gridDim.x + blockIdx.x) * 4 + wave;
     if (n >= a.tokens) return;
     const int slot = __builtin_amdgcn_readfirstlane(a.slots[n]);
     if (slot < 0) return;
@@ -226,7 +227,9 @@ __global__ __launch_bounds__(256, 4) void rotate_write_kernel(RotateArgs a) {
 template <int D, typename S>
 void launch(const RotateArgs& a, hipStream_t s) {
     const unsigned chunks = (unsigned)((a.tokens + 3) / 4);
-    hipLaunchKernelGGL((rotate_write_kernel<D, S>), dim3(chunks, (unsigned)((a.heads + a.span - 1) / a.span)), dim3(256), 0, s, a);
+    const dim3 grid(chunks < kAcross ? chunks : kAcross, (unsigned)((a.heads + a.span - 1) / a.span),
+                    (chunks + kAcross - 1) / kAcross);
+    hipLaunchKernelGGL((rotate_write_kernel<D, S>), grid, dim3(256), 0, s, a);
 }
 
 }  // namespace

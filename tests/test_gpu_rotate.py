@@ -191,6 +191,23 @@ def test_a_pool_past_32_bit_offsets():
     assert not big.pool[1:-2].any()
 
 
+def test_more_tokens_than_a_row_of_the_grid():
+    """300,000 tokens, against two calls of 150,000."""
+    n, D = 300_000, 64
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q, k, v = (torch.randn(1, n, 1, D, generator=g, device=DEV).bfloat16() for _ in range(3))
+    slots = torch.randperm(n, generator=g, device=DEV).int()[None]
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)[None]
+    f = torch.tensor(_freq(D), dtype=torch.float32, device=DEV)
+    one, two = (BlockCache(DEV, n // 64 + 1, 1, D, 64) for _ in range(2))
+    for c in (one, two):
+        c.pool.zero_()
+    got = one.write_rotated(q, k, v, slots, pos, f)
+    parts = [two.write_rotated(*(x[:, i:i + n // 2].contiguous() for x in (q, k, v, slots, pos)), f)
+             for i in (0, n // 2)]
+    assert torch.equal(got, torch.cat(parts, 1)) and torch.equal(one.pool, two.pool)
+
+
 def test_bad_arguments_are_refused():
     c = Case(1, 3, 2, 1, 64, 32, torch.bfloat16, seed=5)
     cache = c.cache()
