@@ -50,6 +50,7 @@ constexpr int kRows = 128;          // rows of a workgroup of the prefix part
 // 5.0 us with 8, 16.7 and 6.9 with 4, 16.8 and 4.1 with 16).
 constexpr int kLeastTiles = 8;
 constexpr int kFewRows = 4096;      // of a call, a workgroup of the join each
+constexpr long long kAcross = 1 << 16;  // of the join's workgroups in x; a dimension holds less than 2^32 threads
 
 // What the plan leaves for a group that shares something.
 struct Group {
@@ -517,7 +518,7 @@ __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs s, int unit
     constexpr int kLanes = D / 4, kSets = 256 / kLanes, kDeep = 4, kBy = kSplit ? kSets : 1;
     __shared__ Joined sh[kSplit ? 256 : 1];
     const int set = threadIdx.x / kLanes, ch = threadIdx.x % kLanes * 4;
-    const long long row = kSplit ? blockIdx.x : (long long)blockIdx.x * kSets + set;
+    const long long row = kSplit ? blockIdx.x : ((long long)blockIdx.y * gridDim.x + blockIdx.x) * kSets + set;
     if (row >= (long long)a.B * (a.K + 1) * a.Hq) return;
     const int head = (int)(row % a.Hq), b = (int)(row / a.Hq / (a.K + 1)), t = (int)(row / a.Hq % (a.K + 1));
     const Block blk = block_of(a.ctx_lens, a.budgets, b, a.K + 1, a.pages, nullptr, false);
@@ -610,8 +611,9 @@ void launch_shared(const SharedArgs& s, const SharedPlan& p, hipStream_t stm) {
     if (rows <= kFewRows) {
         hipLaunchKernelGGL((shared_join_kernel<D, true>), dim3((unsigned)rows), dim3(256), 0, stm, s, 16 * p.tail.mt);
     } else {
-        hipLaunchKernelGGL((shared_join_kernel<D, false>), dim3((unsigned)((rows * D + 1023) / 1024)), dim3(256), 0, stm,
-                           s, 16 * p.tail.mt);
+        const long long joins = (rows * D + 1023) / 1024;
+        const dim3 across((unsigned)std::min(joins, kAcross), (unsigned)((joins + kAcross - 1) / kAcross));
+        hipLaunchKernelGGL((shared_join_kernel<D, false>), across, dim3(256), 0, stm, s, 16 * p.tail.mt);
     }
 }
 

@@ -179,6 +179,13 @@ def test_own_tokens_of_many_requests_are_cut(used, longest):
     c.check(c.run())
 
 
+def test_more_rows_than_a_row_of_the_joins_grid():
+    rng = np.random.default_rng(3)
+    B = 1024
+    c = Case(np.zeros(B, int), [64], 64 + rng.integers(0, 20, B), np.full(B, 32), 32, 16, 2, 128, 32, seed=6)
+    c.check(c.run())
+
+
 def test_the_most_groups():
     B = 2 * sb.SV_MAX_GROUPS
     groups = np.arange(B) % sb.SV_MAX_GROUPS
