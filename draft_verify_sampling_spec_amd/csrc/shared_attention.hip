@@ -28,11 +28,12 @@
 // decoding lanes write without conflicts; it is undone when results are stored.
 //
 // What bounds it: 128 blocks of 3..9 rows x 4 heads behind 8,192 tokens (8 kv heads of
-// 128) 144 us, 9.1e10 operations, of which the plan takes 5, the work 131, the join 13.
-// In the prefix part a workgroup's tile takes 0.43 us with two workgroups a CU; its
-// products alone take 0.25, the rest is decoding (0.1) and the softmax, which a
-// wavefront takes one after another with its products and two wavefronts a SIMD hide
-// from each other only in part. Starting and ending a part takes 6 us.
+// 128) 138 us, 9.1e10 operations; traced, which slows them, the plan takes 5.6, the
+// work 132.7, the join 12.2. In the prefix part a workgroup's tile took 0.43 us with
+// two workgroups a CU before the priorities set below (4 us in all); its products alone
+// take 0.25, the rest is decoding (0.1) and the softmax, which a wavefront takes one
+// after another with its products and two wavefronts a SIMD hide from each other only
+// in part. Starting and ending a part takes 6 us.
 #include <algorithm>
 #include <climits>
 
