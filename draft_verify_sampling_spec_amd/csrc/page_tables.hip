@@ -6,7 +6,8 @@
 // row's window (at or behind ctx - window + 1). A page that a row holds and
 // does not need is given back (one reference less); a needed page that the row
 // does not hold is taken from the same place of its parent's row (a shared
-// prefix, one reference more) or is new: new pages are the lowest-numbered
+// prefix, one reference more; only pages in front of the row's new tokens, whose
+// slots so never lie in another row's page) or is new: new pages are the lowest-numbered
 // free ones (no references), dealt out in the order of requests and, within
 // one, of positions. A request whose new pages, with those of all requests
 // before it, are more than there are free gets none. Everything is whole
@@ -96,6 +97,13 @@ __device__ __forceinline__ int parent_of(const PlanArgs& a, int b, bool report) 
     return p;
 }
 
+// How many of its first pages the row may take from the parent's: whole pages of
+// the prefix, in front of its own new tokens.
+__device__ __forceinline__ int common_of(const PlanArgs& a, const Row& r, int b, int parent) {
+    if (parent < 0 || r.len == 0) return 0;
+    return min(max(a.prefix_lens[b], 0), r.ctx) >> a.pages.shift;
+}
+
 __device__ __forceinline__ bool in_pool(const PlanArgs& a, int page) {
     return (unsigned)page < (unsigned)a.pages.num_pages;
 }
@@ -122,10 +130,6 @@ __device__ __forceinline__ Entry classify(const PlanArgs& a, const Row& r, int32
     atomicAdd(a.refs + shared, 1);
     row[i] = shared;
     return Entry{shared, false};
-}
-
-__device__ __forceinline__ int common_of(const PlanArgs& a, const Row& r, int b, int parent) {
-    return parent >= 0 && r.len > 0 ? max(a.prefix_lens[b], 0) >> a.pages.shift : 0;
 }
 
 // Slot and position of token t of a request whose tokens start at `start`.
@@ -165,14 +169,16 @@ __device__ __forceinline__ int exclusive(int v, int& total, int (&sums)[kWaves])
 // All of a small call: B <= 1024, B max_pages and num_pages at most kSmall.
 __global__ __launch_bounds__(1024) void plan_small_kernel(PlanArgs a) {
     __shared__ Row rows[1024];
-    __shared__ int parents[1024], ends[1024];       // ends: new pages up to the end of each row
+    __shared__ int parents[1024], commons[1024], ends[1024];    // ends: new pages up to the end of each row
     __shared__ int sums[16];
     __shared__ uint16_t list[kSmall];               // free pages
     const int tid = threadIdx.x, width = a.pages.max_pages, all = a.B * width;
     if (tid < a.B) {
         const Row r = row_of(a, tid, true);
         rows[tid] = r;
-        parents[tid] = r.keep ? -1 : parent_of(a, tid, true);
+        const int p = r.keep ? -1 : parent_of(a, tid, true);
+        parents[tid] = p;
+        commons[tid] = common_of(a, r, tid, p);
     }
     __syncthreads();
     // Consecutive entries of a thread.
@@ -190,8 +196,7 @@ __global__ __launch_bounds__(1024) void plan_small_kernel(PlanArgs a) {
             if (r.keep) {
                 e.page = row[i];
             } else {
-                const int p = parents[b];
-                e = classify(a, r, row, i, a.table + (size_t)max(p, 0) * width, common_of(a, r, b, p));
+                e = classify(a, r, row, i, a.table + (size_t)max(parents[b], 0) * width, commons[b]);
             }
             pages[k] = e.page;
             want |= (unsigned)e.want << k;

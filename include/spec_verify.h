@@ -545,11 +545,17 @@ int spec_verify_cache_write(const void* keys, const void* values, int dtype, int
  *   page_refs    int32 [num_pages] (device), changed. At first: all 0. 0 or
  *                less is free. num_pages * page_size is at most 2^31 - 1.
  *   parents, prefix_lens  int32 [B] (device) or NULL: request b takes the
- *                pages of its parent's first prefix_lens[b] tokens (whole
- *                pages; a length of 0 or less: none) where it holds none
- *                itself, as the parent's row was before the call. Negative:
- *                no parent. A parent has none itself (SV_FLAG_BAD_PARENT).
- *                Tokens in shared pages are not to be written again.
+ *                pages of its parent's first prefix_lens[b] tokens (a length
+ *                of 0 or less: none) where it holds none itself, as the
+ *                parent's row was before the call; only whole pages, and only
+ *                in front of ctx_lens[b], so that its own slots lie in pages of
+ *                its own. Tokens behind the last whole page are the request's
+ *                to write: one that starts behind a prefix starts at a multiple
+ *                of page_size (a prompt matched in full runs its last page
+ *                again). Negative: no parent. A parent has none itself
+ *                (SV_FLAG_BAD_PARENT) and has written the prefix before: its
+ *                own length is not below prefix_lens[b], and lengths do not go
+ *                back into shared pages.
  *   T            the block's width, 1..SV_MAX_CONTEXT; B 0..SV_MAX_BATCH.
  *   out_starts   int32 [B] (device): ctx_lens[b] where the request's pages are
  *                all there, else -1 (an empty slot, no pages, or a block that

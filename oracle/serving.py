@@ -52,7 +52,8 @@ def plan(table, refs, ctx, budgets, T, page, window=0, sinks=0, parents=None, pr
         if parent >= 0 and (parent >= B or parent == b or parents[parent] >= 0):
             flags |= BAD_PARENT
             parent = -1
-        common = max(int(prefix[b]), 0) // page if parent >= 0 else 0
+        # Whole pages in front of the request's new tokens.
+        common = min(max(int(prefix[b]), 0), max(c, 0)) // page if parent >= 0 else 0
         new[b] = []
         for i in range(width):
             held = int(before[b, i])
