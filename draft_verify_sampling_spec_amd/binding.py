@@ -40,6 +40,7 @@ SV_FLAG_BAD_LENGTH = 0x8
 SV_FLAG_BAD_PAGE = 0x10
 SV_FLAG_NO_PAGES = 0x20
 SV_FLAG_BAD_PARENT = 0x40
+SV_FLAG_NO_PREFIX = 0x80
 
 SV_MAX_BATCH = 16384
 SV_MAX_K = 32
@@ -1135,7 +1136,9 @@ class PageTables:
         """One step: gives back the pages that a request no longer needs for
         positions 0 .. ctx_lens[b] + budgets[b] (budgets None: length - 1; under a
         ``window`` the first ``sinks`` positions and those of the window), takes
-        what is missing from the parent's row or from the free pages. Returns
+        what is missing from the parent's row (whole pages of prefix_lens[b]
+        tokens and in front of ctx_lens[b]; SV_FLAG_NO_PREFIX in ``status`` if that
+        lacks one) or from the free pages. Returns
         (starts int32 [B]: ctx_lens, -1 where the request cannot run; slots int32
         [B, length] and positions int32 [B, length] of its tokens, -1 behind its
         budget)."""

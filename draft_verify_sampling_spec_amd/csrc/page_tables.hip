@@ -7,7 +7,8 @@
 // does not need is given back (one reference less); a needed page that the row
 // does not hold is taken from the same place of its parent's row (a shared
 // prefix, one reference more; only pages in front of the row's new tokens, whose
-// slots so never lie in another row's page) or is new: new pages are the lowest-numbered
+// slots so never lie in another row's page; flagged if the parent lacks one) or
+// is new: new pages are the lowest-numbered
 // free ones (no references), dealt out in the order of requests and, within
 // one, of positions. A request whose new pages, with those of all requests
 // before it, are more than there are free gets none. Everything is whole
@@ -125,8 +126,12 @@ __device__ __forceinline__ Entry classify(const PlanArgs& a, const Row& r, int32
     if (has && !need) atomicSub(a.refs + page, 1);
     if (!need) return Entry{-1, false};
     if (has) return Entry{page, false};
-    const int shared = i < common ? parent[i] : -1;
-    if (!in_pool(a, shared)) return Entry{-1, true};
+    if (i >= common) return Entry{-1, true};
+    const int shared = parent[i];
+    if (!in_pool(a, shared)) {
+        flag(a.status, SV_FLAG_NO_PREFIX);
+        return Entry{-1, true};
+    }
     atomicAdd(a.refs + shared, 1);
     row[i] = shared;
     return Entry{shared, false};

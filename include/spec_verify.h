@@ -96,6 +96,9 @@ enum sv_status {
 #define SV_FLAG_NO_PAGES 0x20u  /* too few free pages: some request got none */
 #define SV_FLAG_BAD_PARENT 0x40u /* a parent outside the batch, or one that has a
                                    parent itself; treated as none */
+#define SV_FLAG_NO_PREFIX 0x80u /* a page of a prefix was not in the parent's row;
+                                   a new one, which holds nothing of it, took its
+                                   place */
 
 /* Library limits. */
 #define SV_MAX_BATCH 16384
@@ -555,7 +558,12 @@ int spec_verify_cache_write(const void* keys, const void* values, int dtype, int
  *                again). Negative: no parent. A parent has none itself
  *                (SV_FLAG_BAD_PARENT) and has written the prefix before: its
  *                own length is not below prefix_lens[b], and lengths do not go
- *                back into shared pages.
+ *                back into shared pages. Where its row lacks a page that would
+ *                have been taken (it was given back behind a window, refused,
+ *                or the parent never held it), the request gets a new page and
+ *                SV_FLAG_NO_PREFIX: it runs, but what that page holds in front
+ *                of ctx_lens[b] is for the caller to write before any attention
+ *                reads it.
  *   T            the block's width, 1..SV_MAX_CONTEXT; B 0..SV_MAX_BATCH.
  *   out_starts   int32 [B] (device): ctx_lens[b] where the request's pages are
  *                all there, else -1 (an empty slot, no pages, or a block that

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import numpy as np
 
-BAD_BUDGET, BAD_LENGTH, BAD_PAGE, NO_PAGES, BAD_PARENT = 0x1, 0x8, 0x10, 0x20, 0x40
+BAD_BUDGET, BAD_LENGTH, BAD_PAGE, NO_PAGES, BAD_PARENT, NO_PREFIX = 0x1, 0x8, 0x10, 0x20, 0x40, 0x80
 
 
 def visible(p: int, window: int = 0, sinks: int = 0):
@@ -71,6 +71,8 @@ def plan(table, refs, ctx, budgets, T, page, window=0, sinks=0, parents=None, pr
                     table[b, i] = other
                 else:
                     new[b].append(i)
+                    if i < common:
+                        flags |= NO_PREFIX
     free = [p for p in range(len(refs)) if refs[p] <= 0]
     starts, slots, positions = np.full(B, -1), np.full((B, T), -1), np.full((B, T), -1)
     used = 0
