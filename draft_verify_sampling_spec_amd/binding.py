@@ -1098,7 +1098,8 @@ class PageTables:
     max_pages], -1 where there is none) and ``refs`` (int32 [num_pages], how many
     entries hold each page), both on the device and changed by ``plan`` only.
     One object serves the caches of all layers, whose pools it numbers alike.
-    ``table`` and ``refs`` may be given to go on from a state of their own.
+    ``table`` and ``refs`` may be given to go on from a state of their own; a
+    table alone has its pages counted (which waits for the device).
 
     Calls are enqueued on ``stream`` (default: the current torch stream) and not
     waited for; ``status`` as in ``BlockCache``."""
@@ -1124,6 +1125,9 @@ class PageTables:
         self.refs = torch.zeros(self.num_pages, dtype=torch.int32, device=device) \
             if refs is None else refs
         self._state()
+        if table is not None and refs is None:
+            held = table[(table >= 0) & (table < self.num_pages)]
+            self.refs.copy_(torch.bincount(held, minlength=self.num_pages))
         # For small tables, whose plan leaves its 256 bytes alone.
         self._unused = torch.empty(256, dtype=torch.uint8, device=device)
 
