@@ -793,6 +793,14 @@ def _other_stream(stream, index):
     return torch.cuda.stream(stream)
 
 
+def _ready(index):
+    """Waits for what a constructor enqueued, so that calls on any stream find it
+    done (not in a capture, which cannot wait and replays it in order)."""
+    with torch.cuda.device(index):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+
+
 def _token_stride(t, name, index):
     """Elements between tokens of a [B, T, heads, head_dim] tensor whose heads
     are contiguous and whose requests follow each other."""
@@ -813,10 +821,10 @@ def _token_stride(t, name, index):
 class BlockCache:
     """A target layer's paged 4-bit key/value cache on one device: writing
     blocks (or prompts), reading tokens back, and the attention of drafted
-    blocks over it. Holds the pool (torch-allocated unless given: uint8
-    [num_pages, kv_heads, page_size / 32, 34 head_dim]; ``pool`` may be replaced
-    by another of that shape between calls); the page table and the lengths are
-    the caller's.
+    blocks over it. Holds the pool (torch-allocated, and ready on every stream,
+    unless given: uint8 [num_pages, kv_heads, page_size / 32, 34 head_dim];
+    ``pool`` may be replaced by another of that shape between calls); the page
+    table and the lengths are the caller's.
 
     ``status`` (int32 [1] on the device, or None) collects SV_FLAG_* bits;
     nothing clears it. Calls are enqueued on ``stream`` (default: the current
@@ -840,6 +848,8 @@ class BlockCache:
         self._pool_ptr()
         # For calls whose plan has no parts, which leave their 256 bytes alone.
         self._no_parts = torch.empty(256, dtype=torch.uint8, device=device)
+        if pool is None:
+            _ready(self._index)
 
     def _pool_shape(self):
         return self.num_pages, self.kv_heads, self.page_size // 32, 34 * self.head_dim
@@ -1099,7 +1109,7 @@ class PageTables:
     entries hold each page), both on the device and changed by ``plan`` only.
     One object serves the caches of all layers, whose pools it numbers alike.
     ``table`` and ``refs`` may be given to go on from a state of their own; a
-    table alone has its pages counted (which waits for the device).
+    table alone has its pages counted. What is made here is ready on every stream.
 
     Calls are enqueued on ``stream`` (default: the current torch stream) and not
     waited for; ``status`` as in ``BlockCache``."""
@@ -1130,6 +1140,8 @@ class PageTables:
             self.refs.copy_(torch.bincount(held, minlength=self.num_pages))
         # For small tables, whose plan leaves its 256 bytes alone.
         self._unused = torch.empty(256, dtype=torch.uint8, device=device)
+        if table is None or refs is None:
+            _ready(self._index)
 
     def _state(self):
         return (_need(self.table, "table", torch.int32, (self.B, self.max_pages), self._index),
