@@ -30,7 +30,7 @@
 // TB/s, the join's 13 in it, and 197 with 9 rows each; single tokens over the same
 // contexts 129; one block of 5 over 131,071 tokens 41; 64 blocks under a window of
 // 1,024 (8 kv heads of 256) 33. 64 blocks over 2,000..4,000 tokens, 8 kv heads:
-// 64 rows of 128 channels 101 us, 2.0 TB/s (that kernel spills 66 registers, six
+// 64 rows of 128 channels 101 us, 2.0 TB/s (that kernel spills 67 registers, six
 // reloads in its loop over pairs of tiles), 48 rows of 64 channels 50, 2.1 TB/s.
 #pragma once
 

@@ -33,7 +33,14 @@
 // two workgroups a CU before the priorities set below (4 us in all); its products alone
 // take 0.25, the rest is decoding (0.1) and the softmax, which a wavefront takes one
 // after another with its products and two wavefronts a SIMD hide from each other only
-// in part. Starting and ending a part takes 6 us.
+// in part. Starting and ending a part takes 6 us. For 48 and 64 rows of 128
+// channels of a request's own tokens (the heavy batch's 9 rows x 4 heads are of the
+// former) the work kernel spills 19 and 47 registers, outside of the loops over
+// tiles but for six reloads in the loop over pairs of own tiles of 64 rows.
+// Against the attention that shares nothing (32 query and 8 kv heads of 128): the
+// heavy batch 134 us and 199, with all 9 rows 214 and 261; 8 blocks of up to 6 rows
+// behind 2,000 tokens 25 and 21: three launches pay from about 64 requests behind
+// 2,000 tokens or 32 blocks behind 8,000 on.
 #include <algorithm>
 #include <climits>
 
@@ -157,7 +164,10 @@ __global__ __launch_bounds__(64 * kPlanWaves) void shared_plan_kernel(SharedArgs
     }
     __syncthreads();
     if (wave == 0) {
-        // The length of a part: all units' tiles over the workgroups that run at once.
+        // The length of a part: all units' tiles over the workgroups that run at once,
+        // rounded for each group, so that a part may be up to 1.5 times as long, or the
+        // items a few more than the workgroups, some of which then take two (128 blocks
+        // of 9 rows x 4 heads: 576 items on 512).
         const int heads = a.pages.heads, each = (s.G + 63) / 64, g0 = lane * each, g1 = min(g0 + each, s.G);
         unsigned long long work = 0, units = 0;
         for (int i = g0; i < g1; ++i) work += (unsigned long long)found[i].blocks * heads * found[i].tiles;
